@@ -349,6 +349,59 @@ pa_status_t pa_v2_forward_noalloc(void *out, const void *query,
                                   int max_seq_len, float scale,
                                   int partition_size, int dtype, void *stream);
 
+/* Append new keys and values to the paged cache, rotating keys (and queries)
+ * by their positions on the way, and keeping the pages' key bounds.
+ *
+ * The rows are the tokens that the sequences gain: with q_start (device int32
+ * [num_seqs + 1], as for pa_chunks_forward) row r of sequence s is token
+ * t = seq_lens[s] - n_s + (r - q_start[s]), n_s = q_start[s+1] - q_start[s];
+ * with q_start NULL there is one row a sequence (num_rows = num_seqs), its
+ * last token, and a sequence of length 0 is an empty slot, skipped.  seq_lens
+ * are the lengths AFTER the append.  Rows from q_start[num_seqs] on are
+ * padding: nothing of theirs is read, and their query_out is left as it was.
+ *
+ *   key, value         [num_rows][num_kv_heads][head_size]; rows key_stride /
+ *                      value_stride elements apart (16-byte multiples), so
+ *                      they may be slices of one projection's output
+ *   query, query_out   [num_rows][num_heads][head_size], rows of query
+ *                      query_stride apart, query_out contiguous; both NULL
+ *                      when there are no queries to rotate; may be the same
+ *                      contiguous buffer
+ *   cos_sin            f32 [max_position][rotary_dim]: rotary_dim / 2 cosines,
+ *                      then the sines; NULL if rotary_dim is 0
+ *   positions          int32 [num_rows], or NULL for t (a sequence behind a
+ *                      shared prefix starts at the prefix's length)
+ *   key_bounds         [num_blocks][num_kv_heads][2][head_size] in dtype, or
+ *                      NULL: per page and channel the largest ([0]) and the
+ *                      smallest ([1]) key stored, as pa_select_blocks reads it
+ *
+ * The first rotary_dim elements of a head (a multiple of 16, at most
+ * head_size) turn in pairs, in fp32 with one rounding to dtype:
+ * y1 = x1 cos - x2 sin, y2 = x2 cos + x1 sin, the pairs being (j, j +
+ * rotary_dim / 2) with interleaved = 0, (2j, 2j + 1) with 1; the rest and the
+ * values are copied.  A page's bounds start anew with its first token and
+ * otherwise only widen: tokens overwritten later (rejected drafts) leave
+ * theirs in, so the bounds then still hold but are wider than need be.  NaN
+ * keys are passed over.
+ *
+ * dtype as the caches; f32, bf16 and f16.  No two sequences may append to the
+ * same page.  The workspace needs only its 256-byte status block (any
+ * workspace of this library serves); bad tables, lengths, chunks or positions
+ * are reported there as PA_ERR_DEVICE_BAD_INPUT, and nothing of the rows in
+ * question is written. */
+pa_status_t pa_append_kv(void *key_cache, void *value_cache, void *key_bounds,
+                         void *query_out, const void *query, const void *key,
+                         const void *value, long long query_stride,
+                         long long key_stride, long long value_stride,
+                         const float *cos_sin, const int32_t *positions,
+                         const int32_t *block_tables, const int32_t *seq_lens,
+                         const int32_t *q_start, int num_seqs, int num_rows,
+                         int num_heads, int num_kv_heads, int head_size,
+                         int num_blocks, int block_size, int max_blocks_per_seq,
+                         int max_seq_len, int rotary_dim, int interleaved,
+                         int max_position, int dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 /* Host heuristic: 1 if V2 should serve this batch on a GPU with sm_count
  * SMs, 0 for V1.  The pages switch on sequence length alone: the commit note
  * for computility-run.yaml (project_6, commit a2a5dd8) lists the decode path

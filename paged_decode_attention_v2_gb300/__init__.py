@@ -45,7 +45,7 @@ EXPORTS = ("pa_workspace_bytes", "pa_workspace_layout", "pa_workspace_init",
            "pa_v1_forward", "pa_v2_forward", "pa_forward", "pa_choose_v2", "pa_choose_v2_chunks",
            "pa_read_device_status", "pa_status_string", "pa_last_cuda_error",
            "pa_version", "pa_v2_forward_noalloc", "pa_host_staging_bytes", "pa_forward_host",
-           "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine")
+           "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine", "pa_append_kv")
 
 
 class PAError(RuntimeError):
@@ -109,6 +109,9 @@ def load_library(path: str = LIB_PATH):
         lib.pa_forward_host.restype = ci
         lib.pa_forward_host.argtypes = (_FWD_ARGS[:17] + [vp, cs] + _FWD_ARGS[17:] +
                                         [ctypes.POINTER(pa_options_t)])
+        ll = ctypes.c_longlong
+        lib.pa_append_kv.restype = ci
+        lib.pa_append_kv.argtypes = [vp] * 7 + [ll] * 3 + [vp] * 5 + [ci] * 13 + [vp, cs, vp]
         lib.pa_choose_v2.restype = ci
         lib.pa_choose_v2.argtypes = [ci] * 5
         lib.pa_choose_v2_chunks.restype = ci
@@ -305,6 +308,91 @@ def pa_chunks_forward(out, query, key_cache, value_cache, block_tables, seq_lens
         int(max_seq_len), float(scale), int(partition_size), _DTYPES[query.dtype],
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream),
         ctypes.byref(opts)), "pa_chunks_forward")
+
+
+def _check_call(dtype, device, same, ints) -> None:
+    """Every tensor on the current CUDA device, `same` of one dtype, `ints` int32
+    (None entries are absent arguments)."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}: libpa runs on the current CUDA device")
+    for t in same:
+        if t is not None and (t.dtype != dtype or t.device != device):
+            raise ValueError("libpa takes caches, queries and outputs of one dtype on one device")
+    for t in ints:
+        if t is not None and (t.dtype != torch.int32 or t.device != device):
+            raise ValueError("libpa takes int32 tables, lengths and starts on the caches' device")
+
+
+def _rows(t, heads: int, head_size: int):
+    """(pointer, elements between rows) of a [rows, heads, head_size] tensor whose
+    rows are contiguous."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size:
+        raise ValueError(f"expected [rows, {heads}, {head_size}], got {list(t.shape)}")
+    if t.is_contiguous() or t.shape[0] < 2:
+        if not t[:1].is_contiguous():
+            raise ValueError("libpa takes rows of contiguous heads")
+        return t.data_ptr(), heads * head_size
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_size):
+        raise ValueError("libpa takes rows of contiguous heads")
+    return t.data_ptr(), t.stride(0)
+
+
+def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, workspace,
+                 query=None, query_out=None, key_bounds=None, cos_sin=None, positions=None,
+                 q_start=None, rotary_dim=None, interleaved=False, max_seq_len=None,
+                 stream=None) -> None:
+    """Append key / value [rows, Hkv, D] (rows may be strided slices) to the
+    paged cache, keys rotated by cos_sin [max_position, rotary_dim] on the way
+    and query [rows, H, D] rotated into query_out; key_bounds [num_blocks, Hkv,
+    2, D] follows the keys (see include/pa.h).  seq_lens are the lengths after
+    the append.  rotary_dim defaults to cos_sin's width."""
+    nb, hkv, bs, D = key_cache.shape
+    _check_call(key_cache.dtype, key_cache.device,
+                (value_cache, key, value, query, query_out, key_bounds),
+                (block_tables, seq_lens, q_start, positions))
+    R = key.shape[0]
+    B = seq_lens.numel()
+    if value_cache.shape != key_cache.shape or value.shape[0] != R:
+        raise ValueError("key and value (and their caches) differ in shape")
+    if q_start is not None and q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [num_seqs + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    if positions is not None and positions.numel() != R:
+        raise ValueError("positions must be int32 [rows]")
+    if key_bounds is not None and key_bounds.shape != (nb, hkv, 2, D):
+        raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
+    H, qp, qst, qop = hkv, 0, 0, 0
+    if query is not None:
+        if query_out is None or query_out.shape != query.shape or query.shape[0] != R:
+            raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
+        H = query.shape[1]
+        qp, qst = _rows(query, H, D)
+        qop = _ptr(query_out)
+    elif query_out is not None:
+        raise ValueError("query_out without a query")
+    max_position = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.device != key_cache.device \
+                or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+        max_position, width = cos_sin.shape
+        if rotary_dim is None:
+            rotary_dim = width
+        if rotary_dim not in (0, width):
+            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+    if max_seq_len is None:
+        max_seq_len = block_tables.shape[1] * bs
+    kp, kst = _rows(key, hkv, D)
+    vp, vst = _rows(value, hkv, D)
+    _check(load_library().pa_append_kv(
+        _ptr(key_cache), _ptr(value_cache), _ptr(key_bounds), qop, qp, kp, vp, qst, kst, vst,
+        _ptr(cos_sin), _ptr(positions), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R,
+        H, hkv, D, nb, bs, block_tables.shape[1], int(max_seq_len), int(rotary_dim or 0),
+        int(interleaved), max_position, _DTYPES[key_cache.dtype], _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
 
 
 def pa_host_staging_bytes(num_seqs: int, num_heads: int, head_size: int,

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "pa.h"
+#include "pa_host.h"
 #include "pa_internal.h"
 
 namespace {
@@ -905,6 +906,57 @@ pa_status_t stage_in(const void *s0, void *d0, size_t b0, const void *s1, void *
 }
 
 }  // namespace
+
+namespace pa {
+
+pa_status_t host_fail_cuda(const char *what, cudaError_t e) { return fail_cuda(what, e); }
+
+pa_status_t host_sm_count(int *sms) {
+  DeviceFacts *dev = nullptr;
+  pa_status_t st = device_facts(&dev);
+  if (st == PA_OK) *sms = dev->sm_count;
+  return st;
+}
+
+pa_status_t host_ensure_smem(const void *fn, size_t bytes) { return ensure_smem(fn, bytes); }
+
+pa_status_t host_check_cache(int dtype, int num_heads, int num_kv_heads, int head_size,
+                             int num_blocks, int block_size, int max_blocks_per_seq,
+                             int max_seq_len) {
+  if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16)
+    return PA_ERR_INVALID_ARG;
+  if (num_heads < 1 || num_kv_heads < 1 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      max_seq_len < 0 || block_size < 1 || num_heads % num_kv_heads)
+    return PA_ERR_INVALID_ARG;
+  if ((long long)max_seq_len > (long long)max_blocks_per_seq * block_size)
+    return PA_ERR_INVALID_ARG;
+  if (head_size != 64 && head_size != 128 && head_size != 256) return PA_ERR_UNSUPPORTED;
+  if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64)
+    return PA_ERR_UNSUPPORTED;
+  if (num_heads / num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+  if ((long long)num_blocks * num_kv_heads * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+pa_status_t host_launch(const void *fn, unsigned grid_x, unsigned grid_y, int threads, size_t smem,
+                        void *stream, void **args, const char *what) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(grid_x, grid_y, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e != cudaSuccess) return fail_cuda(what, e);
+  return PA_OK;
+}
+
+}  // namespace pa
 
 extern "C" {
 
