@@ -402,6 +402,77 @@ pa_status_t pa_append_kv(void *key_cache, void *value_cache, void *key_bounds,
                          int max_position, int dtype, void *workspace,
                          size_t workspace_bytes, void *stream);
 
+/* Decode attention over the blocks that a cheap score selects.
+ *
+ * For a query row and a KV head, with the pages' key bounds (pa_append_kv),
+ * page j scores the sum over the group's heads of the largest q . k that its
+ * bounds allow:
+ *   score_j = sum_h sum_d max(q_hd max_jd, q_hd min_jd)
+ *           = sum_d Q+_d max_jd + Q-_d min_jd,
+ * Q+_d and Q-_d the sums of the heads' positive and negative q_hd (the second
+ * form counts where a bound is infinite).  Of the pages that hold keys the
+ * row sees, the first sink_blocks and the last recent_blocks are selected
+ * always, the others by their score, ties to the lower page, num_selected in
+ * all; every page if there are no more than that.
+ * The selection is the one that exact scores give (nearly equal ones are
+ * computed again in fp64); a NaN score ranks lowest.
+ *
+ * Rows: one a sequence (q_start NULL, num_rows = num_seqs, the row sees the
+ * sequence's seq_lens keys), or chunks as in pa_chunks_forward (row i of a
+ * chunk of n sees seq_lens - n + i + 1 keys; every row selects for itself).
+ * Rows behind the last chunk, and rows of empty sequences, select nothing.
+ *
+ *   key_bounds  [num_blocks][num_kv_heads][2][head_size] (dtype), 16-byte
+ *               aligned: largest, then smallest key a channel
+ *   selected    int32 [num_rows][num_kv_heads][num_selected]: page numbers of
+ *               the sequence, ascending, -1 behind the last
+ * 0 <= sink_blocks, 1 <= recent_blocks, sink_blocks + recent_blocks <=
+ * num_selected.  query, block_tables, seq_lens and the limits on sizes as in
+ * pa_forward, f32 included; query contiguous [num_rows][num_heads][head_size].
+ * The workspace holds pa_sparse_workspace_bytes(...) bytes, zeroed once by
+ * pa_workspace_init; partition_size is the one it was sized with.  A bad table
+ * entry, length or chunk is reported as PA_ERR_DEVICE_BAD_INPUT: a page with a
+ * bad entry scores lowest, a row with a bad length selects nothing. */
+pa_status_t pa_select_blocks(int32_t *selected, const void *query,
+                             const void *key_bounds,
+                             const int32_t *block_tables,
+                             const int32_t *seq_lens, const int32_t *q_start,
+                             int num_seqs, int num_rows, int num_heads,
+                             int num_kv_heads, int head_size, int num_blocks,
+                             int block_size, int max_blocks_per_seq,
+                             int max_seq_len, int num_selected,
+                             int sink_blocks, int recent_blocks,
+                             int partition_size, int dtype, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Attention over selected blocks: out[r][h] = softmax over the keys that row
+ * r sees in the blocks selected for (r, h's KV head), in the V1/V2 kernels.
+ * With key_bounds, the blocks are selected as by pa_select_blocks in the same
+ * call, and written to `selected` unless that is NULL.  With key_bounds NULL,
+ * `selected` is read: any choice of the row's pages, ascending, -1 behind the
+ * last (another order, or a page that the row does not see, is reported as
+ * PA_ERR_DEVICE_BAD_INPUT, and the row's head group gets zeros); sink_blocks
+ * and recent_blocks must still be valid but are not used.  Nothing selected:
+ * zeros.  Other arguments as pa_select_blocks and pa_forward. */
+pa_status_t pa_sparse_forward(void *out, int32_t *selected, const void *query,
+                              const void *key_cache, const void *value_cache,
+                              const void *key_bounds,
+                              const int32_t *block_tables,
+                              const int32_t *seq_lens, const int32_t *q_start,
+                              int num_seqs, int num_rows, int num_heads,
+                              int num_kv_heads, int head_size, int num_blocks,
+                              int block_size, int max_blocks_per_seq,
+                              int max_seq_len, int num_selected,
+                              int sink_blocks, int recent_blocks, float scale,
+                              int partition_size, int dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for the two calls above (0 on bad arguments). */
+size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
+                                 int head_size, int block_size,
+                                 int max_seq_len, int num_selected,
+                                 int partition_size);
+
 /* Host heuristic: 1 if V2 should serve this batch on a GPU with sm_count
  * SMs, 0 for V1.  The pages switch on sequence length alone: the commit note
  * for computility-run.yaml (project_6, commit a2a5dd8) lists the decode path

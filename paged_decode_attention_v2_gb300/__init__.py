@@ -45,7 +45,8 @@ EXPORTS = ("pa_workspace_bytes", "pa_workspace_layout", "pa_workspace_init",
            "pa_v1_forward", "pa_v2_forward", "pa_forward", "pa_choose_v2", "pa_choose_v2_chunks",
            "pa_read_device_status", "pa_status_string", "pa_last_cuda_error",
            "pa_version", "pa_v2_forward_noalloc", "pa_host_staging_bytes", "pa_forward_host",
-           "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine", "pa_append_kv")
+           "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine", "pa_append_kv",
+           "pa_select_blocks", "pa_sparse_forward", "pa_sparse_workspace_bytes")
 
 
 class PAError(RuntimeError):
@@ -112,6 +113,13 @@ def load_library(path: str = LIB_PATH):
         ll = ctypes.c_longlong
         lib.pa_append_kv.restype = ci
         lib.pa_append_kv.argtypes = [vp] * 7 + [ll] * 3 + [vp] * 5 + [ci] * 13 + [vp, cs, vp]
+        lib.pa_sparse_workspace_bytes.restype = cs
+        lib.pa_sparse_workspace_bytes.argtypes = [ci] * 8
+        lib.pa_select_blocks.restype = ci
+        lib.pa_select_blocks.argtypes = [vp] * 6 + [ci] * 14 + [vp, cs, vp]
+        lib.pa_sparse_forward.restype = ci
+        lib.pa_sparse_forward.argtypes = ([vp] * 9 + [ci] * 12 + [ctypes.c_float, ci, ci, vp, cs,
+                                                                  vp])
         lib.pa_choose_v2.restype = ci
         lib.pa_choose_v2.argtypes = [ci] * 5
         lib.pa_choose_v2_chunks.restype = ci
@@ -393,6 +401,91 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
         H, hkv, D, nb, bs, block_tables.shape[1], int(max_seq_len), int(rotary_dim or 0),
         int(interleaved), max_position, _DTYPES[key_cache.dtype], _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
+
+
+def pa_sparse_workspace_bytes(num_rows: int, num_heads: int, num_kv_heads: int, head_size: int,
+                              block_size: int, max_seq_len: int, num_selected: int,
+                              partition_size: int) -> int:
+    return int(load_library().pa_sparse_workspace_bytes(
+        num_rows, num_heads, num_kv_heads, head_size, block_size, max_seq_len, num_selected,
+        partition_size))
+
+
+def alloc_sparse_workspace(num_rows: int, num_heads: int, num_kv_heads: int, head_size: int,
+                           block_size: int, max_seq_len: int, num_selected: int,
+                           partition_size: int, device=None, stream=None) -> torch.Tensor:
+    """A zeroed workspace for pa_select_blocks and pa_sparse_forward."""
+    n = pa_sparse_workspace_bytes(num_rows, num_heads, num_kv_heads, head_size, block_size,
+                                  max_seq_len, num_selected, partition_size)
+    if n == 0:
+        raise ValueError("bad sizes for a sparse workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    pa_workspace_init(ws, stream)
+    return ws
+
+
+def _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv):
+    R, H, D = query.shape
+    B = seq_lens.numel()
+    if q_start is not None and q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [num_seqs + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    if selected is not None and (selected.dim() != 3 or selected.shape[0] != R
+                                 or selected.shape[1] != hkv):
+        raise ValueError("selected must be int32 [rows, num_kv_heads, num_selected]")
+    if key_bounds is not None and (key_bounds.dim() != 4 or key_bounds.shape[1] != hkv
+                                   or key_bounds.shape[2] != 2 or key_bounds.shape[3] != D):
+        raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
+    return R, H, D, B
+
+
+def pa_select_blocks(selected, query, key_bounds, block_tables, seq_lens, block_size: int,
+                     partition_size, workspace, sink_blocks=0, recent_blocks=1, q_start=None,
+                     max_seq_len=None, stream=None) -> None:
+    """Choose the blocks that each (row, KV head) attends to from the pages' key
+    bounds into selected, int32 [rows, Hkv, num_selected] (see include/pa.h)."""
+    nb, hkv = key_bounds.shape[:2]
+    _check_call(query.dtype, query.device, (key_bounds,), (selected, block_tables, seq_lens, q_start))
+    R, H, D, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
+    if max_seq_len is None:
+        max_seq_len = block_tables.shape[1] * block_size
+    _check(load_library().pa_select_blocks(
+        _ptr(selected), _ptr(query), _ptr(key_bounds), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(q_start), B, R, H, hkv, D, nb, block_size, block_tables.shape[1], int(max_seq_len),
+        selected.shape[2], sink_blocks, recent_blocks, int(partition_size), _DTYPES[query.dtype],
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream)),
+        "pa_select_blocks")
+
+
+def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables, seq_lens, scale,
+                      partition_size, workspace, key_bounds=None, num_selected=None,
+                      sink_blocks=0, recent_blocks=1, q_start=None, max_seq_len=None,
+                      stream=None) -> None:
+    """Attention over selected blocks (see include/pa.h): with key_bounds they
+    are selected in the call and written to `selected` (None: not wanted, give
+    num_selected); without, `selected` is read."""
+    nb, hkv, bs, D = key_cache.shape
+    _check_call(query.dtype, query.device, (out, key_cache, value_cache, key_bounds),
+                (selected, block_tables, seq_lens, q_start))
+    R, H, D2, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
+    if out.shape != query.shape or D2 != D or value_cache.shape != key_cache.shape \
+            or (key_bounds is not None and key_bounds.shape[0] != nb):
+        raise ValueError("query and out, or the caches and their bounds, differ in shape")
+    if selected is not None:
+        if num_selected not in (None, selected.shape[2]):
+            raise ValueError("num_selected differs from selected's last dimension")
+        num_selected = selected.shape[2]
+    elif num_selected is None:
+        raise ValueError("num_selected or a selected tensor is needed")
+    if max_seq_len is None:
+        max_seq_len = block_tables.shape[1] * bs
+    _check(load_library().pa_sparse_forward(
+        _ptr(out), _ptr(selected), _ptr(query), _ptr(key_cache), _ptr(value_cache),
+        _ptr(key_bounds), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R, H, hkv, D, nb,
+        bs, block_tables.shape[1], int(max_seq_len), int(num_selected), sink_blocks, recent_blocks,
+        float(scale), int(partition_size), _DTYPES[query.dtype], _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_sparse_forward")
 
 
 def pa_host_staging_bytes(num_seqs: int, num_heads: int, head_size: int,

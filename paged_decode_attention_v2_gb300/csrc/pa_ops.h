@@ -25,4 +25,31 @@ struct AppendParams {
   int tile_rows;  // rows of a CTA
 };
 
+// The block of the view in which every (row, KV head) is a sequence of one KV
+// head: cache [num_blocks * Hkv][1][bs][D].  A bad entry stays out of range,
+// for the attention kernels to report.
+__host__ __device__ __forceinline__ int view_block(int blk, int kv_head, int num_kv_heads,
+                                                   int num_blocks) {
+  return (unsigned)blk < (unsigned)num_blocks ? blk * num_kv_heads + kv_head : -1;
+}
+
+struct SelectParams {
+  const void *query;       // [rows][H][D]
+  const void *key_bounds;  // [num_blocks][Hkv][2][D]
+  const int32_t *block_tables, *seq_lens, *q_start;
+  int32_t *selected;       // [rows][Hkv][num_selected] or null
+  const int32_t *given;    // a given selection instead
+  int32_t *table, *lens;   // the view's block table and lengths, or null
+  int *counters;           // [rows * Hkv] finished chunks, zero between calls
+  float *amax;             // [rows * Hkv][chunks] largest bound seen
+  float *scores;           // [rows * Hkv][max_pages]
+  double *fine;            // [rows * Hkv][max_pages]
+  int *status;
+  int num_seqs, num_rows, num_heads, num_kv_heads, num_blocks;
+  int block_size, log2_block_size, max_blocks_per_seq, max_seq_len, max_pages;
+  int num_selected, sinks, recent;
+  int chunks, chunk_pages;  // CTAs of an item, pages of each
+  int smem_pages;           // scores that the shared memory holds
+};
+
 }  // namespace pa
