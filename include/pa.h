@@ -473,6 +473,56 @@ size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
                                  int max_seq_len, int num_selected,
                                  int partition_size);
 
+/* Decode attention for sequences that share prefixes (a system prompt, a
+ * document, the prompt of several samples): sequence s attends to the
+ * prefix_lens[g] tokens of its group's prefix and to its own seq_lens[s]
+ * tokens,
+ *   out[s][h] = softmax over both of (scale q[s][h] . K) @ V.
+ * The prefix's keys and values are read once for all the rows (sequence, head)
+ * of a group, as a matrix product on the tensor cores; the own tokens run as
+ * in pa_v2_forward, and Phase 2 merges the partitions of both.  Keys carry
+ * their positions' rotation already, so the own tokens are appended with the
+ * prefix's length added to their positions (pa_append_kv).
+ *
+ *   prefix_tables  int32 [num_prefixes][max_prefix_blocks]: the prefixes'
+ *                  pages, in the same caches
+ *   prefix_lens    int32 [num_prefixes], each in [0, max_prefix_len], of any
+ *                  length (the last page may be partly filled)
+ *   prefix_start   int32 [num_prefixes + 1], non-decreasing, from 0 to
+ *                  num_seqs: sequences prefix_start[g] .. prefix_start[g+1]-1
+ *                  are group g; a group may be empty
+ * block_tables and seq_lens hold the own tokens only, with max_seq_len their
+ * bound (0 if no sequence has any).  Sequences with no tokens at all get
+ * zeros.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); the other arguments and
+ * limits as pa_v2_forward.  The workspace holds pa_prefix_workspace_bytes(...)
+ * bytes, zeroed once by pa_workspace_init.  Bad tables, lengths or groups are
+ * reported as PA_ERR_DEVICE_BAD_INPUT; the rows in question then hold no
+ * meaningful values.  opts as in pa_forward (variant V2 or auto; no fused
+ * combine, no CUDA-core path). */
+pa_status_t pa_prefix_forward(void *out, const void *query,
+                              const void *key_cache, const void *value_cache,
+                              const int32_t *block_tables,
+                              const int32_t *seq_lens,
+                              const int32_t *prefix_tables,
+                              const int32_t *prefix_lens,
+                              const int32_t *prefix_start, int num_seqs,
+                              int num_prefixes, int num_heads,
+                              int num_kv_heads, int head_size, int num_blocks,
+                              int block_size, int max_blocks_per_seq,
+                              int max_prefix_blocks, int max_seq_len,
+                              int max_prefix_len, float scale,
+                              int partition_size, int dtype, void *workspace,
+                              size_t workspace_bytes, void *stream,
+                              const pa_options_t *opts);
+
+/* Bytes of workspace for pa_prefix_forward (0 on bad arguments): as
+ * pa_workspace_bytes with slots for the prefix's splits, which the library
+ * chooses from these sizes, behind every row's own partitions. */
+size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads,
+                                 int num_kv_heads, int head_size,
+                                 int max_seq_len, int max_prefix_len,
+                                 int partition_size);
+
 /* Host heuristic: 1 if V2 should serve this batch on a GPU with sm_count
  * SMs, 0 for V1.  The pages switch on sequence length alone: the commit note
  * for computility-run.yaml (project_6, commit a2a5dd8) lists the decode path

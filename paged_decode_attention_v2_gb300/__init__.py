@@ -46,7 +46,8 @@ EXPORTS = ("pa_workspace_bytes", "pa_workspace_layout", "pa_workspace_init",
            "pa_read_device_status", "pa_status_string", "pa_last_cuda_error",
            "pa_version", "pa_v2_forward_noalloc", "pa_host_staging_bytes", "pa_forward_host",
            "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine", "pa_append_kv",
-           "pa_select_blocks", "pa_sparse_forward", "pa_sparse_workspace_bytes")
+           "pa_select_blocks", "pa_sparse_forward", "pa_sparse_workspace_bytes",
+           "pa_prefix_forward", "pa_prefix_workspace_bytes")
 
 
 class PAError(RuntimeError):
@@ -113,6 +114,12 @@ def load_library(path: str = LIB_PATH):
         ll = ctypes.c_longlong
         lib.pa_append_kv.restype = ci
         lib.pa_append_kv.argtypes = [vp] * 7 + [ll] * 3 + [vp] * 5 + [ci] * 13 + [vp, cs, vp]
+        lib.pa_prefix_workspace_bytes.restype = cs
+        lib.pa_prefix_workspace_bytes.argtypes = [ci] * 8
+        lib.pa_prefix_forward.restype = ci
+        lib.pa_prefix_forward.argtypes = ([vp] * 9 + [ci] * 11 +
+                                          [ctypes.c_float, ci, ci, vp, cs, vp,
+                                           ctypes.POINTER(pa_options_t)])
         lib.pa_sparse_workspace_bytes.restype = cs
         lib.pa_sparse_workspace_bytes.argtypes = [ci] * 8
         lib.pa_select_blocks.restype = ci
@@ -401,6 +408,62 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
         H, hkv, D, nb, bs, block_tables.shape[1], int(max_seq_len), int(rotary_dim or 0),
         int(interleaved), max_position, _DTYPES[key_cache.dtype], _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
+
+
+def pa_prefix_workspace_bytes(num_seqs: int, num_prefixes: int, num_heads: int, num_kv_heads: int,
+                              head_size: int, max_seq_len: int, max_prefix_len: int,
+                              partition_size: int) -> int:
+    return int(load_library().pa_prefix_workspace_bytes(
+        num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len, max_prefix_len,
+        partition_size))
+
+
+def alloc_prefix_workspace(num_seqs: int, num_prefixes: int, num_heads: int, num_kv_heads: int,
+                           head_size: int, max_seq_len: int, max_prefix_len: int,
+                           partition_size: int, device=None, stream=None) -> torch.Tensor:
+    """A zeroed workspace for pa_prefix_forward."""
+    n = pa_prefix_workspace_bytes(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size,
+                                  max_seq_len, max_prefix_len, partition_size)
+    if n == 0:
+        raise ValueError("bad sizes for a prefix workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    pa_workspace_init(ws, stream)
+    return ws
+
+
+def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens, prefix_tables,
+                      prefix_lens, prefix_start, scale, partition_size, workspace,
+                      max_seq_len=None, max_prefix_len=None, stream=None, num_stages=0,
+                      ctas_per_sm=0, debug_flags=0, wait_limit_ns=0) -> None:
+    """Decode attention for sequences that share prefixes (see include/pa.h):
+    prefix_tables int32 [num_prefixes, max_prefix_blocks], prefix_lens int32
+    [num_prefixes], prefix_start int32 [num_prefixes + 1]; block_tables and
+    seq_lens are the sequences' own tokens."""
+    B, H, D = query.shape
+    nb, hkv, bs, D2 = key_cache.shape
+    _check_call(query.dtype, query.device, (out, key_cache, value_cache),
+                (block_tables, seq_lens, prefix_tables, prefix_lens, prefix_start))
+    G = prefix_lens.numel()
+    if out.shape != query.shape or D2 != D or value_cache.shape != key_cache.shape:
+        raise ValueError("query and out, or the caches, differ in shape")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    if prefix_tables.dim() != 2 or prefix_tables.shape[0] != G or prefix_start.numel() != G + 1:
+        raise ValueError("prefix_tables must be int32 [num_prefixes, max_prefix_blocks], "
+                         "prefix_start int32 [num_prefixes + 1]")
+    if max_seq_len is None:
+        max_seq_len = block_tables.shape[1] * bs
+    if max_prefix_len is None:
+        max_prefix_len = prefix_tables.shape[1] * bs
+    opts = pa_options_t(PA_VARIANT_V2, PA_MATH_AUTO, num_stages, debug_flags, wait_limit_ns, None,
+                        ctas_per_sm, 0, 0)
+    _check(load_library().pa_prefix_forward(
+        _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
+        _ptr(seq_lens), _ptr(prefix_tables), _ptr(prefix_lens), _ptr(prefix_start), B, G, H, hkv,
+        D, nb, bs, block_tables.shape[1], prefix_tables.shape[1], int(max_seq_len),
+        int(max_prefix_len), float(scale), int(partition_size), _DTYPES[query.dtype],
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream),
+        ctypes.byref(opts)), "pa_prefix_forward")
 
 
 def pa_sparse_workspace_bytes(num_rows: int, num_heads: int, num_kv_heads: int, head_size: int,

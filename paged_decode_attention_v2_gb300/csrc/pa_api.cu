@@ -11,6 +11,7 @@
 #include "pa.h"
 #include "pa_host.h"
 #include "pa_internal.h"
+#include "pa_ops.h"
 
 namespace {
 
@@ -223,6 +224,10 @@ struct Call {
   // run (bit 0: Phase 1, bit 1: Phase 2) and Phase 1's range of partitions
   int phases = 3;
   int part_begin = 0, part_end = INT_MAX;
+  // Shared prefixes (pa_prefix_forward): slots of every row behind its own
+  // partitions for its prefix's, and the rows' slot counts x partition_size
+  int extra_parts = 0;
+  const int *row_limit = nullptr;
 };
 
 // Rows of query (and output) and of the V2 workspace: sequences, or the query
@@ -235,6 +240,14 @@ int chunk_tokens_of(const Call &c) { return 16 / (c.num_heads / c.num_kv_heads);
 
 int max_parts_of(int max_seq_len, int partition_size) {
   return (max_seq_len + partition_size - 1) / partition_size;
+}
+
+// The length that sizes the workspace: every row's own partitions and the
+// extra ones.
+int layout_len(const Call &c) {
+  return c.extra_parts == 0 ? c.max_seq_len
+                            : (max_parts_of(c.max_seq_len, c.partition_size) + c.extra_parts) *
+                                  c.partition_size;
 }
 
 constexpr int kMaxReduceParts = 1 << 20;  // bound on partitions per sequence
@@ -281,7 +294,7 @@ pa_status_t check_args(const Call &c, bool need_v2) {
       !aligned(c.workspace, 256))
     return PA_ERR_INVALID_ARG;
   const size_t need = need_v2 ? pa_workspace_bytes(query_rows(c), c.num_heads, c.head_size,
-                                                   c.max_seq_len, c.partition_size)
+                                                   layout_len(c), c.partition_size)
                               : (size_t)kStatusBytes;
   if (need == 0) return PA_ERR_INVALID_ARG;
   if (c.workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
@@ -405,9 +418,9 @@ pa_status_t plan_phase2(const Call &c, const AttnParams &p, const DeviceFacts *d
   r.head_size = c.head_size;
   r.max_parts = p.max_parts;
   r.partition_size = c.partition_size;
-  r.max_seq_len = c.max_seq_len;
+  r.max_seq_len = layout_len(c);
   r.fuse_limit = p.fuse_limit;
-  r.row_limit = p.row_limit;
+  r.row_limit = c.row_limit ? c.row_limit : p.row_limit;
   // Rows whose partials fit in 8 KB (and 32 partitions, one a lane): a warp
   // takes each row's partials in one bulk copy, the next row's in flight
   // while it reduces the current one, so that the whole batch crosses the
@@ -615,10 +628,10 @@ pa_status_t launch(const Call &c, bool v2, const pa_options_t &opt) {
   }
 
   uint8_t *ws = static_cast<uint8_t *>(c.workspace);
-  const int max_parts = v2 ? max_parts_of(c.max_seq_len, c.partition_size) : 1;
+  const int max_parts = v2 ? max_parts_of(layout_len(c), c.partition_size) : 1;
   size_t off[5] = {0, 0, 0, 0, 0};
   if (v2) {
-    if (pa_workspace_layout(query_rows(c), c.num_heads, c.head_size, c.max_seq_len,
+    if (pa_workspace_layout(query_rows(c), c.num_heads, c.head_size, layout_len(c),
                             c.partition_size, off) != PA_OK)
       return PA_ERR_INVALID_ARG;
   }
@@ -1096,6 +1109,130 @@ pa_status_t pa_chunks_forward(void *out, const void *query, const void *key_cach
   c.max_chunk = max_chunk;
   if (num_rows == 0) return check_args(c, false);
   return run(c, opt.variant, opt);
+}
+
+size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads,
+                                 int head_size, int max_seq_len, int max_prefix_len,
+                                 int partition_size) {
+  if (num_seqs < 0 || num_prefixes < 1 || num_heads < 1 || num_kv_heads < 1 ||
+      num_heads % num_kv_heads || max_seq_len < 0 || max_prefix_len < 0 || partition_size < 1 ||
+      (head_size != 64 && head_size != 128 && head_size != 256))
+    return 0;
+  int split = 0, splits = 0;
+  prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_prefix_len, &split,
+              &splits);
+  const long long parts = (long long)max_parts_of(max_seq_len, partition_size) + splits;
+  if (parts > kMaxReduceParts || parts * partition_size > INT_MAX - partition_size) return 0;
+  return pa_workspace_bytes(num_seqs, num_heads, head_size, (int)parts * partition_size,
+                            partition_size) +
+         align256((size_t)num_seqs * 4);
+}
+
+pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cache,
+                              const void *value_cache, const int32_t *block_tables,
+                              const int32_t *seq_lens, const int32_t *prefix_tables,
+                              const int32_t *prefix_lens, const int32_t *prefix_start,
+                              int num_seqs, int num_prefixes, int num_heads, int num_kv_heads,
+                              int head_size, int num_blocks, int block_size,
+                              int max_blocks_per_seq, int max_prefix_blocks, int max_seq_len,
+                              int max_prefix_len, float scale, int partition_size, int dtype,
+                              void *workspace, size_t workspace_bytes, void *stream,
+                              const pa_options_t *opts) {
+  pa_options_t opt;
+  memset(&opt, 0, sizeof opt);
+  if (opts) opt = *opts;
+  if (opt.variant != PA_VARIANT_AUTO && opt.variant != PA_VARIANT_V2) return PA_ERR_INVALID_ARG;
+  opt.fuse_partitions = 0;
+  if (num_prefixes < 1 || max_prefix_blocks < 1 || max_prefix_len < 0 || !prefix_tables ||
+      !prefix_lens || !prefix_start || !aligned(prefix_tables, 4) || !aligned(prefix_lens, 4) ||
+      !aligned(prefix_start, 4))
+    return PA_ERR_INVALID_ARG;
+  if (block_size > 0 && (long long)max_prefix_len > (long long)max_prefix_blocks * block_size)
+    return PA_ERR_INVALID_ARG;
+  Call c = make_call(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_heads, num_kv_heads, head_size, num_blocks, block_size,
+                     max_blocks_per_seq, max_seq_len, scale, partition_size, dtype, workspace,
+                     workspace_bytes, stream);
+  // the sizes first (check_args with a workspace that always suffices), since
+  // the plan needs them
+  c.workspace_bytes = (size_t)-1;
+  pa_status_t st = check_args(c, true);
+  if (st != PA_OK) return st;
+  if (dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;  // tensor path only
+  if (opt.math == PA_MATH_SIMT) return PA_ERR_UNSUPPORTED;
+  int split = 0, splits = 0;
+  prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_prefix_len, &split,
+              &splits);
+  const size_t need = pa_prefix_workspace_bytes(num_seqs, num_prefixes, num_heads, num_kv_heads,
+                                                head_size, max_seq_len, max_prefix_len,
+                                                partition_size);
+  if (need == 0) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (num_seqs == 0) return PA_OK;
+  c.workspace_bytes = workspace_bytes;
+  c.extra_parts = splits;
+  size_t off[5];
+  const size_t limits = need - align256((size_t)num_seqs * 4);
+  if (pa_workspace_layout(num_seqs, num_heads, head_size, layout_len(c), partition_size, off) !=
+      PA_OK)
+    return PA_ERR_INVALID_ARG;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  c.row_limit = reinterpret_cast<const int *>(ws + limits);
+  st = check_args(c, true);
+  if (st != PA_OK) return st;
+
+  DeviceFacts *dev = nullptr;
+  st = device_facts(&dev);
+  if (st != PA_OK) return st;
+  const PrefixKernelInfo k = prefix_kernel(dtype == PA_DTYPE_BF16 ? 1 : 0, head_size);
+  if (!k.fn || k.smem > (size_t)dev->max_smem_optin) return PA_ERR_UNSUPPORTED;
+  st = ensure_smem(k.fn, k.smem);
+  if (st != PA_OK) return st;
+  CUtensorMap tmap_k, tmap_v;
+  const long long rows = (long long)num_blocks * num_kv_heads * block_size;
+  st = encode_cache_map_umma(&tmap_k, key_cache, dtype, head_size, rows, block_size);
+  if (st != PA_OK) return st;
+  st = encode_cache_map_umma(&tmap_v, value_cache, dtype, head_size, rows, block_size);
+  if (st != PA_OK) return st;
+  PrefixParams p{};
+  p.query = query;
+  p.prefix_tables = prefix_tables;
+  p.prefix_lens = prefix_lens;
+  p.prefix_start = prefix_start;
+  p.seq_lens = seq_lens;
+  p.max_logits = reinterpret_cast<float *>(ws + off[1]);
+  p.exp_sums = reinterpret_cast<float *>(ws + off[2]);
+  p.tmp_out = reinterpret_cast<float *>(ws + off[3]);
+  p.row_limit = reinterpret_cast<int *>(ws + limits);
+  p.status = reinterpret_cast<int *>(ws);
+  p.num_seqs = num_seqs;
+  p.num_prefixes = num_prefixes;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_heads / num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.log2_block_size = ilog2(block_size);
+  p.max_prefix_blocks = max_prefix_blocks;
+  p.max_prefix_len = max_prefix_len;
+  p.max_seq_len = max_seq_len;
+  p.partition_size = partition_size;
+  p.max_parts = max_parts_of(layout_len(c), partition_size);
+  p.split_tokens = split;
+  p.debug_flags = opt.debug_flags;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.wait_limit_ns = opt.wait_limit_ns ? opt.wait_limit_ns : kDefaultWaitLimitNs;
+  // one CTA an SM (its shared memory), never more than there can be items
+  const long long tiles = (long long)num_seqs * p.group / k.tile_rows +
+                          (num_prefixes < num_seqs ? num_prefixes : num_seqs);
+  long long grid = tiles * num_kv_heads * splits;
+  if (grid > dev->sm_count) grid = dev->sm_count;
+  if (grid < 1) grid = 1;
+  void *args[3] = {&p, &tmap_k, &tmap_v};
+  st = host_launch(k.fn, (unsigned)grid, 1, k.threads, k.smem, stream, args,
+                   "launch prefix kernel");
+  if (st != PA_OK) return st;
+  return launch(c, true, opt);
 }
 
 size_t pa_host_staging_bytes(int num_seqs, int num_heads, int head_size,

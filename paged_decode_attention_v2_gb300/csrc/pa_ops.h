@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace pa {
@@ -32,6 +33,38 @@ __host__ __device__ __forceinline__ int view_block(int blk, int kv_head, int num
                                                    int num_blocks) {
   return (unsigned)blk < (unsigned)num_blocks ? blk * num_kv_heads + kv_head : -1;
 }
+
+constexpr int kMaxPrefixSplits = 64;
+constexpr int kPrefixDebugStall = 1;  // PA_DEBUG_STALL_CONSUMERS
+
+struct PrefixParams {
+  const void *query;                   // [B][H][D]
+  const int32_t *prefix_tables;        // [num_prefixes][max_prefix_blocks]
+  const int32_t *prefix_lens;          // [num_prefixes]
+  const int32_t *prefix_start;         // [num_prefixes + 1]: sequences of each group
+  const int32_t *seq_lens;             // [B]: own keys
+  float *max_logits, *exp_sums, *tmp_out;  // [B][H][max_parts](, [D])
+  int *row_limit;                      // [B]: partitions x partition_size, for Phase 2
+  int *status;
+  int num_seqs, num_prefixes, num_heads, num_kv_heads, group, num_blocks;
+  int block_size, log2_block_size, max_prefix_blocks, max_prefix_len;
+  int max_seq_len, partition_size, max_parts;
+  int split_tokens;  // keys of a split, a multiple of the kernel's stage
+  int debug_flags;
+  float scale_log2;  // scale * log2(e)
+  uint64_t wait_limit_ns;
+};
+
+struct PrefixKernelInfo {
+  const void *fn;
+  int threads;
+  size_t smem;
+  int tile_rows;   // rows of an item
+  int stage_keys;  // keys of a stage
+};
+PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size);
+void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
+                 int max_prefix_len, int *split_tokens, int *max_splits);
 
 struct SelectParams {
   const void *query;       // [rows][H][D]

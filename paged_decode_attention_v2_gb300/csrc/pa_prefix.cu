@@ -1,0 +1,655 @@
+// Decode attention over a prefix that a group of sequences shares: Phase 1 of
+// pa_prefix_forward, on the 5th-generation tensor cores (tcgen05, sm_103a).
+//
+// For the rows (sequence, head) of a group and one KV head, and one split of
+// the prefix's keys,
+//   S = Q K^T,  m = max_k S,  l = sum_k exp(S - m),  O = exp(S - m) V / l,
+// the three going to the workspace as one more partition of every row's own
+// (Phase 2 merges them with the log-sum-exp rule).  The prefix's keys and
+// values are read once for all the rows of an item, so with many rows this is
+// a matrix product and bound by the tensor cores, with few by the read of the
+// prefix.
+//
+// An item is up to NT x 128 rows of a (group, KV head) and one split.  The CTA
+// holds the rows' queries in shared memory and streams the split through a
+// ring of slots (TMA, whole pages): K of stage j, V of stage j, K of stage
+// j + 1, ...  One thread issues the MMAs.  S lives in tensor memory, fp32, one
+// row a lane; a softmax thread owns a row: its maximum and sum need no
+// shuffles.  P goes back over S's columns, rounded to the input type (the sum
+// adds the unrounded exponentials; the two differ by 2^-9 relative at most,
+// unbiased), and is the PV product's A operand straight from tensor memory.
+//   D 64, 128: two row tiles (NT 2) share every stage of 128 keys; while the
+//     softmax of one runs, the tensor cores work on the other:
+//     PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) ...
+//     Tensor memory: S_0 S_1 (128 columns each), O_0 O_1 (D each).
+//   D 256: O takes 256 columns, so one tile (NT 1), stages of 64 keys and two
+//     S buffers: S(j+1) is issued before PV(j).
+// MMAs of one thread execute in order, so a PV has read its P before the next
+// S of that buffer overwrites it, and a commit behind an S also covers the PV
+// before it.  The running maximum is raised lazily: O is rescaled only when a
+// stage exceeds it by more than 2^8, which the final sum undoes exactly.
+//
+// Warps: 0-3 (and 4-7) softmax, then one producer and one MMA warp.  Every
+// role works out the CTA's items by itself from the lengths, so there are no
+// headers to pass.  Every wait is bounded.
+#include <type_traits>
+
+#include <math_constants.h>
+
+#include "pa_device.cuh"
+#include "pa_ops.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTileRows = 128;      // the MMA's M
+constexpr float kLazyMargin = 8.f;  // log2 units
+
+template <int D>
+struct PrefixShape {
+  static constexpr int NT = D == 256 ? 1 : 2;       // row tiles of an item
+  static constexpr int KEYS = D == 256 ? 64 : 128;  // keys of a stage
+  static constexpr int SLOTS = D == 64 ? 10 : 5;    // K or V of a stage each
+  static constexpr int PANELS = D * 2 / 128;        // 128-byte panels of a row
+  static constexpr int GROUP = PANELS * 1024;       // bytes of 8 keys
+  static constexpr int SLOT = KEYS / 8 * GROUP;
+  static constexpr int QPANEL = kTileRows * 128;
+  static constexpr int QTILE = PANELS * QPANEL;
+  static constexpr int SOFTMAX_WARPS = 4 * NT;
+  static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
+  // full and empty of each slot, Q ready a tile, S and P ready a buffer, O
+  // done a tile, PV done (NT 1), drain, never
+  static constexpr int BARS = 2 * SLOTS + 2 + 2 + 2 + 2 + 3;
+  static constexpr size_t SMEM = (size_t)NT * QTILE + (size_t)SLOTS * SLOT + BARS * 8 + 16;
+};
+
+// D = A . B (+ D), A from tensor memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// eight floats in one store (32-byte aligned)
+__device__ __forceinline__ void store8(float *dst, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// One item: rows [row0, row0 + rows) of group [seq0, ...), one KV head, one
+// split of the prefix.
+struct PrefixItem {
+  int group, seq0, rows, row0, kvh, split, tok0, tok1;
+};
+
+// Group g's first sequence, sequences and prefix length, clamped to what the
+// buffers hold.
+__device__ __forceinline__ void prefix_group(const PrefixParams &p, int g, int &seq0, int &n,
+                                             int &len) {
+  seq0 = __ldg(p.prefix_start + g);
+  int end = __ldg(p.prefix_start + g + 1);
+  len = __ldg(p.prefix_lens + g);
+  if (seq0 < 0 || end < seq0 || end > p.num_seqs || len < 0 || len > p.max_prefix_len) {
+    report(p.status, kStatusBadInput);
+    seq0 = max(0, min(seq0, p.num_seqs));
+    end = max(seq0, min(end, p.num_seqs));
+    len = max(0, min(len, p.max_prefix_len));
+  }
+  n = end - seq0;
+}
+
+// Walks the item list in order (the same list in every role): find() must be
+// called by a whole warp with non-decreasing indices.
+template <int ROWS>
+struct ItemWalk {
+  int base = 0, first_group = 0;      // items before, and first of, the 32 groups held
+  int cnt, incl, seq0, n, len;        // this lane's group
+  bool loaded = false;
+
+  __device__ __forceinline__ bool find(const PrefixParams &p, int item, PrefixItem &it) {
+    const int lane = threadIdx.x & 31;
+    while (true) {
+      if (!loaded) {
+        cnt = seq0 = n = len = 0;
+        const int g = first_group + lane;
+        if (g < p.num_prefixes) {
+          prefix_group(p, g, seq0, n, len);
+          const int tiles = (n * p.group + ROWS - 1) / ROWS;
+          const int splits = (len + p.split_tokens - 1) / p.split_tokens;
+          cnt = tiles * splits * p.num_kv_heads;
+        }
+        incl = cnt;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += t;
+        }
+        loaded = true;
+      }
+      const int total = __shfl_sync(0xffffffffu, incl, 31);
+      if (item < base + total) {
+        const unsigned hit = __ballot_sync(0xffffffffu, base + incl > item);
+        const int l = __ffs(hit) - 1;
+        int rem = item - base - __shfl_sync(0xffffffffu, incl - cnt, l);
+        it.group = first_group + l;
+        it.seq0 = __shfl_sync(0xffffffffu, seq0, l);
+        const int rows = __shfl_sync(0xffffffffu, n, l) * p.group;
+        const int plen = __shfl_sync(0xffffffffu, len, l);
+        // row tiles fastest: the CTAs of one wave share their keys in L2
+        const int tiles = (rows + ROWS - 1) / ROWS;
+        const int tile = rem % tiles;
+        rem /= tiles;
+        it.kvh = rem % p.num_kv_heads;
+        it.split = rem / p.num_kv_heads;
+        it.row0 = tile * ROWS;
+        it.rows = min(ROWS, rows - it.row0);
+        it.tok0 = it.split * p.split_tokens;
+        it.tok1 = min(it.tok0 + p.split_tokens, plen);
+        return true;
+      }
+      if (first_group + 32 >= p.num_prefixes) return false;
+      first_group += 32;
+      base += total;
+      loaded = false;
+    }
+  }
+};
+
+// Partitions of a sequence's own keys (its partials come before the prefix's).
+__device__ __forceinline__ int own_parts(const PrefixParams &p, int seq) {
+  const int L = max(0, min(__ldg(p.seq_lens + seq), p.max_seq_len));
+  return (L + p.partition_size - 1) / p.partition_size;
+}
+
+}  // namespace
+
+template <typename T, int D>
+__global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
+    pa_prefix_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v) {
+  using Z = PrefixShape<D>;
+  constexpr int NT = Z::NT, KEYS = Z::KEYS, NS = Z::SLOTS;
+  constexpr uint32_t kIdescS = instr_desc<T>(kTileRows, KEYS, false);
+  constexpr uint32_t kIdescPV = instr_desc<T>(kTileRows, D, true);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // 1024-byte aligned as the swizzle needs it: dynamic shared memory starts
+  // right after the 1 KB that the system reserves (checked)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) report(p.status, kStatusBadInput);
+    return;
+  }
+  uint8_t *qbuf = smem_raw;                       // NT x [panel][128 rows][128 B]
+  uint8_t *ring = qbuf + NT * Z::QTILE;           // NS x [8-key group][panel][8 keys][128 B]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ring + NS * Z::SLOT);
+  volatile int *flags = reinterpret_cast<volatile int *>(bars + Z::BARS);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::BARS) + 1;
+  const uint32_t q_u32 = smem_u32(qbuf), ring_u32 = smem_u32(ring);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * NS, q_full = empty0 + 8 * NS,
+                 s_full = q_full + 16, p_full = s_full + 16, o_done = p_full + 16,
+                 pv_done = o_done + 16, drain = pv_done + 8, never = drain + 8;
+  const uint64_t limit = p.wait_limit_ns;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 4);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(never, 1);
+    flags[0] = 0;
+    fence_mbar_init();
+  }
+  // wait for the kernel before in the stream, also before taking tensor
+  // memory that a CTA of it may still hold
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (warp == Z::SOFTMAX_WARPS + 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem_o = tmem + 256;  // S (and P) buffers at columns 0 and 128
+  ItemWalk<NT * kTileRows> walk;
+  PrefixItem it;
+
+  if (warp == Z::SOFTMAX_WARPS) {
+    // ======================= producer warp =======================
+    if (lane == 0) {
+      prefetch_tmap(&tmap_k);
+      prefetch_tmap(&tmap_v);
+    }
+    bool ok = true;
+    int op = 0;  // copies issued: K and V of each stage, in turn
+    const int U = p.block_size;
+    for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
+      const int32_t *bt = p.prefix_tables + (size_t)it.group * p.max_prefix_blocks;
+      const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
+      // lane's page of a stage; the next stage's entries load while this one waits
+      auto entry = [&](int j) -> int {
+        const int tok = it.tok0 + j * KEYS + lane * U;
+        return j < stages && lane < KEYS / U && tok < it.tok1 ? __ldg(bt + (tok >> p.log2_block_size)) : -1;
+      };
+      int blk = entry(0);
+      for (int j = 0; ok && j < stages; ++j) {
+        const int next = entry(j + 1);
+        const int tok = it.tok0 + j * KEYS + lane * U;
+        int y = -1;
+        if (lane < KEYS / U && tok < it.tok1) {
+          if ((unsigned)blk >= (unsigned)p.num_blocks)
+            report(p.status, kStatusBadInput);
+          else
+            y = (blk * p.num_kv_heads + it.kvh) * U;
+        }
+        blk = next;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, y >= 0)) * U * D * 2u;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int sl = op % NS;
+          if (op >= NS) {
+            bool w = true;
+            if (lane == 0) w = mbar_wait(empty0 + 8 * sl, ((op / NS) - 1) & 1, limit, flags);
+            ok = __shfl_sync(0xffffffffu, w, 0);
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * sl, bytes);
+          __syncwarp();
+          if (y >= 0)
+            tma_load_4d(ring_u32 + (uint32_t)sl * Z::SLOT + (uint32_t)(lane * U / 8) * Z::GROUP,
+                        kv == 0 ? &tmap_k : &tmap_v, 0, 0, 0, y >> 3, full0 + 8 * sl);
+          ++op;
+        }
+      }
+    }
+    // the partitions of every row, for Phase 2: its own, then its prefix's
+    for (int s = blockIdx.x * 32 + lane; s < p.num_seqs; s += gridDim.x * 32) {
+      int lo = 0, hi = p.num_prefixes + 1;  // the first start above s
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.prefix_start + mid) > s)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      int splits = 0;
+      if (lo == 0 || lo > p.num_prefixes) {  // in no group
+        report(p.status, kStatusBadInput);
+      } else {
+        int s0, n, len;
+        prefix_group(p, lo - 1, s0, n, len);
+        splits = (len + p.split_tokens - 1) / p.split_tokens;
+      }
+      p.row_limit[s] = (own_parts(p, s) + splits) * p.partition_size;
+    }
+    if (!ok && lane == 0) {
+      report(p.status, kStatusTimeout);
+      flags[0] = 1;
+    }
+    if (lane == 0)  // every copy lands before the CTA retires
+      for (int i = op > NS ? op - NS : 0; i < op; ++i)
+        mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, kDrainLimitNs, nullptr);
+    __syncwarp();
+  } else if (warp == Z::SOFTMAX_WARPS + 1) {
+    // ======================= MMA warp (one thread issues) =======================
+    bool ok = true;
+    int op = 0;                 // slots consumed so far: K of the next stage
+    int items[2] = {0, 0};      // items of each tile
+    int done[2] = {0, 0};       // stages of each tile (NT 1: [0], over both buffers)
+    for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
+      const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
+      const int nt = (it.rows + kTileRows - 1) / kTileRows;
+      if (lane == 0) {
+        auto wait_slot = [&](int o) -> bool {
+          return mbar_wait(full0 + 8 * (o % NS), (o / NS) & 1, limit, flags);
+        };
+        // S = Q K^T: D / 16 k-steps of 32 bytes inside a panel
+        auto issue_s = [&](int o, int t, int buf) {
+          const uint32_t kst = ring_u32 + (uint32_t)(o % NS) * Z::SLOT;
+          const uint32_t qt = q_u32 + (uint32_t)t * Z::QTILE;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (uint32_t)(ks & 3) * 32u;
+            const uint64_t da = smem_desc(qt + (uint32_t)(ks >> 2) * Z::QPANEL + off, 16, 1024);
+            const uint64_t db = smem_desc(kst + (uint32_t)(ks >> 2) * 1024u + off, 16, Z::GROUP);
+            tc_mma(tmem + 128u * (uint32_t)buf, da, db, kIdescS, ks > 0 ? 1u : 0u);
+          }
+          tc_commit(s_full + 8u * (uint32_t)buf);
+        };
+        // O += P V: k-steps of 16 keys; P two keys a column, V MN-major
+        auto issue_pv = [&](int o, int t, int buf, bool first) {
+          const uint32_t vst = ring_u32 + (uint32_t)(o % NS) * Z::SLOT;
+#pragma unroll
+          for (int kk = 0; kk < KEYS / 16; ++kk) {
+            const uint64_t db = smem_desc(vst + (uint32_t)kk * 2u * Z::GROUP, 1024, Z::GROUP);
+            tc_mma_ts(tmem_o + (uint32_t)(t * D), tmem + 128u * (uint32_t)buf + 8u * (uint32_t)kk, db,
+                      kIdescPV, first && kk == 0 ? 0u : 1u);
+          }
+        };
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (ok && t < nt) ok = mbar_wait(q_full + 8 * t, items[t] & 1, limit, flags);
+        if (ok) ok = wait_slot(op);
+        if (ok) {
+          tc_fence_after();
+          if constexpr (NT == 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (t < nt) issue_s(op, t, t);
+          } else {
+            issue_s(op, 0, done[0] & 1);
+          }
+          tc_commit(empty0 + 8 * (op % NS));
+        }
+        for (int j = 0; ok && j < stages; ++j) {
+          const int ok_k = op + 2 * j, ov = ok_k + 1, nk = ok_k + 2;  // K, V, the next K
+          const bool more = j + 1 < stages;
+          if constexpr (NT == 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t >= nt) break;
+              ok = mbar_wait(p_full + 8 * t, done[t] & 1, limit, flags);
+              if (ok && t == 0) ok = wait_slot(ov);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(ov, t, t, j == 0);
+              if (t == nt - 1) tc_commit(empty0 + 8 * (ov % NS));
+              if (more) {
+                if (t == 0) {
+                  ok = wait_slot(nk);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                issue_s(nk, t, t);
+                if (t == nt - 1) tc_commit(empty0 + 8 * (nk % NS));
+              } else {
+                tc_commit(o_done + 8 * t);
+              }
+              ++done[t];
+            }
+          } else {
+            const int b = done[0] & 1;
+            if (more) {
+              ok = wait_slot(nk);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(nk, 0, b ^ 1);
+              tc_commit(empty0 + 8 * (nk % NS));
+            }
+            ok = mbar_wait(p_full + 8 * b, (done[0] >> 1) & 1, limit, flags) && wait_slot(ov);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(ov, 0, b, j == 0);
+            tc_commit(empty0 + 8 * (ov % NS));
+            tc_commit(pv_done);
+            if (!more) tc_commit(o_done);
+            ++done[0];
+          }
+        }
+        op += 2 * stages;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) items[t] += t < nt;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {  // nothing may still run when the memory is freed
+      tc_commit(drain);
+      mbar_wait(drain, 0, kDrainLimitNs, nullptr);
+      if (!ok) {
+        report(p.status, kStatusTimeout);
+        flags[0] = 1;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ======================= softmax warps: thread = row =======================
+    const int t = warp >> 2;               // the tile
+    const int r = threadIdx.x & 127;       // row of the tile, and tensor-memory lane
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t my_o = tmem_o + (uint32_t)(t * D) + lane_off;
+    uint8_t *qt = qbuf + t * Z::QTILE;
+    const float sc = fabsf(p.scale_log2);
+    const bool neg = p.scale_log2 < 0.f;
+    bool ok = true;
+    int done = 0, items = 0, ops = 0;
+    if (p.debug_flags & kPrefixDebugStall) {
+      // wait on a barrier that nothing releases: the bound must end it
+      ok = mbar_wait(never, 0, limit, flags);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
+      const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
+      const int rows = it.rows - t * kTileRows;  // of this tile
+      if (rows <= 0) {
+        ops += 2 * stages;
+        continue;
+      }
+      const int gr = it.row0 + t * kTileRows + r;  // row of the group
+      const bool live = r < rows;
+      const bool warp_live = 32 * (warp & 3) < rows;
+      const int seq = it.seq0 + (live ? gr / p.group : 0);
+      const int head = it.kvh * p.group + (live ? gr % p.group : 0);
+      const size_t orow = (size_t)seq * p.num_heads + head;
+      {  // the row's query into the swizzled tile (zeros past the item's rows)
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) + orow * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(qt + (c >> 3) * Z::QPANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + 8 * t);
+      }
+      float m_run = -CUDART_INF_F, l = 0.f;
+      for (int j = 0; ok && j < stages; ++j) {
+        const int buf = NT == 2 ? t : done & 1;
+        const uint32_t par = NT == 2 ? (uint32_t)done & 1u : ((uint32_t)done >> 1) & 1u;
+        const uint32_t sbuf = tmem + 128u * (uint32_t)buf + lane_off;
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * buf, par, limit, flags));
+        if (!ok) break;
+        tc_fence_after();
+        const int valid = min(KEYS, it.tok1 - it.tok0 - j * KEYS);
+        if (valid < KEYS && t == 0) {
+          // V rows past the range may hold anything (0 x NaN would reach O):
+          // zeros.  Tile 0's P is awaited before either tile's PV.
+          const int ov = ops + 2 * j + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * (ov % NS), (ov / NS) & 1, limit, flags));
+          if (!ok) break;
+          uint8_t *vst = ring + (size_t)(ov % NS) * Z::SLOT;
+          for (int i = r; i < (KEYS - valid) * (D / 8); i += 128) {
+            const int row = valid + i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4 *>(vst + (row >> 3) * Z::GROUP + (c >> 3) * 1024 + (row & 7) * 128 +
+                                       (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (warp_live) {
+          uint32_t s[KEYS / 32][32];
+#pragma unroll
+          for (int c = 0; c < KEYS / 32; ++c) tmem_ld32(sbuf + 32 * c, s[c]);
+#pragma unroll
+          for (int c = 0; c < KEYS / 32; ++c) tmem_ld_wait(s[c]);
+          auto x = [&](int k) -> float { return __uint_as_float(s[k >> 5][k & 31]); };
+          if (neg) {  // a negative scale: the largest logit has the smallest product
+#pragma unroll
+            for (int k = 0; k < KEYS; ++k) s[k >> 5][k & 31] ^= 0x80000000u;
+          }
+          if (valid < KEYS) {  // (no infinities: their P is set to zero below)
+#pragma unroll
+            for (int k = 1; k < KEYS; ++k)
+              if (k >= valid) s[k >> 5][k & 31] = s[0][0];
+          }
+          float m8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            m8[i] = x(i);
+#pragma unroll
+            for (int k = i + 8; k + 8 < KEYS; k += 16) m8[i] = fmax3(m8[i], x(k), x(k + 8));
+            m8[i] = fmaxf(m8[i], x(KEYS - 8 + i));
+          }
+          const float mt = sc * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                      fmaxf(m8[6], m8[7]));
+          const bool raise = mt > m_run + kLazyMargin;
+          const float alpha = raise ? exp2f(m_run - mt) : 1.f;
+          if (raise) m_run = mt;
+          if (j > 0 && __any_sync(0xffffffffu, raise)) {
+            // rescale the rows' O, once the PV of the stage before is done (NT
+            // 2: this S was issued behind it)
+            if constexpr (NT == 1) {
+              ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (uint32_t)(done - 1) & 1u, limit, flags));
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(my_o + 32 * c, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(my_o + 32 * c, o);
+            }
+            tmem_st_wait();
+          }
+          const float mb = m_run == -CUDART_INF_F ? 0.f : -m_run;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < KEYS / 32; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int k = 32 * c + 2 * e;
+              float p0 = ex2(fmaf(x(k), sc, mb)), p1 = ex2(fmaf(x(k + 1), sc, mb));
+              if (valid < KEYS) {
+                p0 = k < valid ? p0 : 0.f;
+                p1 = k + 1 < valid ? p1 : 0.f;
+              }
+              l4[e & 3] += p0 + p1;
+              w[e] = MmaOp<T>::pack(p0, p1);
+            }
+            tmem_st16(sbuf + 16 * c, w);
+          }
+          l = l * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * buf);
+        ++done;
+      }
+      ops += 2 * stages;
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * t, items & 1, limit, flags));
+      if (!ok) break;
+      ++items;
+      tc_fence_after();
+      if (warp_live) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const size_t slot = orow * p.max_parts + own_parts(p, seq) + it.split;
+        float *dst = p.tmp_out + slot * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(my_o + 32 * c, o);
+          tmem_ld_wait(o);
+          if (!live) continue;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[k + e]) * inv;
+            store8(dst + 32 * c + k, v);
+          }
+        }
+        if (live) {
+          p.max_logits[slot] = m_run * 0.69314718055994530942f;  // natural-log units
+          p.exp_sums[slot] = l;
+        }
+      }
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) {
+      report(p.status, kStatusTimeout);
+      flags[0] = 1;
+    }
+  }
+  // every role is done with the tensor memory: free it
+  tc_fence_before();
+  __syncthreads();
+  if (warp == Z::SOFTMAX_WARPS + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+template <typename T>
+PrefixKernelInfo pick(int head_size) {
+  switch (head_size) {
+    case 64:
+      return {reinterpret_cast<const void *>(&pa_prefix_kernel<T, 64>), PrefixShape<64>::THREADS,
+              PrefixShape<64>::SMEM, PrefixShape<64>::NT * kTileRows, PrefixShape<64>::KEYS};
+    case 128:
+      return {reinterpret_cast<const void *>(&pa_prefix_kernel<T, 128>), PrefixShape<128>::THREADS,
+              PrefixShape<128>::SMEM, PrefixShape<128>::NT * kTileRows, PrefixShape<128>::KEYS};
+    case 256:
+      return {reinterpret_cast<const void *>(&pa_prefix_kernel<T, 256>), PrefixShape<256>::THREADS,
+              PrefixShape<256>::SMEM, PrefixShape<256>::NT * kTileRows, PrefixShape<256>::KEYS};
+  }
+  return {};
+}
+}  // namespace
+
+PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size) {
+  return dtype_bf16 ? pick<__nv_bfloat16>(head_size) : pick<__half>(head_size);
+}
+
+// Splits of the prefix.  One wave of items should fill the SMs, with as few
+// splits as that takes: each is another partial of every row to write and
+// read back.  The cost counted here, in stages of an item's keys: the waves
+// times (an item's stages, and its start-up and epilogue, about four), plus
+// the partials' bytes.  The sizes of the groups are not known on the host:
+// rows are counted as if packed, with at least one tile a group.
+void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
+                 int max_prefix_len, int *split_tokens, int *max_splits) {
+  constexpr int kSms = 152;
+  const PrefixKernelInfo k = prefix_kernel(1, head_size);
+  const long long rows = (long long)num_seqs * (num_heads / num_kv_heads);
+  long long tiles = (rows + k.tile_rows - 1) / k.tile_rows;
+  const long long groups = num_prefixes < num_seqs ? num_prefixes : num_seqs;
+  if (tiles < groups) tiles = groups;
+  const long long heads = tiles * num_kv_heads;
+  const int stages = (max_prefix_len + k.stage_keys - 1) / k.stage_keys;
+  int best = 1;
+  double best_cost = 0.;
+  for (int n = 1; n <= kMaxPrefixSplits && n <= (stages > 0 ? stages : 1); ++n) {
+    const int per = (stages + n - 1) / n;
+    const long long waves = (heads * n + kSms - 1) / kSms;
+    // a stage takes about 1 us on every SM; partials 2 x 4 D bytes a row at 6 TB/s
+    const double cost = (double)waves * (per + 4) + (double)rows * num_kv_heads * n * head_size * 8. / 6e6;
+    if (n == 1 || cost < best_cost) {
+      best = n;
+      best_cost = cost;
+    }
+  }
+  const int per = (stages + best - 1) / best;
+  *split_tokens = (per > 0 ? per : 1) * k.stage_keys;
+  *max_splits = (max_prefix_len + *split_tokens - 1) / *split_tokens;
+}
+
+}  // namespace pa

@@ -1,0 +1,308 @@
+"""pa_prefix_forward against the definition in 64 bits: groups of sequences
+that share a prefix, every head size and 16-bit type, lengths that end anywhere
+in a page, a stage or a split; refusals (CPU), reports of bad data, timeouts."""
+import math
+import random
+
+import pytest
+import torch
+
+import paged_decode_attention_v2_gb300 as pa
+from gpu_helpers import assert_close
+
+FAKE = 1 << 20  # aligned, never dereferenced by the host checks
+
+BASE = dict(out=FAKE, query=FAKE, key_cache=FAKE, value_cache=FAKE, block_tables=FAKE, seq_lens=FAKE,
+            prefix_tables=FAKE, prefix_lens=FAKE, prefix_start=FAKE, num_seqs=3, num_prefixes=2,
+            num_heads=8, num_kv_heads=2, head_size=128, num_blocks=64, block_size=16,
+            max_blocks_per_seq=8, max_prefix_blocks=32, max_seq_len=128, max_prefix_len=512,
+            scale=0.1, partition_size=512, dtype=pa.PA_DTYPE_BF16, workspace=FAKE,
+            workspace_bytes=1 << 30, stream=0, opts=None)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    return pa.load_library()
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(out=0), pa.PA_ERR_INVALID_ARG),
+    (dict(query=0), pa.PA_ERR_INVALID_ARG),
+    (dict(prefix_tables=0), pa.PA_ERR_INVALID_ARG),
+    (dict(prefix_lens=0), pa.PA_ERR_INVALID_ARG),
+    (dict(prefix_start=FAKE + 2), pa.PA_ERR_INVALID_ARG),
+    (dict(num_prefixes=0), pa.PA_ERR_INVALID_ARG),
+    (dict(max_prefix_blocks=0), pa.PA_ERR_INVALID_ARG),
+    (dict(max_prefix_len=513), pa.PA_ERR_INVALID_ARG),
+    (dict(max_prefix_len=-1), pa.PA_ERR_INVALID_ARG),
+    (dict(max_seq_len=129), pa.PA_ERR_INVALID_ARG),
+    (dict(num_heads=9), pa.PA_ERR_INVALID_ARG),
+    (dict(scale=math.nan), pa.PA_ERR_INVALID_ARG),
+    (dict(query=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(workspace=FAKE + 64), pa.PA_ERR_INVALID_ARG),
+    (dict(dtype=pa.PA_DTYPE_F32), pa.PA_ERR_UNSUPPORTED),
+    (dict(head_size=96), pa.PA_ERR_UNSUPPORTED),
+    (dict(num_heads=34), pa.PA_ERR_UNSUPPORTED),
+    (dict(partition_size=96), pa.PA_ERR_UNSUPPORTED),
+    (dict(block_size=24, max_prefix_len=500), pa.PA_ERR_UNSUPPORTED),
+    (dict(workspace_bytes=1000), pa.PA_ERR_WORKSPACE_TOO_SMALL),
+])
+def test_refusals(lib, over, status):
+    assert lib.pa_prefix_forward(*dict(BASE, **over).values()) == status
+
+
+def test_refused_variants(lib):
+    for kw in (dict(variant=pa.PA_VARIANT_V1), dict(variant=7)):
+        o = pa.pa_options_t(**kw)
+        assert lib.pa_prefix_forward(*dict(BASE, opts=o).values()) == pa.PA_ERR_INVALID_ARG
+    o = pa.pa_options_t(math=pa.PA_MATH_SIMT)
+    assert lib.pa_prefix_forward(*dict(BASE, opts=o).values()) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_workspace_bytes(lib):
+    f = pa.pa_prefix_workspace_bytes
+    n = f(3, 2, 8, 2, 128, 128, 512, 512)
+    assert n % 256 == 0 and n > pa.pa_workspace_bytes(3, 8, 128, 128, 512)
+    assert lib.pa_prefix_forward(*dict(BASE, workspace_bytes=n - 1).values()) == \
+        pa.PA_ERR_WORKSPACE_TOO_SMALL
+    assert lib.pa_prefix_forward(*dict(BASE, num_seqs=0).values()) == pa.PA_OK
+    assert f(3, 0, 8, 2, 128, 128, 512, 512) == 0 and f(3, 1, 8, 3, 128, 128, 512, 512) == 0
+    assert f(3, 1, 8, 2, 128, 0, 0, 512) > 0
+
+
+# ---------------------------------------------------------------------------
+
+class Case:
+    def __init__(self, seed, dtype, H, K, D, bs, counts, prefix, own, P=512, k_mult=2.0, scale=None):
+        g = torch.Generator().manual_seed(seed)
+        B = sum(counts)
+        assert len(own) == B and len(prefix) == len(counts)
+        self.__dict__.update(dtype=dtype, H=H, K=K, D=D, bs=bs, counts=counts, prefix=prefix, own=own,
+                             P=P, B=B, scale=1 / math.sqrt(D) if scale is None else scale)
+        pages = [-(-L // bs) for L in prefix + own]
+        pool = sum(pages) + 2
+        perm = torch.randperm(pool, generator=g).to(torch.int32)
+        at, tabs = 0, []
+        for n in pages:
+            tabs.append(perm[at:at + n])
+            at += n
+
+        def table(rows):
+            t = torch.full((len(rows), max([len(x) for x in rows] + [1])), -1, dtype=torch.int32)
+            for i, x in enumerate(rows):
+                t[i, :len(x)] = x
+            return t
+        self.pt, self.bt = table(tabs[:len(prefix)]), table(tabs[len(prefix):])
+        self.start = [0]
+        for n in counts:
+            self.start.append(self.start[-1] + n)
+        self.q = torch.randn(B, H, D, generator=g).to(dtype)
+        self.kc = (k_mult * torch.randn(pool, K, bs, D, generator=g)).to(dtype)
+        self.vc = torch.randn(pool, K, bs, D, generator=g).to(dtype)
+
+    def rows(self, cache, table, n):
+        t = torch.arange(n)
+        return cache[table[t // self.bs].long(), :, t % self.bs].double().transpose(0, 1)  # [K, n, D]
+
+    def reference(self):
+        G = self.H // self.K
+        out = torch.zeros(self.B, self.K, G, self.D, dtype=torch.float64)
+        for g, P in enumerate(self.prefix):
+            kp, vp = self.rows(self.kc, self.pt[g], P), self.rows(self.vc, self.pt[g], P)
+            for s in range(self.start[g], self.start[g + 1]):
+                k = torch.cat([kp, self.rows(self.kc, self.bt[s], self.own[s])], 1)
+                v = torch.cat([vp, self.rows(self.vc, self.bt[s], self.own[s])], 1)
+                if k.shape[1]:
+                    x = self.q[s].double().view(self.K, G, self.D) @ k.transpose(1, 2) * self.scale
+                    out[s] = torch.softmax(x, -1) @ v
+        return out.view(self.B, self.H, self.D).numpy()
+
+    def device(self, poison=True):
+        dev = "cuda"
+        kc, vc = self.kc.clone(), self.vc.clone()
+        if poison:  # what lies behind the last token of a page is never used
+            for t, L in zip(list(self.pt) + list(self.bt), self.prefix + self.own):
+                if L % self.bs:
+                    kc[t[L // self.bs], :, L % self.bs:] = math.nan
+                    vc[t[L // self.bs], :, L % self.bs:] = math.inf
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+        return dict(q=self.q.to(dev), kc=kc.to(dev), vc=vc.to(dev), bt=self.bt.to(dev), sl=i32(self.own),
+                    pt=self.pt.to(dev), pl=i32(self.prefix), ps=i32(self.start),
+                    ws=pa.alloc_prefix_workspace(self.B, len(self.prefix), self.H, self.K, self.D,
+                                                 max(self.own), max(self.prefix), self.P),
+                    out=torch.full((self.B, self.H, self.D), math.nan, dtype=self.dtype, device=dev))
+
+    def run(self, d, **kw):
+        pa.pa_prefix_forward(d["out"], d["q"], d["kc"], d["vc"], d["bt"], d["sl"], d["pt"], d["pl"], d["ps"],
+                             self.scale, self.P, d["ws"], max_seq_len=max(self.own),
+                             max_prefix_len=max(self.prefix), **kw)
+
+    def check(self, calls=2):
+        d = self.device()
+        ref = self.reference()
+        last = None
+        for _ in range(calls):
+            d["out"].fill_(math.nan)
+            self.run(d)
+            assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+            assert_close(d["out"], ref, self.dtype, "shared prefix")
+            assert last is None or torch.equal(last, d["out"])  # no order of anything in the result
+            last = d["out"].clone()
+
+
+DTYPES = [torch.bfloat16, torch.float16]
+ids = lambda v: str(v).replace("torch.", "")  # noqa: E731
+
+
+@pytest.mark.gpu
+def test_one_small_group():
+    Case(1, torch.bfloat16, 8, 1, 128, 16, [2], [128], [5, 20]).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bs", [8, 64])
+def test_lengths(dtype, D, bs):
+    """Prefixes that end inside a page, a stage, a split; own lengths from none."""
+    for P in (1, 63, 64, 65, 127, 128, 129, 300, 1000):
+        Case(P, dtype, 4, 2, D, bs, [3], [P], [0, 1, 40], P=256).check(calls=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("D,G,K,bs", [(64, 16, 1, 16), (128, 8, 2, 16), (256, 4, 2, 32), (128, 1, 4, 8),
+                                      (128, 7, 1, 32), (64, 3, 2, 64), (256, 5, 1, 16)], ids=ids)
+def test_groups(dtype, D, G, K, bs):
+    """Groups of none, one and many sequences, rows beyond one and two tiles."""
+    rng = random.Random(D + G)
+    counts = [3, 0, 1, 40, 0, 20]
+    prefix = [700, 99, 0, 1500, 5, 2049]
+    own = [rng.choice([0, 1, 17, 300, 600]) for _ in range(sum(counts))]
+    Case(D, dtype, G * K, K, D, bs, counts, prefix, own).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_and_splits(D):
+    """More items than SMs: CTAs take several, of different shapes."""
+    rng = random.Random(D)
+    own = [rng.randint(0, 50) for _ in range(150)]
+    Case(D, torch.bfloat16, 16, 2, D, 16, [100, 50], [6001, 9000], own).check()
+
+
+@pytest.mark.gpu
+def test_more_groups_than_lanes():
+    rng = random.Random(3)
+    counts = [rng.choice([0, 1, 2, 3]) for _ in range(70)]
+    prefix = [rng.choice([0, 1, 64, 200, 513]) for _ in counts]
+    Case(3, torch.bfloat16, 4, 1, 128, 16, counts, prefix, [rng.randint(0, 30) for _ in range(sum(counts))]).check()
+
+
+@pytest.mark.gpu
+def test_nothing_at_all_gives_zeros():
+    c = Case(4, torch.bfloat16, 4, 2, 64, 16, [2, 1], [0, 0], [0, 0, 0])
+    d = c.device()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK and (d["out"] == 0).all()
+
+
+@pytest.mark.gpu
+def test_long_prefix():
+    Case(5, torch.bfloat16, 8, 1, 128, 16, [5], [100001], [1, 2, 3, 4, 5]).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rising_maxima(D):
+    """Keys that grow along the prefix: the running maximum is raised, and O
+    rescaled, in most stages; large negative and zero scales too."""
+    c = Case(6, torch.bfloat16, 4, 1, D, 16, [40], [1500], [9] * 40, k_mult=1.0)
+    for j in range(c.pt.shape[1]):
+        c.kc[c.pt[0, j]] *= 0.1 * (1 + j)
+    c.check()
+    Case(7, torch.float16, 4, 1, D, 16, [40], [700], [9] * 40, scale=-0.2).check()
+    Case(8, torch.float16, 4, 1, D, 16, [2], [700], [9] * 2, scale=0.0).check()
+
+
+@pytest.mark.gpu
+def test_equals_the_sequences_with_the_prefix_in_their_tables():
+    """A whole number of prefix pages, put in front of every sequence's own
+    table: pa_v2_forward gives the same within the bar of both."""
+    c = Case(9, torch.bfloat16, 32, 4, 128, 16, [30], [1024], [i * 7 for i in range(30)])
+    d = c.device()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    bt = torch.cat([d["pt"].expand(30, -1), d["bt"]], 1).contiguous()
+    out = torch.empty_like(d["out"])
+    ws = pa.alloc_workspace(30, 32, 128, bt.shape[1] * 16, 512)
+    pa.pa_v2_forward(out, d["q"], d["kc"], d["vc"], bt, d["sl"] + 1024, c.scale, 512, ws)
+    assert_close(d["out"], out.double().cpu().numpy(), c.dtype, "against pa_v2_forward")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["block", "prefix_len", "own_len", "start", "end", "order"])
+def test_bad_data_is_reported(what):
+    """Found by the kernels' own checks before an address is formed; groups that
+    are not concerned are served as usual."""
+    c = Case(10, torch.bfloat16, 4, 1, 128, 16, [2, 3, 1], [300, 200, 100], [5, 50, 0, 7, 20, 1])
+    ref = c.reference()
+    d = c.device()
+    if what == "block":
+        d["pt"][0, 3] = -7
+    elif what == "prefix_len":
+        d["pl"][0] = 301
+    elif what == "own_len":
+        d["sl"][0] = 51
+    elif what == "start":
+        d["ps"][0] = 1
+    elif what == "end":
+        d["ps"][3] = 5
+    else:
+        d["ps"].copy_(torch.tensor([0, 5, 2, 6]))
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_BAD_INPUT
+    if what != "order":
+        assert_close(d["out"][2:5], ref[2:5], c.dtype, "the second group")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_wait_that_runs_out_is_reported(D):
+    """Softmax warps that never come: the bounded waits end, the kernel frees
+    what it holds and reports; the next call on a fresh workspace is right."""
+    c = Case(11, torch.bfloat16, 4, 1, D, 16, [3], [1000], [5, 0, 50])
+    d = c.device()
+    c.run(d, debug_flags=pa.PA_DEBUG_STALL_CONSUMERS, wait_limit_ns=20_000_000)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_TIMEOUT
+    pa.pa_workspace_init(d["ws"])
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    assert_close(d["out"], c.reference(), c.dtype, "after the timeout")
+
+
+@pytest.mark.gpu
+def test_captured_replayed_and_on_another_stream():
+    c = Case(12, torch.bfloat16, 16, 2, 128, 16, [4, 9], [777, 1300], [3 * i for i in range(13)])
+    d = c.device(poison=False)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.run(d, stream=s)
+    s.synchronize()
+    assert_close(d["out"], c.reference(), c.dtype, "another stream")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(d)
+    for prefix, own, start in (([777, 1300], c.own, [0, 4, 13]), ([5, 1299], [0] * 13, [0, 13, 13]),
+                               ([640, 0], [i for i in range(13)], [0, 0, 13])):
+        c.prefix, c.own, c.start = prefix, own, start
+        d["pl"].copy_(torch.tensor(prefix))
+        d["sl"].copy_(torch.tensor(own))
+        d["ps"].copy_(torch.tensor(start))
+        for _ in range(2):
+            d["out"].fill_(math.nan)
+            g.replay()
+            assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+            assert_close(d["out"], c.reference(), c.dtype, f"replay {prefix} {start}")
