@@ -57,21 +57,65 @@ struct PrefixShape {
   static constexpr int QPANEL = kTileRows * 128;
   static constexpr int QTILE = PANELS * QPANEL;
   static constexpr int SOFTMAX_WARPS = 4 * NT;
-  static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
-  // full and empty of each slot, Q ready a tile, S and P ready a buffer, O
-  // done a tile, PV done (NT 1), drain, never
-  static constexpr int BARS = 2 * SLOTS + 2 + 2 + 2 + 2 + 3;
+  // NT 2: a third warpgroup (two idle warps) whose registers the softmax
+  // warps take over: a row's 128 scores stay in registers
+  static constexpr int THREADS = (SOFTMAX_WARPS + (NT == 2 ? 4 : 2)) * 32;
+  // full and empty of each slot, Q ready a tile, S, P and (NT 2) half of P
+  // ready a buffer, O done a tile, PV done (NT 1), drain, never
+  static constexpr int BARS = 2 * SLOTS + 2 + 2 + 2 + 2 + 2 + 3;
   static constexpr size_t SMEM = (size_t)NT * QTILE + (size_t)SLOTS * SLOT + BARS * 8 + 16;
 };
 
-// D = A . B (+ D), A from tensor memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+// 1 in one lane of the warp, the same each time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+// D = A . B (+ D) in the lane with `on`, A from shared or from tensor memory.
+__device__ __forceinline__ void tc_mma_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+// pairs of floats, one instruction for both
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 // eight floats in one store (32-byte aligned)
 __device__ __forceinline__ void store8(float *dst, const float (&v)[8]) {
@@ -192,7 +236,8 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
   const uint32_t q_u32 = smem_u32(qbuf), ring_u32 = smem_u32(ring);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * NS, q_full = empty0 + 8 * NS,
                  s_full = q_full + 16, p_full = s_full + 16, o_done = p_full + 16,
-                 pv_done = o_done + 16, drain = pv_done + 8, never = drain + 8;
+                 p_half = o_done + 16,
+                 pv_done = p_half + 16, drain = pv_done + 8, never = drain + 8;
   const uint64_t limit = p.wait_limit_ns;
 
   if (threadIdx.x == 0) {
@@ -204,6 +249,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
       mbar_init(q_full + 8 * i, 4);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
+      mbar_init(p_half + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
     }
     mbar_init(pv_done, 1);
@@ -228,6 +274,9 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
   ItemWalk<NT * kTileRows> walk;
   PrefixItem it;
 
+  // NT 2: 3 warpgroups at 168 registers, 2 x 208 + 80 <= 3 x 168
+  if (warp >= Z::SOFTMAX_WARPS) {
+  if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == Z::SOFTMAX_WARPS) {
     // ======================= producer warp =======================
     if (lane == 0) {
@@ -305,125 +354,143 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
         mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, kDrainLimitNs, nullptr);
     __syncwarp();
   } else if (warp == Z::SOFTMAX_WARPS + 1) {
-    // ======================= MMA warp (one thread issues) =======================
+    // ======================= MMA warp =======================
+    // The whole warp runs the loop, so that descriptors and control stay in
+    // uniform registers; one elected lane issues.
+    const uint32_t leader = elect_one();
     bool ok = true;
-    int op = 0;                 // slots consumed so far: K of the next stage
+    int sk = 0, par = 0;        // ring slot of the next stage's K, its phase
     int items[2] = {0, 0};      // items of each tile
     int done[2] = {0, 0};       // stages of each tile (NT 1: [0], over both buffers)
+    // The tile and ring descriptors' constant parts; a k-step adds to the
+    // address field (16-byte units) only.
+    const uint64_t q_desc = smem_desc(q_u32, 16, 1024);
+    const uint64_t k_desc = smem_desc(ring_u32, 16, Z::GROUP);
+    const uint64_t v_desc = smem_desc(ring_u32, 1024, Z::GROUP);
+    auto wait_slot = [&](int sl, int ph) -> bool {
+      return mbar_wait(full0 + 8 * sl, (uint32_t)ph, limit, flags);
+    };
+    auto advance = [&](int &sl, int &ph) {
+      if (++sl == NS) {
+        sl = 0;
+        ph ^= 1;
+      }
+    };
+    // S = Q K^T: D / 16 k-steps of 32 bytes inside a panel
+    auto issue_s = [&](int sl, int t, int buf) {
+      const uint64_t db0 = k_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
+      const uint64_t da0 = q_desc + (uint32_t)t * (uint32_t)(Z::QTILE >> 4);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        tc_mma_if(leader, tmem + 128u * (uint32_t)buf,
+                  da0 + (uint32_t)(((ks >> 2) * Z::QPANEL + (ks & 3) * 32) >> 4),
+                  db0 + (uint32_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
+      tc_commit_if(leader, s_full + 8u * (uint32_t)buf);
+    };
+    // O += P V: k-steps of 16 keys; P two keys a column, V MN-major
+    auto issue_pv = [&](int sl, int t, int buf, bool first, int k0, int k1) {
+      const uint64_t db0 = v_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
+#pragma unroll
+      for (int kk = k0; kk < k1; ++kk)
+        tc_mma_ts_if(leader, tmem_o + (uint32_t)(t * D), tmem + 128u * (uint32_t)buf + 8u * (uint32_t)kk,
+                     db0 + (uint32_t)((kk * 2 * Z::GROUP) >> 4), kIdescPV, first && kk == 0 ? 0u : 1u);
+    };
     for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
       const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
       const int nt = (it.rows + kTileRows - 1) / kTileRows;
-      if (lane == 0) {
-        auto wait_slot = [&](int o) -> bool {
-          return mbar_wait(full0 + 8 * (o % NS), (o / NS) & 1, limit, flags);
-        };
-        // S = Q K^T: D / 16 k-steps of 32 bytes inside a panel
-        auto issue_s = [&](int o, int t, int buf) {
-          const uint32_t kst = ring_u32 + (uint32_t)(o % NS) * Z::SLOT;
-          const uint32_t qt = q_u32 + (uint32_t)t * Z::QTILE;
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (uint32_t)(ks & 3) * 32u;
-            const uint64_t da = smem_desc(qt + (uint32_t)(ks >> 2) * Z::QPANEL + off, 16, 1024);
-            const uint64_t db = smem_desc(kst + (uint32_t)(ks >> 2) * 1024u + off, 16, Z::GROUP);
-            tc_mma(tmem + 128u * (uint32_t)buf, da, db, kIdescS, ks > 0 ? 1u : 0u);
-          }
-          tc_commit(s_full + 8u * (uint32_t)buf);
-        };
-        // O += P V: k-steps of 16 keys; P two keys a column, V MN-major
-        auto issue_pv = [&](int o, int t, int buf, bool first) {
-          const uint32_t vst = ring_u32 + (uint32_t)(o % NS) * Z::SLOT;
-#pragma unroll
-          for (int kk = 0; kk < KEYS / 16; ++kk) {
-            const uint64_t db = smem_desc(vst + (uint32_t)kk * 2u * Z::GROUP, 1024, Z::GROUP);
-            tc_mma_ts(tmem_o + (uint32_t)(t * D), tmem + 128u * (uint32_t)buf + 8u * (uint32_t)kk, db,
-                      kIdescPV, first && kk == 0 ? 0u : 1u);
-          }
-        };
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (ok && t < nt) ok = mbar_wait(q_full + 8 * t, items[t] & 1, limit, flags);
-        if (ok) ok = wait_slot(op);
-        if (ok) {
-          tc_fence_after();
-          if constexpr (NT == 2) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (t < nt) issue_s(op, t, t);
-          } else {
-            issue_s(op, 0, done[0] & 1);
-          }
-          tc_commit(empty0 + 8 * (op % NS));
+      for (int t = 0; t < NT; ++t)
+        if (ok && t < nt) ok = mbar_wait(q_full + 8 * t, items[t] & 1, limit, flags);
+      if (ok) ok = wait_slot(sk, par);
+      if (ok) {
+        tc_fence_after();
+        if constexpr (NT == 2) {
+          issue_s(sk, 0, 0);
+          if (nt == 2) issue_s(sk, 1, 1);
+        } else {
+          issue_s(sk, 0, done[0] & 1);
         }
-        for (int j = 0; ok && j < stages; ++j) {
-          const int ok_k = op + 2 * j, ov = ok_k + 1, nk = ok_k + 2;  // K, V, the next K
-          const bool more = j + 1 < stages;
-          if constexpr (NT == 2) {
+        tc_commit_if(leader, empty0 + 8 * sk);
+      }
+      for (int j = 0; ok && j < stages; ++j) {
+        const bool more = j + 1 < stages;
+        int sv = sk, pv = par;  // V's slot, then the next K's
+        advance(sv, pv);
+        int sn = sv, pn = pv;
+        advance(sn, pn);
+        sk = sn;
+        par = pn;
+        if constexpr (NT == 2) {
+          // this V and the next K are in long before P, as a rule: awaited
+          // first, they cost nothing between P and its MMAs
+          ok = wait_slot(sv, pv) && (!more || wait_slot(sn, pn));
+          if (!ok) break;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (t >= nt) break;
-              ok = mbar_wait(p_full + 8 * t, done[t] & 1, limit, flags);
-              if (ok && t == 0) ok = wait_slot(ov);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(ov, t, t, j == 0);
-              if (t == nt - 1) tc_commit(empty0 + 8 * (ov % NS));
-              if (more) {
-                if (t == 0) {
-                  ok = wait_slot(nk);
-                  if (!ok) break;
-                  tc_fence_after();
-                }
-                issue_s(nk, t, t);
-                if (t == nt - 1) tc_commit(empty0 + 8 * (nk % NS));
-              } else {
-                tc_commit(o_done + 8 * t);
-              }
-              ++done[t];
-            }
-          } else {
-            const int b = done[0] & 1;
-            if (more) {
-              ok = wait_slot(nk);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(nk, 0, b ^ 1);
-              tc_commit(empty0 + 8 * (nk % NS));
-            }
-            ok = mbar_wait(p_full + 8 * b, (done[0] >> 1) & 1, limit, flags) && wait_slot(ov);
+          for (int t = 0; t < 2; ++t) {
+            if (t >= nt) break;
+            ok = mbar_wait(p_half + 8 * t, done[t] & 1, limit, flags);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(ov, 0, b, j == 0);
-            tc_commit(empty0 + 8 * (ov % NS));
-            tc_commit(pv_done);
-            if (!more) tc_commit(o_done);
-            ++done[0];
+            issue_pv(sv, t, t, j == 0, 0, KEYS / 32);
+            ok = mbar_wait(p_full + 8 * t, done[t] & 1, limit, flags);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(sv, t, t, false, KEYS / 32, KEYS / 16);
+            if (t == nt - 1) tc_commit_if(leader, empty0 + 8 * sv);
+            if (more) {
+              issue_s(sn, t, t);
+              if (t == nt - 1) tc_commit_if(leader, empty0 + 8 * sn);
+            } else {
+              tc_commit_if(leader, o_done + 8 * t);
+            }
+            ++done[t];
           }
+        } else {
+          const int b = done[0] & 1;
+          if (more) {
+            ok = wait_slot(sn, pn);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(sn, 0, b ^ 1);
+            tc_commit_if(leader, empty0 + 8 * sn);
+          }
+          ok = mbar_wait(p_full + 8 * b, (done[0] >> 1) & 1, limit, flags) && wait_slot(sv, pv);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(sv, 0, b, j == 0, 0, KEYS / 16);
+          tc_commit_if(leader, empty0 + 8 * sv);
+          tc_commit_if(leader, pv_done);
+          if (!more) tc_commit_if(leader, o_done);
+          ++done[0];
         }
-        op += 2 * stages;
+      }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) items[t] += t < nt;
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int t = 0; t < NT; ++t) items[t] += t < nt;
+      ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0) {  // nothing may still run when the memory is freed
-      tc_commit(drain);
-      mbar_wait(drain, 0, kDrainLimitNs, nullptr);
-      if (!ok) {
-        report(p.status, kStatusTimeout);
-        flags[0] = 1;
-      }
+    // nothing may still run when the memory is freed
+    tc_commit_if(leader, drain);
+    mbar_wait(drain, 0, kDrainLimitNs, nullptr);
+    if (!ok && lane == 0) {
+      report(p.status, kStatusTimeout);
+      flags[0] = 1;
     }
     __syncwarp();
+  }
   } else {
     // ======================= softmax warps: thread = row =======================
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2;               // the tile
     const int r = threadIdx.x & 127;       // row of the tile, and tensor-memory lane
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t my_o = tmem_o + (uint32_t)(t * D) + lane_off;
     uint8_t *qt = qbuf + t * Z::QTILE;
-    const float sc = fabsf(p.scale_log2);
-    const bool neg = p.scale_log2 < 0.f;
+    // a negative scale's sign goes into the queries, and a zero scale is zero
+    // queries, so that the largest product is always the largest logit and a
+    // masked product of -inf always a weight of zero
+    const float sc = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    const uint32_t q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const uint32_t q_keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
     bool ok = true;
     int done = 0, items = 0, ops = 0;
     if (p.debug_flags & kPrefixDebugStall) {
@@ -444,12 +511,26 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
       const int seq = it.seq0 + (live ? gr / p.group : 0);
       const int head = it.kvh * p.group + (live ? gr % p.group : 0);
       const size_t orow = (size_t)seq * p.num_heads + head;
-      {  // the row's query into the swizzled tile (zeros past the item's rows)
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) + orow * D);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4 *>(qt + (c >> 3) * Z::QPANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      {  // the warp's 32 queries into the swizzled tile (zeros past the item's
+         // rows), lanes along a row
+        constexpr int CPR = D / 8;        // 16-byte pieces of a row
+        constexpr int RPI = CPR < 32 ? 32 / CPR : 1;
+        const int c = lane % CPR;
+        int rr = 32 * (warp & 3) + lane / CPR;  // row of the tile
+        int qseq = (it.row0 + t * kTileRows + rr) / p.group;
+        int qhead = it.row0 + t * kTileRows + rr - qseq * p.group;
+        const uint4 *src = static_cast<const uint4 *>(p.query) + c;
+        // (a short loop: code that runs once an item costs its fetch)
+#pragma unroll 4
+        for (int i = 0; i < 32; i += RPI) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < rows)
+            v = __ldg(src + ((size_t)(it.seq0 + qseq) * p.num_heads + it.kvh * p.group + qhead) * CPR);
+          v = make_uint4((v.x ^ q_flip) & q_keep, (v.y ^ q_flip) & q_keep, (v.z ^ q_flip) & q_keep,
+                         (v.w ^ q_flip) & q_keep);
+          *reinterpret_cast<uint4 *>(qt + (c >> 3) * Z::QPANEL + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
+          rr += RPI;
+          for (qhead += RPI; qhead >= p.group; qhead -= p.group) ++qseq;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -479,28 +560,38 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
           fence_proxy_async_smem();
         }
         if (warp_live) {
+          // the scores, the second half in flight behind the first's maximum
           uint32_t s[KEYS / 32][32];
-#pragma unroll
-          for (int c = 0; c < KEYS / 32; ++c) tmem_ld32(sbuf + 32 * c, s[c]);
-#pragma unroll
-          for (int c = 0; c < KEYS / 32; ++c) tmem_ld_wait(s[c]);
           auto x = [&](int k) -> float { return __uint_as_float(s[k >> 5][k & 31]); };
-          if (neg) {  // a negative scale: the largest logit has the smallest product
-#pragma unroll
-            for (int k = 0; k < KEYS; ++k) s[k >> 5][k & 31] ^= 0x80000000u;
-          }
-          if (valid < KEYS) {  // (no infinities: their P is set to zero below)
-#pragma unroll
-            for (int k = 1; k < KEYS; ++k)
-              if (k >= valid) s[k >> 5][k & 31] = s[0][0];
-          }
           float m8[8];
+          auto row_max = [&](int c) {
+            if (valid < KEYS) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            m8[i] = x(i);
+              for (int k = 0; k < 32; ++k)
+                if (32 * c + k >= valid) s[c][k] = 0xff800000u;  // -inf
+            }
 #pragma unroll
-            for (int k = i + 8; k + 8 < KEYS; k += 16) m8[i] = fmax3(m8[i], x(k), x(k + 8));
-            m8[i] = fmaxf(m8[i], x(KEYS - 8 + i));
+            for (int i = 0; i < 8; ++i) {
+              const int k = 32 * c + i;
+              m8[i] = c == 0 ? fmaxf(fmax3(x(k), x(k + 8), x(k + 16)), x(k + 24))
+                             : fmax3(fmax3(m8[i], x(k), x(k + 8)), x(k + 16), x(k + 24));
+            }
+          };
+          tmem_ld32(sbuf, s[0]);
+          tmem_ld32(sbuf + 32, s[1]);
+          tmem_ld_wait(s[0]);
+          tmem_ld_wait(s[1]);
+          if constexpr (KEYS == 128) {
+            tmem_ld32(sbuf + 64, s[2]);
+            tmem_ld32(sbuf + 96, s[3]);
+          }
+          row_max(0);
+          row_max(1);
+          if constexpr (KEYS == 128) {
+            tmem_ld_wait(s[2]);
+            tmem_ld_wait(s[3]);
+            row_max(2);
+            row_max(3);
           }
           const float mt = sc * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
                                       fmaxf(m8[6], m8[7]));
@@ -527,25 +618,37 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
             tmem_st_wait();
           }
           const float mb = m_run == -CUDART_INF_F ? 0.f : -m_run;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pair(sc, sc), mb2 = pair(mb, mb);
+          uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+          // P over the scores' own registers (word e holds keys 2e, 2e + 1), so
+          // that no register waits for a store in flight
+          auto weights = [&](int h, int e0, int e1) {
 #pragma unroll
-          for (int c = 0; c < KEYS / 32; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int k = 32 * c + 2 * e;
-              float p0 = ex2(fmaf(x(k), sc, mb)), p1 = ex2(fmaf(x(k + 1), sc, mb));
-              if (valid < KEYS) {
-                p0 = k < valid ? p0 : 0.f;
-                p1 = k + 1 < valid ? p1 : 0.f;
-              }
-              l4[e & 3] += p0 + p1;
-              w[e] = MmaOp<T>::pack(p0, p1);
+            for (int e = e0; e < e1; ++e) {
+              const int k = 64 * h + 2 * e;
+              const float2 y = unpair(fma2(pair(x(k), x(k + 1)), sc2, mb2));
+              const float p0 = ex2(y.x), p1 = ex2(y.y);
+              l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
+              s[h][e] = MmaOp<T>::pack(p0, p1);
             }
-            tmem_st16(sbuf + 16 * c, w);
+          };
+          weights(0, 0, 32);
+          tmem_st32(sbuf, s[0]);
+          if constexpr (KEYS == 128) {
+            // the first 64 keys' PV may begin; by now their store has landed
+            weights(1, 0, 8);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_half + 8 * buf);
+            weights(1, 8, 32);
+            tmem_st32(sbuf + 32, s[1]);
           }
-          l = l * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+          const float2 ls = unpair(add2(l2[0], l2[1]));
+          l = fmaf(l, alpha, ls.x + ls.y);
           tmem_st_wait();
+        } else if (NT == 2) {
+          if (lane == 0) mbar_arrive(p_half + 8 * buf);
         }
         tc_fence_before();
         __syncwarp();
