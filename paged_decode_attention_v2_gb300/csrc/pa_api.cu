@@ -688,6 +688,7 @@ pa_status_t launch(const Call &c, bool v2, const pa_options_t &opt) {
   }
   p.num_stages = stages;
   p.debug_flags = opt.debug_flags;
+  p.late_wait = c.extra_parts > 0 && !k.umma;  // behind the prefix kernel
   p.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
   p.wait_limit_ns = opt.wait_limit_ns ? opt.wait_limit_ns : kDefaultWaitLimitNs;
 
@@ -1119,8 +1120,8 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, 
       (head_size != 64 && head_size != 128 && head_size != 256))
     return 0;
   int split = 0, splits = 0;
-  prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_prefix_len, &split,
-              &splits);
+  prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
+              max_prefix_len, partition_size, &split, &splits);
   const long long parts = (long long)max_parts_of(max_seq_len, partition_size) + splits;
   if (parts > kMaxReduceParts || parts * partition_size > INT_MAX - partition_size) return 0;
   return pa_workspace_bytes(num_seqs, num_heads, head_size, (int)parts * partition_size,
@@ -1159,10 +1160,11 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   pa_status_t st = check_args(c, true);
   if (st != PA_OK) return st;
   if (dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;  // tensor path only
+  if ((long long)num_seqs * (num_heads / num_kv_heads) >= (1ll << 28)) return PA_ERR_UNSUPPORTED;
   if (opt.math == PA_MATH_SIMT) return PA_ERR_UNSUPPORTED;
   int split = 0, splits = 0;
-  prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_prefix_len, &split,
-              &splits);
+  prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
+              max_prefix_len, partition_size, &split, &splits);
   const size_t need = pa_prefix_workspace_bytes(num_seqs, num_prefixes, num_heads, num_kv_heads,
                                                 head_size, max_seq_len, max_prefix_len,
                                                 partition_size);
@@ -1218,6 +1220,7 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   p.max_seq_len = max_seq_len;
   p.partition_size = partition_size;
   p.max_parts = max_parts_of(layout_len(c), partition_size);
+  p.group_magic = ((1ull << 36) + p.group - 1) / p.group;
   p.split_tokens = split;
   p.debug_flags = opt.debug_flags;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);

@@ -809,7 +809,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) __maxnreg__((attn_max_regs<M
   // only shared memory; wait here until the previous kernel in the stream has
   // finished and its writes are visible (it may have produced the queries or
   // the cache, or still be reading what this kernel writes).
-  pdl_wait_primary();
+  if (!p.late_wait) pdl_wait_primary();
 
   const StageGeom geom{p.log2_unit_rows, p.unit_rows - 1, (uint32_t)p.unit_rows * kPanelBytes,
                        (uint32_t)(NPANELS * p.unit_rows * kPanelBytes)};
@@ -1364,6 +1364,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) __maxnreg__((attn_max_regs<M
       }
     }
   }
+  // (one CTA holds the grid open; the others leave, so that CTAs not yet
+  // placed find room)
+  if (p.late_wait && blockIdx.x == 0) pdl_wait_primary();
 }
 
 template <typename T, int D, int NW, int GMAX, class Math, bool SIMT>

@@ -50,6 +50,11 @@ struct AttnParams {
   int num_stages;
   int cluster;        // tcgen05 chunk kernel: CTAs of a thread-block cluster (1: none)
   int debug_flags;
+  // 1: the kernel before this one in the stream (the prefix kernel of the same
+  // call) writes nothing that this one reads, and started only after all that
+  // came before it was complete: wait for it at the end instead of the start,
+  // so that both run at once and Phase 2 still finds both complete.
+  int late_wait;
   float scale_log2;   // scale * log2(e)
   uint64_t wait_limit_ns;
 };

@@ -49,6 +49,7 @@ struct PrefixParams {
   int num_seqs, num_prefixes, num_heads, num_kv_heads, group, num_blocks;
   int block_size, log2_block_size, max_prefix_blocks, max_prefix_len;
   int max_seq_len, partition_size, max_parts;
+  uint64_t group_magic;  // ceil(2^36 / group): x / group for x < 2^28 is x * it >> 36
   int split_tokens;  // keys of a split, a multiple of the kernel's stage
   int debug_flags;
   float scale_log2;  // scale * log2(e)
@@ -64,7 +65,8 @@ struct PrefixKernelInfo {
 };
 PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size);
 void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
-                 int max_prefix_len, int *split_tokens, int *max_splits);
+                 int max_seq_len, int max_prefix_len, int partition_size, int *split_tokens,
+                 int *max_splits);
 
 struct SelectParams {
   const void *query;       // [rows][H][D]

@@ -258,6 +258,20 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
     flags[0] = 0;
     fence_mbar_init();
   }
+  // What the items' first loads need (the lists, tables and queries, as if one
+  // line of them a thread), on its way to L2 while the kernel before this one
+  // ends
+  {
+    const long long i = (long long)blockIdx.x * Z::THREADS + threadIdx.x;
+    const auto fetch = [&](const void *base, long long bytes) {
+      if (i * 128 < bytes) prefetch_l2(static_cast<const char *>(base) + i * 128);
+    };
+    fetch(p.prefix_start, 4ll * (p.num_prefixes + 1));
+    fetch(p.prefix_lens, 4ll * p.num_prefixes);
+    fetch(p.seq_lens, 4ll * p.num_seqs);
+    fetch(p.prefix_tables, 4ll * p.num_prefixes * p.max_prefix_blocks);
+    fetch(p.query, (long long)p.num_seqs * p.num_heads * D * 2);
+  }
   // wait for the kernel before in the stream, also before taking tensor
   // memory that a CTA of it may still hold
   pdl_wait_primary();
@@ -508,29 +522,39 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
       const int gr = it.row0 + t * kTileRows + r;  // row of the group
       const bool live = r < rows;
       const bool warp_live = 32 * (warp & 3) < rows;
-      const int seq = it.seq0 + (live ? gr / p.group : 0);
-      const int head = it.kvh * p.group + (live ? gr % p.group : 0);
+      const int sq = (int)(((uint64_t)(uint32_t)gr * p.group_magic) >> 36);  // gr / group
+      const int seq = it.seq0 + (live ? sq : 0);
+      const int head = it.kvh * p.group + (live ? gr - sq * p.group : 0);
       const size_t orow = (size_t)seq * p.num_heads + head;
       {  // the warp's 32 queries into the swizzled tile (zeros past the item's
          // rows), lanes along a row
         constexpr int CPR = D / 8;        // 16-byte pieces of a row
         constexpr int RPI = CPR < 32 ? 32 / CPR : 1;
         const int c = lane % CPR;
-        int rr = 32 * (warp & 3) + lane / CPR;  // row of the tile
-        int qseq = (it.row0 + t * kTileRows + rr) / p.group;
-        int qhead = it.row0 + t * kTileRows + rr - qseq * p.group;
         const uint4 *src = static_cast<const uint4 *>(p.query) + c;
-        // (a short loop: code that runs once an item costs its fetch)
-#pragma unroll 4
-        for (int i = 0; i < 32; i += RPI) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < rows)
-            v = __ldg(src + ((size_t)(it.seq0 + qseq) * p.num_heads + it.kvh * p.group + qhead) * CPR);
-          v = make_uint4((v.x ^ q_flip) & q_keep, (v.y ^ q_flip) & q_keep, (v.z ^ q_flip) & q_keep,
-                         (v.w ^ q_flip) & q_keep);
-          *reinterpret_cast<uint4 *>(qt + (c >> 3) * Z::QPANEL + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
-          rr += RPI;
-          for (qhead += RPI; qhead >= p.group; qhead -= p.group) ++qseq;
+        // eight loads in flight a lane, in a short loop: code that runs once
+        // an item costs its fetch
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 8 * RPI) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 32 * (warp & 3) + i0 + i * RPI + lane / CPR;  // row of the tile
+            const int g = it.row0 + t * kTileRows + rr;
+            const int sq = (int)(((uint64_t)(uint32_t)g * p.group_magic) >> 36);  // g / group
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < rows)
+              v[i] = __ldg(src + ((size_t)(it.seq0 + sq) * p.num_heads + it.kvh * p.group +
+                                  (g - sq * p.group)) * CPR);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 32 * (warp & 3) + i0 + i * RPI + lane / CPR;
+            v[i] = make_uint4((v[i].x ^ q_flip) & q_keep, (v[i].y ^ q_flip) & q_keep,
+                              (v[i].z ^ q_flip) & q_keep, (v[i].w ^ q_flip) & q_keep);
+            *reinterpret_cast<uint4 *>(qt + (c >> 3) * Z::QPANEL + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+                v[i];
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -722,29 +746,51 @@ PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size) {
   return dtype_bf16 ? pick<__nv_bfloat16>(head_size) : pick<__half>(head_size);
 }
 
-// Splits of the prefix.  One wave of items should fill the SMs, with as few
-// splits as that takes: each is another partial of every row to write and
-// read back.  The cost counted here, in stages of an item's keys: the waves
-// times (an item's stages, and its start-up and epilogue, about four), plus
-// the partials' bytes.  The sizes of the groups are not known on the host:
-// rows are counted as if packed, with at least one tile a group.
+// Splits of the prefix, from a model of the call's time in microseconds
+// (coefficients measured on GB300; the sizes of the groups are not known on
+// the host, so a row tile is counted as half empty a group, and own lengths as
+// half their bound):
+//   - the prefix kernel: waves of items on 152 SMs, each an item's stages at
+//     the tensor cores' pace or that of the keys' bytes, plus 10 us an item
+//     (start, queries, epilogue);
+//   - the own tokens run on the SMs left free meanwhile, 40 GB/s each, and
+//     the rest of them after it at 5.7 TB/s, which costs 5 us more if
+//     anything is left: so it pays to leave SMs free (8 sequences behind
+//     100,000 tokens: 37 splits, 148 items, 50.4 us, against 38 splits, 152
+//     items, 53.6 us; 256 behind 8192 with 264 of their own: 3 splits, 96
+//     items, 62.9 us, against 4 splits, 128 items, 68.6 us and 2 splits, 64
+//     items, 70.6 us);
+//   - Phase 2: every split is another partial of every row.
 void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
-                 int max_prefix_len, int *split_tokens, int *max_splits) {
+                 int max_seq_len, int max_prefix_len, int partition_size, int *split_tokens,
+                 int *max_splits) {
   constexpr int kSms = 152;
   const PrefixKernelInfo k = prefix_kernel(1, head_size);
-  const long long rows = (long long)num_seqs * (num_heads / num_kv_heads);
-  long long tiles = (rows + k.tile_rows - 1) / k.tile_rows;
-  const long long groups = num_prefixes < num_seqs ? num_prefixes : num_seqs;
+  const double rows = (double)num_seqs * (num_heads / num_kv_heads);
+  const int groups = num_prefixes < num_seqs ? num_prefixes : (num_seqs > 0 ? num_seqs : 1);
+  const long long packed = (long long)((rows + k.tile_rows - 1) / k.tile_rows);
+  long long tiles = packed + (groups > 1 ? groups / 2 : 0);
   if (tiles < groups) tiles = groups;
+  if (tiles < 1) tiles = 1;
   const long long heads = tiles * num_kv_heads;
   const int stages = (max_prefix_len + k.stage_keys - 1) / k.stage_keys;
+  const double pace = head_size == 64 ? 0.9 : head_size == 128 ? 1.4 : 0.65;
+  const double stage_us = (double)k.stage_keys * head_size * 4. / 6.3e6;  // of its bytes alone
+  const double own_mb = (double)num_seqs * max_seq_len * 0.5 * num_kv_heads * head_size * 4e-6;
+  const double own_parts = 0.7 * ((max_seq_len + partition_size - 1) / partition_size);
   int best = 1;
   double best_cost = 0.;
-  for (int n = 1; n <= kMaxPrefixSplits && n <= (stages > 0 ? stages : 1); ++n) {
+  for (int n = 1; n <= kMaxPrefixSplits && (n == 1 || n <= stages); ++n) {
     const int per = (stages + n - 1) / n;
-    const long long waves = (heads * n + kSms - 1) / kSms;
-    // a stage takes about 1 us on every SM; partials 2 x 4 D bytes a row at 6 TB/s
-    const double cost = (double)waves * (per + 4) + (double)rows * num_kv_heads * n * head_size * 8. / 6e6;
+    const long long items = heads * (per > 0 ? (stages + per - 1) / per : 1);
+    const long long waves = (items + kSms - 1) / kSms;
+    const long long active = items < kSms ? items : kSms;
+    const double bytes_pace = (double)active * groups / tiles * stage_us;
+    const double t = waves * (per * (bytes_pace > pace ? bytes_pace : pace) + 10.);
+    const double shadow_mb = waves == 1 ? t * (kSms - active) * 0.04 : 0.;
+    const double left_mb = own_mb - shadow_mb;
+    const double cost = t + (left_mb > 0. ? 5. + left_mb / 5.7 : 0.) +
+                        (double)num_seqs * num_heads * (n + own_parts) * head_size * 4. / 3e6;
     if (n == 1 || cost < best_cost) {
       best = n;
       best_cost = cost;
