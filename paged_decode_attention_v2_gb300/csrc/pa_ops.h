@@ -76,15 +76,15 @@ struct SelectParams {
   const int32_t *given;    // a given selection instead
   int32_t *table, *lens;   // the view's block table and lengths, or null
   int *counters;           // [rows * Hkv] finished chunks, zero between calls
-  float *amax;             // [rows * Hkv][chunks] largest bound seen
-  float *scores;           // [rows * Hkv][max_pages]
-  double *fine;            // [rows * Hkv][max_pages]
+  float *sizes;            // [rows * Hkv][chunks] largest sum of magnitudes
+  uint32_t *keys;          // [rows * Hkv][max_pages] scores as ordered integers
+  double *fine;            // [rows * Hkv][max_pages] scores in fp64, where needed
   int *status;
   int num_seqs, num_rows, num_heads, num_kv_heads, num_blocks;
   int block_size, log2_block_size, max_blocks_per_seq, max_seq_len, max_pages;
   int num_selected, sinks, recent;
   int chunks, chunk_pages;  // CTAs of an item, pages of each
-  int smem_pages;           // scores that the shared memory holds
+  int smem_pages;           // keys that the shared memory holds
 };
 
 }  // namespace pa

@@ -10,14 +10,14 @@
 // whatever the group's size: the bounds are read once a row.
 //
 // Which block is read must not hang on a rounding, so the selection is the
-// one that exact scores give (ties to the lower page).  Scores in fp32 are
-// within eps of the exact ones, eps = 48 2^-24 W A, with W = sum |Q| and A the
-// largest bound: Q has up to 15 additions of one sign (relative error 15
-// 2^-24), a lane's chain up to 16 products, the warp's sum 5 more, and 48 >
-// 15 + 16 + 5 + 1 leaves room for W and A themselves.  A page more than 2 eps
-// above the k-th largest fp32 score is in, one more than 2 eps below is out;
-// the few between are scored again in fp64, where products of 16-bit numbers
-// are exact.
+// one that exact scores give (ties to the lower page).  A score in fp32 is
+// within eps = gamma 2^-24 sum |Q| |bound| of the exact one: gamma counts the
+// G - 1 additions in Q (all of one sign), a lane's chain of products, the
+// warp's 5 additions and 3 for the sum of magnitudes itself, which is taken
+// as the sum over lanes of the largest a lane saw on any page.  Where the
+// scores on the two sides of the cut are more than 2 eps apart, the cut is
+// the exact one.  Else the pages within 2 eps of the last one in are scored
+// again in fp64, where products of 16-bit numbers are exact.
 //
 // Layout of the work: an item is one (row, KV head); its pages are cut into
 // chunks, one CTA each, so that a single long sequence fills the GPU; the CTA
@@ -38,12 +38,10 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 512;       // of the score histogram, two a thread
-constexpr int kSelList = 256;       // pages scored again in shared memory
-constexpr int kSelSegment = 8;      // pages of a warp at a time
-constexpr int kSelSmemPages = 8192; // scores kept in shared memory
+constexpr int kSelMaxWarps = 8;     // of a CTA
+constexpr int kSelList = 256;       // pages listed in shared memory
+constexpr int kSelWarpPages = 256;  // candidates that one warp selects from, eight a lane
+constexpr int kSelSmemPages = 8192; // keys kept in shared memory
 
 template <typename T>
 __device__ __forceinline__ void widen(const uint4 &c, float (&f)[16 / sizeof(T)]) {
@@ -103,69 +101,295 @@ __device__ __forceinline__ void locate(const SelectParams &p, int row, int &seq,
   if (!p.q_start) vis = L;
 }
 
+// An order-preserving map of floats (no NaN) to unsigned integers and back.
+__device__ __forceinline__ uint32_t order32(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unorder32(uint32_t u) {
+  return __uint_as_float((u >> 31) ? u ^ 0x80000000u : ~u);
+}
+
+// Marks of pages whose order fp64 decided, outside the range of any float.
+constexpr uint32_t kKeyIn = 0xffffffffu, kKeyOut = 0u;
+
 struct SelShared {
-  double w[512];  // Q+ then Q-, 2 D numbers
+  float w[512];           // Q+ then Q-, 2 D numbers
+  double wide[512];       // the same in fp64, where it is needed
   double fine[kSelList];
   int list[kSelList];
-  int hist[kSelBins];
-  float red_f[2 * kSelWarps];
-  int red_i[kSelWarps];
-  int bin, above, flag, count;
+  uint32_t mark[kSelList];
+  int counts[32 * kSelMaxWarps];
+  int red_i[2][kSelMaxWarps];
+  uint32_t red_u[2][kSelMaxWarps];
+  float red_f[kSelMaxWarps];
+  int flag, count;
 };
 
-// Sum (or maximum) over the CTA; every thread gets it.
-__device__ __forceinline__ int block_sum(int v, int *red) {
+// Sum over the CTA, for every thread.  `turn` alternates between calls, so
+// that one barrier a call suffices.
+template <int WARPS>
+__device__ __forceinline__ int block_sum(int v, SelShared &sh, int &turn) {
   v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) sh.red_i[turn][threadIdx.x >> 5] = v;
   __syncthreads();
   int t = 0;
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) t += red[i];
+  for (int i = 0; i < WARPS; ++i) t += sh.red_i[turn][i];
   return t;
 }
-__device__ __forceinline__ void block_min_max(float &lo, float &hi, float *red) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-  }
+// The smallest lo and the largest hi over the CTA, for every thread.
+template <int WARPS>
+__device__ __forceinline__ void block_min_max(uint32_t &lo, uint32_t &hi, SelShared &sh) {
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) {
-    red[threadIdx.x >> 5] = lo;
-    red[kSelWarps + (threadIdx.x >> 5)] = hi;
+    sh.red_u[0][threadIdx.x >> 5] = lo;
+    sh.red_u[1][threadIdx.x >> 5] = hi;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) {
-    lo = fminf(lo, red[i]);
-    hi = fmaxf(hi, red[kSelWarps + i]);
+  for (int i = 0; i < WARPS; ++i) {
+    lo = min(lo, sh.red_u[0][i]);
+    hi = max(hi, sh.red_u[1][i]);
   }
 }
+template <int WARPS>
+__device__ __forceinline__ float block_max(float v, SelShared &sh) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.red_f[threadIdx.x >> 5] = v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) v = fmaxf(v, sh.red_f[i]);
+  return v;
+}
 
-__device__ __forceinline__ int bin_of(float s, float lo, float inv) {
-  const float x = (s - lo) * inv;  // non-decreasing in s
-  return !(x >= 0.f) ? 0 : x >= (float)kSelBins ? kSelBins - 1 : min((int)x, kSelBins - 1);
+// Q+ and Q- in fp64 (exact: at most 16 numbers), for rescoring.
+template <typename T, int D, int WARPS>
+__device__ __forceinline__ void wide_weights(const T *q, int G, SelShared &sh) {
+  for (int d = threadIdx.x; d < D; d += WARPS * 32) {
+    double qp = 0.0, qn = 0.0;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) {
+      const double f = g < G ? (double)to_float(q[(size_t)g * D + d]) : 0.0;
+      if (f > 0.0) qp += f;
+      if (f < 0.0) qn += f;
+    }
+    sh.wide[d] = qp;
+    sh.wide[D + d] = qn;
+  }
+  __syncthreads();
+}
+// A page's score in fp64, by a warp (every lane gets it).
+template <typename T, int D>
+__device__ __forceinline__ double fine_score(const SelectParams &p, int blk, int h, const SelShared &sh) {
+  if ((unsigned)blk >= (unsigned)p.num_blocks) return -CUDART_INF;
+  const T *b = static_cast<const T *>(p.key_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D;
+  double s = 0.0;
+#pragma unroll 4
+  for (int d = threadIdx.x & 31; d < 2 * D; d += 32) s += sh.wide[d] * (double)to_float(b[d]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s != s ? -CUDART_INF : s;
+}
+// The m pages listed in sh.list scored in fp64 and the `more` best of them (ties
+// to the lower page) marked, kKeyIn or kKeyOut, in sh.mark.
+template <typename T, int D, int WARPS>
+__device__ __forceinline__ void rescore_list(const SelectParams &p, const T *q, const int32_t *bt, int h,
+                                             int G, int m, int more, SelShared &sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wide_weights<T, D, WARPS>(q, G, sh);  // its barrier also publishes the list
+  for (int j = warp; j < m; j += WARPS) {
+    const double s = fine_score<T, D>(p, __ldg(bt + sh.list[j]), h, sh);
+    if (lane == 0) sh.fine[j] = s;
+  }
+  __syncthreads();
+  for (int j0 = tid; j0 < m; j0 += WARPS * 32) {
+    const double s = sh.fine[j0];
+    const int i = sh.list[j0];
+    int rank = 0;
+    for (int j = 0; j < m; ++j) {
+      const double t = sh.fine[j];
+      rank += t > s || (t == s && sh.list[j] < i);
+    }
+    sh.mark[j0] = rank < more ? kKeyIn : kKeyOut;
+  }
+  __syncthreads();
+}
+
+// The highest bit in which keys between lo and hi can differ (-1: none) and
+// the bits above it, where the search for a cut starts.
+__device__ __forceinline__ int first_bit(uint32_t lo, uint32_t hi, uint32_t &cut) {
+  const int bit = lo == hi ? -1 : 31 - __clz(lo ^ hi);
+  cut = bit < 0 ? lo : bit == 31 ? 0u : (hi >> (bit + 1)) << (bit + 1);
+  return bit;
+}
+
+// The need best of the cand pages from `first` on, by the whole CTA with up to
+// REGS keys a thread in registers, listed in page order.  False (nothing
+// listed) if more pages than the list holds are too close to call.
+template <typename T, int D, int WARPS, int REGS>
+__device__ __forceinline__ bool select_in_registers(const SelectParams &p, const T *q, const int32_t *bt,
+                                                    const uint32_t *kc, int32_t *list, int h, int G,
+                                                    int first, int cand, int need, float eps,
+                                                    SelShared &sh) {
+  constexpr int THREADS = WARPS * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // one barrier a bit
+  int turn = 0;
+  uint32_t key[REGS];
+  uint32_t klo = 0xffffffffu, khi = 0u;
+  // (no early ends in these loops: a missing page's key is below every
+  // score and cut, and a branch a round would cost more than the round)
+#pragma unroll
+  for (int v = 0; v < REGS; ++v) {
+    const int i = tid + v * THREADS;
+    key[v] = i < cand ? kc[first + i] : kKeyOut;
+  }
+#pragma unroll
+  for (int v = 0; v < REGS; ++v) {
+    klo = min(klo, key[v] == kKeyOut ? 0xffffffffu : key[v]);
+    khi = max(khi, key[v]);
+  }
+  block_min_max<WARPS>(klo, khi, sh);
+  uint32_t cut;
+  int have = cand;
+  for (int bit = first_bit(klo, khi, cut); bit >= 0 && have != need; --bit) {
+    const uint32_t mid = cut | (1u << bit);
+    int c = 0;
+#pragma unroll
+    for (int v = 0; v < REGS; ++v) {
+      c += key[v] >= mid;
+    }
+    c = block_sum<WARPS>(c, sh, turn);
+    if (c >= need) {
+      cut = mid;
+      have = c;
+    }
+  }
+  uint32_t ka = 0xffffffffu, kb = 0u;
+#pragma unroll
+  for (int v = 0; v < REGS; ++v) {
+    if (key[v] >= cut)
+      ka = min(ka, key[v]);
+    else
+      kb = max(kb, key[v]);
+  }
+  block_min_max<WARPS>(ka, kb, sh);
+  const float tau = unorder32(ka);
+  bool done = have == need && tau - unorder32(kb) > 2.f * eps;
+  if (!done) {
+    const float fhi = tau + 2.f * eps, flo = tau - 2.f * eps;
+    const uint32_t hi = fhi == fhi ? order32(fhi) : kKeyIn - 1;
+    const uint32_t lo = flo == flo ? order32(flo) : kKeyOut + 1;
+    int c = 0, m = 0;
+#pragma unroll
+    for (int v = 0; v < REGS; ++v) {
+      c += key[v] > hi;
+      m += key[v] >= lo && key[v] <= hi;
+    }
+    if (tid == 0) sh.count = 0;
+    const int more = need - block_sum<WARPS>(c, sh, turn);
+    m = block_sum<WARPS>(m, sh, turn);
+    if (m <= kSelList) {
+#pragma unroll
+      for (int v = 0; v < REGS; ++v) {
+          if (key[v] >= lo && key[v] <= hi)
+          sh.list[atomicAdd(&sh.count, 1)] = first + tid + v * THREADS;
+      }
+      rescore_list<T, D, WARPS>(p, q, bt, h, G, m, more, sh);
+#pragma unroll
+      for (int v = 0; v < REGS; ++v) {
+          if (key[v] >= lo && key[v] <= hi)
+          for (int j = 0; j < m; ++j)
+            if (sh.list[j] == first + tid + v * THREADS) {
+              key[v] = sh.mark[j];
+              break;
+            }
+      }
+      cut = hi + 1;
+      done = true;
+      __syncthreads();  // the list is free for the pages chosen
+    }
+  }
+  if (done) {
+    // in page order: round v before round v + 1, warp by warp in each
+#pragma unroll
+    for (int v = 0; v < REGS; ++v) {
+      const unsigned m = __ballot_sync(0xffffffffu, key[v] >= cut);
+      if (lane == 0) sh.counts[v * WARPS + warp] = __popc(m);
+    }
+    __syncthreads();
+    if (warp == 0) {  // running sums, a few a lane
+      constexpr int PER = REGS * WARPS / 32;
+      int c[PER], sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        c[i] = sh.counts[lane * PER + i];
+        sum += c[i];
+      }
+      int run = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, run, d);
+        if (lane >= d) run += t;
+      }
+      run -= sum;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        sh.counts[lane * PER + i] = run;
+        run += c[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < REGS; ++v) {
+      const unsigned m = __ballot_sync(0xffffffffu, key[v] >= cut);
+      if (key[v] >= cut)
+        list[sh.counts[v * WARPS + warp] + __popc(m & ((1u << lane) - 1u))] =
+            first + tid + v * THREADS;
+    }
+  }
+  __syncthreads();
+  return done;
 }
 
 }  // namespace
 
-// Dynamic shared memory: the scores of min(max_pages, kSelSmemPages) pages.
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_constant__ SelectParams p) {
+// Dynamic shared memory: the keys (order32 of the scores) of p.smem_pages
+// pages.
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
+    pa_select_kernel(const __grid_constant__ SelectParams p) {
+  // (32 warps an SM: at most 64 registers a thread)
+  constexpr int THREADS = WARPS * 32;
   constexpr int N = 16 / (int)sizeof(T);       // elements of a 16-byte piece
   constexpr int PIECES = 2 * D / N;            // of a page's bounds
   constexpr int LPP = PIECES < 32 ? PIECES : 32;  // lanes of a page
   constexpr int VPL = PIECES / LPP;            // pieces a lane
   constexpr int PPW = 32 / LPP;                // pages of a warp side by side
+  constexpr int SEG = VPL <= 1 ? 8 : 8 / VPL;  // pages of a warp at a time: 32 registers' worth
   __shared__ SelShared sh;
-  extern __shared__ __align__(16) float s_scores[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int item = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int row = item / p.num_kv_heads, h = item % p.num_kv_heads;
   const int G = p.num_heads / p.num_kv_heads;
 
+  // the row's queries and (one row a sequence) its table, on their way to L2
+  // while the kernel before this one ends
+  const T *q = static_cast<const T *>(p.query) + ((size_t)row * p.num_heads + h * G) * D;
+  for (int i = tid * 128; i < G * D * (int)sizeof(T); i += THREADS * 128)
+    prefetch_l2(reinterpret_cast<const char *>(q) + i);
+  if (tid == 0) prefetch_l2(p.seq_lens + (p.q_start ? 0 : row));
+  if (!p.q_start && tid * 32 < p.chunk_pages)
+    prefetch_l2(p.block_tables + (size_t)row * p.max_blocks_per_seq +
+                min(chunk * p.chunk_pages + tid * 32, p.max_blocks_per_seq - 1));
   pdl_wait_primary();
   pdl_launch_dependents();
   int seq, vis;
@@ -177,48 +401,48 @@ __global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_con
   const int nch = all ? 1 : (n + p.chunk_pages - 1) / p.chunk_pages;
   if (chunk >= nch) return;
   const int first = p.sinks, last = n - p.recent;  // pages [first, last) go by their score
-  const bool local = n <= kSelSmemPages && n <= p.smem_pages;  // the selecting CTA's scores: in smem
-  float *gscores = p.scores + (size_t)item * p.max_pages;
-  const T *q = static_cast<const T *>(p.query) + ((size_t)row * p.num_heads + h * G) * D;
+  const int need = k - p.sinks - p.recent;         // of them
+  // the keys: in shared memory if the CTA scores them all and they fit
+  uint32_t *kc = p.chunks == 1 && n <= p.smem_pages ? s_keys : p.keys + (size_t)item * p.max_pages;
+  int32_t *selected = p.selected ? p.selected + (size_t)item * k : nullptr;
+  int32_t *table = p.table ? p.table + (size_t)item * k : nullptr;
+  // where the chosen candidates' pages are listed, in page order
+  int32_t *list = need <= kSelList ? sh.list : (table ? table : selected) + p.sinks;
 
-  float *sc = s_scores;
   if (!all) {
+    // ---- Q+ and Q-: the group's loads all in flight ----
+    for (int d = tid; d < D; d += THREADS) {
+      float qp = 0.f, qn = 0.f;
+#pragma unroll
+      for (int g = 0; g < 16; ++g) {
+        const float f = g < G ? to_float(q[(size_t)g * D + d]) : 0.f;
+        qp += fmaxf(f, 0.f);
+        qn += fminf(f, 0.f);
+      }
+      sh.w[d] = qp;
+      sh.w[D + d] = qn;
+    }
+    __syncthreads();
+
     // ---- scores of the chunk's pages ----
     float w[VPL][N];
-    float wsum = 0.f;
     const int lp = lane % LPP;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int piece = v * LPP + lp;
-      const bool pos = piece < PIECES / 2;
-      const int d0 = (pos ? piece : piece - PIECES / 2) * N;
+    for (int v = 0; v < VPL; ++v)
 #pragma unroll
-      for (int e = 0; e < N; ++e) w[v][e] = 0.f;
-      for (int g = 0; g < G; ++g) {
-        float f[N];
-        widen<T>(__ldg(reinterpret_cast<const uint4 *>(q + (size_t)g * D + d0)), f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) w[v][e] += pos ? fmaxf(f[e], 0.f) : fminf(f[e], 0.f);
-      }
-#pragma unroll
-      for (int e = 0; e < N; ++e) wsum += fabsf(w[v][e]);
-    }
-#pragma unroll
-    for (int d = LPP / 2; d > 0; d >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, d);
-    float amax = 0.f;
+      for (int e = 0; e < N; ++e) w[v][e] = sh.w[(v * LPP + lp) * N + e];
+    float size = 0.f;  // the largest sum |Q| |bound| of this lane's part of a page
     const int c_end = min(n, (chunk + 1) * p.chunk_pages);
-    float *out = p.chunks == 1 && local ? s_scores : gscores;
-    for (int p0 = chunk * p.chunk_pages + warp * kSelSegment; p0 < c_end;
-         p0 += kSelWarps * kSelSegment) {
+    for (int p0 = chunk * p.chunk_pages + warp * SEG; p0 < c_end; p0 += WARPS * SEG) {
       int blk = -1;  // also past the chunk: those lanes load nothing
-      if (lane < kSelSegment && p0 + lane < c_end) {
+      if (lane < SEG && p0 + lane < c_end) {
         blk = __ldg(bt + p0 + lane);
         if ((unsigned)blk >= (unsigned)p.num_blocks) {
           report(p.status, kStatusBadInput);
           blk = -1;
         }
       }
-      constexpr int STEPS = kSelSegment / PPW;
+      constexpr int STEPS = SEG / PPW;
       float acc[STEPS];
       uint4 x[STEPS][VPL];
 #pragma unroll
@@ -233,6 +457,7 @@ __global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_con
 #pragma unroll
       for (int j = 0; j < STEPS; ++j) {
         acc[j] = 0.f;
+        float mag = 0.f;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
           float f[N];
@@ -240,9 +465,10 @@ __global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < N; ++e) {
             acc[j] = fmaf(w[v][e], f[e], acc[j]);
-            amax = fmaxf(amax, fabsf(f[e]));
+            mag = fmaf(fabsf(w[v][e]), fabsf(f[e]), mag);
           }
         }
+        size = fmaxf(size, mag);
       }
 #pragma unroll
       for (int d = LPP / 2; d > 0; d >>= 1)
@@ -255,231 +481,279 @@ __global__ void __launch_bounds__(kSelThreads) pa_select_kernel(const __grid_con
         const float t = __shfl_sync(0xffffffffu, acc[j], (lane % PPW) * LPP);
         if (lane / PPW == j) mine = t;
       }
-      if (lane < kSelSegment && p0 + lane < c_end)
-        out[p0 + lane] = blk < 0 || mine != mine ? -CUDART_INF_F : mine;
+      if (lane < SEG && p0 + lane < c_end)
+        kc[p0 + lane] = order32(blk < 0 || mine != mine ? -CUDART_INF_F : mine);
     }
-    float lo = 0.f;
-    block_min_max(lo, amax, sh.red_f);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) size += __shfl_xor_sync(0xffffffffu, size, d);
+    size = block_max<WARPS>(size, sh);  // (its barriers also publish the keys)
     if (p.chunks > 1) {
-      if (tid == 0) p.amax[(size_t)item * p.chunks + chunk] = amax;
-      __syncthreads();
-      if (tid == 0) sh.flag = atomic_add_acq_rel_gpu(p.counters + item, 1) == nch - 1;
+      if (tid == 0) {
+        p.sizes[(size_t)item * p.chunks + chunk] = size;
+        sh.flag = atomic_add_acq_rel_gpu(p.counters + item, 1) == nch - 1;
+      }
       __syncthreads();
       if (!sh.flag) return;
       if (tid == 0) p.counters[item] = 0;  // every chunk is in: ready for the next call
-      amax = 0.f;
-      for (int c = tid; c < nch; c += kSelThreads)
-        amax = fmaxf(amax, __ldcg(p.amax + (size_t)item * p.chunks + c));
-      block_min_max(lo, amax, sh.red_f);
+      size = 0.f;
+      for (int c = tid; c < nch; c += THREADS)
+        size = fmaxf(size, __ldcg(p.sizes + (size_t)item * p.chunks + c));
+      size = block_max<WARPS>(size, sh);
     }
-    if (!local) {
-      sc = gscores;
-    } else if (p.chunks > 1) {
-      for (int i = tid; i < n; i += kSelThreads) s_scores[i] = __ldcg(gscores + i);
-    }
-    __syncthreads();
+    const float eps = (float)(G + VPL * N + 7) * 5.9604644775390625e-8f * size + 1e-36f;
 
     // ---- the need best of pages [first, last) ----
-    const int need = k - p.sinks - p.recent;
-    float hi_in = CUDART_INF_F, lo_in = CUDART_INF_F;  // in above hi_in, out below lo_in
-    bool marked = false;  // those in between carry +inf (in) or -inf (out)
-    if (need > 0) {
-      const float eps = 48.f * 5.9604644775390625e-8f * wsum * amax + 1e-36f;
-      float lo = CUDART_INF_F, hi = -CUDART_INF_F;  // finite scores' range
-      for (int i = first + tid; i < last; i += kSelThreads) {
-        const float s = sc[i];
-        if (fabsf(s) <= 3.402823466e38f) {
-          lo = fminf(lo, s);
-          hi = fmaxf(hi, s);
-        }
-      }
-      block_min_max(lo, hi, sh.red_f);
-      // The bin of a histogram over [lo, hi] that holds the need-th score;
-      // then, if too many scores are that close, over that bin's own range.
-      int m = 0;
-      float t_lo = -CUDART_INF_F, t_hi = CUDART_INF_F;
-      int above0 = 0;  // scores above the histogram's range
-      for (int pass = 0; pass < 4; ++pass) {
-        const float inv = hi > lo ? (float)kSelBins / (hi - lo) : 0.f;
-        const bool ranged = pass > 0;
-        for (int b = tid; b < kSelBins; b += kSelThreads) sh.hist[b] = 0;
-        __syncthreads();
-        for (int i = first + tid; i < last; i += kSelThreads) {
-          const float s = sc[i];
-          if (!ranged || (s >= t_lo && s <= t_hi)) atomicAdd(&sh.hist[bin_of(s, lo, inv)], 1);
-        }
-        __syncthreads();
-        // bins from the top: thread t holds bins (511 - 2t, 510 - 2t)
-        const int b1 = sh.hist[kSelBins - 1 - 2 * tid], b0 = sh.hist[kSelBins - 2 - 2 * tid];
-        int run = b0 + b1;
+    // A cut with exactly need keys at or above it, by bisection on the keys'
+    // bits from the highest in which any two differ.  It is exact if the
+    // scores on its two sides are more than 2 eps apart.
+    const int cand = last - first;  // more than need
+    bool done = need == 0;
+    if (!done && cand <= kSelWarpPages) {
+      // one warp, the keys in registers, no barriers
+      if (warp == 0) {
+        uint32_t key[kSelWarpPages / 32];
+        uint32_t klo = 0xffffffffu, khi = 0u;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int t = __shfl_up_sync(0xffffffffu, run, d);
-          if (lane >= d) run += t;
+        for (int v = 0; v < kSelWarpPages / 32; ++v) {
+          const int i = lane + 32 * v;
+          key[v] = i < cand ? kc[first + i] : kKeyOut;  // below every score
+          klo = min(klo, i < cand ? key[v] : 0xffffffffu);
+          khi = max(khi, key[v]);
         }
-        if (lane == 31) sh.red_i[warp] = run;
-        __syncthreads();
-        int base = above0;
-        for (int i = 0; i < warp; ++i) base += sh.red_i[i];
-        const int before = base + run - b0 - b1;  // scores above this thread's bins
-        if (before < need && before + b1 >= need) {
-          sh.bin = kSelBins - 1 - 2 * tid;
-          sh.above = before;
-        } else if (before + b1 < need && before + b1 + b0 >= need) {
-          sh.bin = kSelBins - 2 - 2 * tid;
-          sh.above = before + b1;
-        }
-        __syncthreads();
-        const int bin = sh.bin, above = sh.above;
-        float blo = CUDART_INF_F, bhi = -CUDART_INF_F;  // the bin's own range
-        for (int i = first + tid; i < last; i += kSelThreads) {
-          const float s = sc[i];
-          if ((!ranged || (s >= t_lo && s <= t_hi)) && bin_of(s, lo, inv) == bin) {
-            blo = fminf(blo, s);
-            bhi = fmaxf(bhi, s);
-          }
-        }
-        block_min_max(blo, bhi, sh.red_f);
-        t_lo = blo;
-        t_hi = bhi;
-        above0 = above;
-        hi_in = t_hi + 2.f * eps;
-        lo_in = t_lo - 2.f * eps;
-        int c = 0;
-        for (int i = first + tid; i < last; i += kSelThreads) c += !(sc[i] > hi_in) && !(sc[i] < lo_in);
-        m = block_sum(c, sh.red_i);
-        if (m <= kSelList || !(t_hi > t_lo) || !(t_hi - t_lo > 4.f * eps)) break;
-        lo = t_lo;
-        hi = t_hi;
-      }
-      int c = 0;
-      for (int i = first + tid; i < last; i += kSelThreads) c += sc[i] > hi_in;
-      const int more = need - block_sum(c, sh.red_i);  // of the m in between
-      if (more < m) {
-        // ---- score those m again in fp64 ----
-        for (int d = tid; d < 2 * D; d += kSelThreads) {
-          double a = 0.0;
-          for (int g = 0; g < G; ++g) {
-            const double f = (double)to_float(q[(size_t)g * D + d % D]);
-            a += d < D ? fmax(f, 0.0) : fmin(f, 0.0);
-          }
-          sh.w[d] = a;
-        }
-        if (tid == 0) sh.count = 0;
-        __syncthreads();
-        const bool small = m <= kSelList;
-        if (small) {
-          for (int i = first + tid; i < last; i += kSelThreads)
-            if (!(sc[i] > hi_in) && !(sc[i] < lo_in)) sh.list[atomicAdd(&sh.count, 1)] = i;
-          __syncthreads();
-        }
-        double *gfine = p.fine + (size_t)item * p.max_pages;
-        const int jobs = small ? m : last - first;
-        for (int j = warp; j < jobs; j += kSelWarps) {
-          const int i = small ? sh.list[j] : first + j;
-          if (!small && (sc[i] > hi_in || sc[i] < lo_in)) continue;
-          const int blk = __ldg(bt + i);
-          double s = -CUDART_INF;
-          if ((unsigned)blk < (unsigned)p.num_blocks) {
-            s = 0.0;
-            const T *b = static_cast<const T *>(p.key_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D;
-#pragma unroll 4
-            for (int d = lane; d < 2 * D; d += 32) s += sh.w[d] * (double)to_float(b[d]);
+        klo = __reduce_min_sync(0xffffffffu, klo);
+        khi = __reduce_max_sync(0xffffffffu, khi);
+        uint32_t cut;
+        int have = cand;
+        for (int bit = first_bit(klo, khi, cut); bit >= 0 && have != need; --bit) {
+          const uint32_t mid = cut | (1u << bit);
+          int c = 0;
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (s != s) s = -CUDART_INF;
-          }
-          if (lane == 0) {
-            if (small)
-              sh.fine[j] = s;
-            else
-              gfine[i] = s;
+          for (int v = 0; v < kSelWarpPages / 32; ++v) c += key[v] >= mid;
+          c = __reduce_add_sync(0xffffffffu, c);
+          if (c >= need) {
+            cut = mid;
+            have = c;
           }
         }
-        __syncthreads();
-        // mark: +inf for the `more` best (ties to the lower page), -inf for
-        // the others
-        if (small) {
-          if (tid < m) {
-            const double s = sh.fine[tid];
-            const int i = sh.list[tid];
+        uint32_t ka = 0xffffffffu, kb = 0u;
+#pragma unroll
+        for (int v = 0; v < kSelWarpPages / 32; ++v) {
+          if (key[v] >= cut)
+            ka = min(ka, key[v]);
+          else
+            kb = max(kb, key[v]);
+        }
+        ka = __reduce_min_sync(0xffffffffu, ka);
+        kb = __reduce_max_sync(0xffffffffu, kb);
+        const float tau = unorder32(ka);
+        bool exact = have == need && tau - unorder32(kb) > 2.f * eps;
+        if (!exact) {
+          // up to 32 pages between: scored again here, one lane each to keep
+          const float fhi = tau + 2.f * eps, flo = tau - 2.f * eps;
+          const uint32_t hi = fhi == fhi ? order32(fhi) : kKeyIn - 1;
+          const uint32_t lo = flo == flo ? order32(flo) : kKeyOut + 1;
+          int c = 0, m = 0, mine = -1;
+#pragma unroll
+          for (int v = 0; v < kSelWarpPages / 32; ++v) {
+            c += key[v] > hi;
+            const bool in = key[v] >= lo && key[v] <= hi;
+            const unsigned b = __ballot_sync(0xffffffffu, in);
+            // lane m + r takes the r-th of them
+            const int r = lane - m;
+            if (r >= 0 && r < __popc(b)) mine = 32 * v + __fns(b, 0, r + 1);
+            m += __popc(b);
+          }
+          const int more = need - __reduce_add_sync(0xffffffffu, c);
+          if (m <= 32) {
+            double wp[D / 32], wn[D / 32];
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+              wp[d] = wn[d] = 0.0;
+#pragma unroll 8
+              for (int g = 0; g < G; ++g) {
+                const double f = (double)to_float(q[(size_t)g * D + lane + 32 * d]);
+                if (f > 0.0) wp[d] += f;
+                if (f < 0.0) wn[d] += f;
+              }
+            }
+            double score = 0.0;
+            for (int j = 0; j < m; ++j) {
+              const int blk = __ldg(bt + first + __shfl_sync(0xffffffffu, mine, j));
+              double sum = -CUDART_INF;
+              if ((unsigned)blk < (unsigned)p.num_blocks) {
+                const T *b = static_cast<const T *>(p.key_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D;
+                sum = 0.0;
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d)
+                  sum += wp[d] * (double)to_float(b[lane + 32 * d]) +
+                         wn[d] * (double)to_float(b[D + lane + 32 * d]);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (sum != sum) sum = -CUDART_INF;
+              }
+              if (lane == j) score = sum;
+            }
             int rank = 0;
             for (int j = 0; j < m; ++j) {
-              const double t = sh.fine[j];
-              rank += t > s || (t == s && sh.list[j] < i);
+              const double t = __shfl_sync(0xffffffffu, score, j);
+              rank += t > score || (t == score && j < lane);  // in page order already
             }
-            sc[i] = rank < more ? CUDART_INF_F : -CUDART_INF_F;
+            for (int j = 0; j < m; ++j) {
+              const int i = __shfl_sync(0xffffffffu, mine, j);
+              const uint32_t mark = __shfl_sync(0xffffffffu, rank, j) < more ? kKeyIn : kKeyOut;
+#pragma unroll
+              for (int v = 0; v < kSelWarpPages / 32; ++v)
+                if (i == lane + 32 * v) key[v] = mark;
+            }
+            cut = hi + 1;
+            exact = true;
           }
+        }
+        if (exact) {
+          int at = 0;
+#pragma unroll
+          for (int v = 0; v < kSelWarpPages / 32; ++v) {
+            const unsigned m = __ballot_sync(0xffffffffu, key[v] >= cut);
+            if (key[v] >= cut) list[at + __popc(m & ((1u << lane) - 1u))] = first + lane + 32 * v;
+            at += __popc(m);
+          }
+        }
+        if (lane == 0) sh.flag = exact;
+      }
+      __syncthreads();
+      done = sh.flag;
+    } else if (!done && cand <= 8 * THREADS) {
+      done = select_in_registers<T, D, WARPS, 8>(p, q, bt, kc, list, h, G, first, cand, need, eps, sh);
+    } else if (WARPS == 8 && !done && cand <= 32 * THREADS) {
+      done = select_in_registers<T, D, WARPS, 32>(p, q, bt, kc, list, h, G, first, cand, need, eps, sh);
+    }
+    if (!done) {
+      int turn = 0;
+      uint32_t klo = 0xffffffffu, khi = 0u;
+#pragma unroll 4
+      for (int i = first + tid; i < last; i += THREADS) {
+        const uint32_t u = kc[i];
+        klo = min(klo, u);
+        khi = max(khi, u);
+      }
+      block_min_max<WARPS>(klo, khi, sh);
+      uint32_t cut;
+      int have = cand;
+      for (int bit = first_bit(klo, khi, cut); bit >= 0 && have != need; --bit) {
+        const uint32_t mid = cut | (1u << bit);
+        int c = 0;
+#pragma unroll 8
+        for (int i = first + tid; i < last; i += THREADS) c += kc[i] >= mid;
+        c = block_sum<WARPS>(c, sh, turn);
+        if (c >= need) {
+          cut = mid;
+          have = c;
+        }
+      }
+      // tau, the need-th largest score, is the lowest above the cut
+      uint32_t ka = 0xffffffffu, kb = 0u;
+#pragma unroll 4
+      for (int i = first + tid; i < last; i += THREADS) {
+        const uint32_t u = kc[i];
+        if (u >= cut)
+          ka = min(ka, u);
+        else
+          kb = max(kb, u);
+      }
+      block_min_max<WARPS>(ka, kb, sh);
+      const float tau = unorder32(ka);
+      if (!(have == need && tau - unorder32(kb) > 2.f * eps)) {
+        // Pages above hi are in, pages below lo out; those between (all of
+        // them, if eps is not finite) are scored again in fp64.
+        const float fhi = tau + 2.f * eps, flo = tau - 2.f * eps;
+        const uint32_t hi = fhi == fhi ? order32(fhi) : kKeyIn - 1;
+        const uint32_t lo = flo == flo ? order32(flo) : kKeyOut + 1;
+        int c = 0, m = 0;
+        for (int i = first + tid; i < last; i += THREADS) {
+          c += kc[i] > hi;
+          m += kc[i] >= lo && kc[i] <= hi;
+        }
+        const int more = need - block_sum<WARPS>(c, sh, turn);  // of the m in between
+        m = block_sum<WARPS>(m, sh, turn);
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        if (m <= kSelList) {
+          for (int i = first + tid; i < last; i += THREADS)
+            if (kc[i] >= lo && kc[i] <= hi) sh.list[atomicAdd(&sh.count, 1)] = i;
+          rescore_list<T, D, WARPS>(p, q, bt, h, G, m, more, sh);
+          for (int j = tid; j < m; j += THREADS) kc[sh.list[j]] = sh.mark[j];
         } else {
+          double *gfine = p.fine + (size_t)item * p.max_pages;
+          wide_weights<T, D, WARPS>(q, G, sh);
+          for (int i = first + warp; i < last; i += WARPS) {
+            if (kc[i] > hi || kc[i] < lo) continue;
+            const double s = fine_score<T, D>(p, __ldg(bt + i), h, sh);
+            if (lane == 0) gfine[i] = s;
+          }
+          __syncthreads();
           // the more-th largest by bisection, then its ties in page order
           unsigned long long t = 0;
-          for (int bit = 63; bit >= 0; --bit) {
-            const unsigned long long cand = t | (1ull << bit);
+          for (int b = 63; b >= 0; --b) {
+            const unsigned long long mid = t | (1ull << b);
             int cnt = 0;
-            for (int i = first + tid; i < last; i += kSelThreads)
-              if (!(sc[i] > hi_in) && !(sc[i] < lo_in)) cnt += order64(gfine[i]) >= cand;
-            if (block_sum(cnt, sh.red_i) >= more) t = cand;
+            for (int i = first + tid; i < last; i += THREADS)
+              if (kc[i] >= lo && kc[i] <= hi) cnt += order64(gfine[i]) >= mid;
+            if (block_sum<WARPS>(cnt, sh, turn) >= more) t = mid;
           }
           int cnt = 0;
-          for (int i = first + tid; i < last; i += kSelThreads)
-            if (!(sc[i] > hi_in) && !(sc[i] < lo_in)) cnt += order64(gfine[i]) > t;
-          int ties = more - block_sum(cnt, sh.red_i);
+          for (int i = first + tid; i < last; i += THREADS)
+            if (kc[i] >= lo && kc[i] <= hi) cnt += order64(gfine[i]) > t;
+          int ties = more - block_sum<WARPS>(cnt, sh, turn);
           if (warp == 0) {
             for (int i0 = first; i0 < last; i0 += 32) {
               const int i = i0 + lane;
-              const bool in = i < last && !(sc[i] > hi_in) && !(sc[i] < lo_in);
+              const bool in = i < last && kc[i] >= lo && kc[i] <= hi;
               const unsigned long long u = in ? order64(gfine[i]) : 0;
               const unsigned eq = __ballot_sync(0xffffffffu, in && u == t);
               const bool keep = in && (u > t || (u == t && __popc(eq & ((1u << lane) - 1u)) < ties));
               ties = max(0, ties - __popc(eq));
-              if (in) sc[i] = keep ? CUDART_INF_F : -CUDART_INF_F;
+              if (in) kc[i] = keep ? kKeyIn : kKeyOut;
             }
           }
         }
         __syncthreads();
-        marked = true;
-      }  // else all of them are in
-    }
-    // ---- the selected pages in page order ----
-    auto selected = [&](int i) -> bool {
-      if (i < first || i >= last) return true;
-      if (need <= 0) return false;
-      const float s = sc[i];
-      return marked ? s > hi_in || s == CUDART_INF_F : !(s < lo_in);
-    };
-    const int seg = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int s0 = min(n, warp * seg), s1 = min(n, s0 + seg);
-    int cnt = 0;
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-      const int i = i0 + lane;
-      cnt += __popc(__ballot_sync(0xffffffffu, i < s1 && selected(i)));
-    }
-    __syncthreads();
-    if (lane == 0) sh.red_i[warp] = cnt;
-    __syncthreads();
-    int at = 0;
-    for (int i = 0; i < warp; ++i) at += sh.red_i[i];
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < s1 && selected(i);
-      const unsigned m = __ballot_sync(0xffffffffu, in);
-      const int o = at + __popc(m & ((1u << lane) - 1u));
-      if (in && o < k) {
-        if (p.selected) p.selected[(size_t)item * k + o] = i;
-        if (p.table) p.table[(size_t)item * k + o] = view_block(__ldg(bt + i), h, p.num_kv_heads, p.num_blocks);
+        cut = hi + 1;  // those above and the marks
       }
-      at += __popc(m);
+      // the chosen candidates in page order, a segment a warp
+      const int seg = ((cand + WARPS - 1) / WARPS + 31) / 32 * 32;
+      const int s0 = first + min(cand, warp * seg), s1 = min(last, s0 + seg);
+      int cnt = 0;
+#pragma unroll 4
+      for (int i = s0 + lane; i < s1; i += 32) cnt += kc[i] >= cut;
+      cnt = __reduce_add_sync(0xffffffffu, cnt);
+      turn ^= 1;
+      if (lane == 0) sh.red_i[turn][warp] = cnt;
+      __syncthreads();
+      int at = 0;
+      for (int i = 0; i < warp; ++i) at += sh.red_i[turn][i];
+#pragma unroll 4
+      for (int i0 = s0; i0 < s1; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < s1 && kc[i] >= cut;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        const int o = at + __popc(m & ((1u << lane) - 1u));
+        if (in && o < need) list[o] = i;
+        at += __popc(m);
+      }
+      __syncthreads();
     }
-    if (tid == 0 && p.lens) p.lens[item] = (k - 1) * p.block_size + vis - (n - 1) * p.block_size;
-  } else {
-    for (int o = tid; o < k; o += kSelThreads) {
-      if (p.selected) p.selected[(size_t)item * k + o] = o < n ? o : -1;
-      if (p.table)
-        p.table[(size_t)item * k + o] =
-            o < n ? view_block(__ldg(bt + o), h, p.num_kv_heads, p.num_blocks) : -1;
-    }
-    if (tid == 0 && p.lens) p.lens[item] = vis;
   }
+  // ---- the selected pages, in page order ----
+  for (int o = tid; o < k; o += THREADS) {
+    const int i = all ? (o < n ? o : -1)
+                  : o < p.sinks       ? o
+                  : o < k - p.recent  ? list[o - p.sinks]
+                                      : n - (k - o);
+    if (selected) selected[o] = i;
+    if (table) table[o] = i >= 0 ? view_block(__ldg(bt + i), h, p.num_kv_heads, p.num_blocks) : -1;
+  }
+  if (tid == 0 && p.lens)
+    p.lens[item] = all ? vis : (k - 1) * p.block_size + vis - (n - 1) * p.block_size;
 }
 
 // A given selection (pages in ascending order, -1 behind the last) as the
@@ -529,14 +803,18 @@ __global__ void __launch_bounds__(128) pa_given_blocks_kernel(const __grid_const
 
 namespace {
 
-template <typename T>
+template <typename T, int WARPS>
 const void *pick_select(int head_size) {
   switch (head_size) {
-    case 64: return reinterpret_cast<const void *>(&pa_select_kernel<T, 64>);
-    case 128: return reinterpret_cast<const void *>(&pa_select_kernel<T, 128>);
-    case 256: return reinterpret_cast<const void *>(&pa_select_kernel<T, 256>);
+    case 64: return reinterpret_cast<const void *>(&pa_select_kernel<T, 64, WARPS>);
+    case 128: return reinterpret_cast<const void *>(&pa_select_kernel<T, 128, WARPS>);
+    case 256: return reinterpret_cast<const void *>(&pa_select_kernel<T, 256, WARPS>);
   }
   return nullptr;
+}
+template <typename T>
+const void *pick_select(int head_size, int warps) {
+  return warps == 4 ? pick_select<T, 4>(head_size) : pick_select<T, 8>(head_size);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -544,7 +822,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // The workspace: the attention's over the view, then table, lengths, counters
 // and what the selection keeps a page.
 struct SparseLayout {
-  size_t table, lens, counters, amax, scores, fine, total;
+  size_t table, lens, counters, sizes, keys, fine, total;
   int max_pages, view_len;
 };
 constexpr int kSelMaxChunks = 1024;  // of an item
@@ -565,10 +843,10 @@ bool sparse_layout(int num_rows, int num_heads, int num_kv_heads, int head_size,
   o->table = align256(attn);
   o->lens = o->table + align256((size_t)items * num_selected * 4);
   o->counters = o->lens + align256((size_t)items * 4);
-  o->amax = o->counters + align256((size_t)items * 4);
+  o->sizes = o->counters + align256((size_t)items * 4);
   const int chunks = (o->max_pages + 63) / 64;
-  o->scores = o->amax + align256((size_t)items * (chunks < kSelMaxChunks ? chunks : kSelMaxChunks) * 4);
-  o->fine = o->scores + align256((size_t)items * o->max_pages * 4);
+  o->keys = o->sizes + align256((size_t)items * (chunks < kSelMaxChunks ? chunks : kSelMaxChunks) * 4);
+  o->fine = o->keys + align256((size_t)items * o->max_pages * 4);
   o->total = o->fine + align256((size_t)items * o->max_pages * 8);
   return true;
 }
@@ -629,8 +907,8 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
   p.table = table ? reinterpret_cast<int32_t *>(ws + lay.table) : nullptr;
   p.lens = table ? reinterpret_cast<int32_t *>(ws + lay.lens) : nullptr;
   p.counters = reinterpret_cast<int *>(ws + lay.counters);
-  p.amax = reinterpret_cast<float *>(ws + lay.amax);
-  p.scores = reinterpret_cast<float *>(ws + lay.scores);
+  p.sizes = reinterpret_cast<float *>(ws + lay.sizes);
+  p.keys = reinterpret_cast<uint32_t *>(ws + lay.keys);
   p.fine = reinterpret_cast<double *>(ws + lay.fine);
   p.status = reinterpret_cast<int *>(ws);
   p.num_seqs = c.num_seqs;
@@ -652,12 +930,15 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
     return host_launch(reinterpret_cast<const void *>(&pa_given_blocks_kernel),
                        (unsigned)((items + 3) / 4), 1, 128, 0, c.stream, args,
                        "launch given-blocks kernel");
-  // One CTA an item if that gives every SM four; otherwise chunks of at least
-  // 64 pages (a round of the CTA's warps) towards that number.
+  // One CTA an item if that gives every SM four.  Otherwise chunks of at
+  // least 64 pages (a round of the CTA's warps) towards sixteen an SM: with
+  // lengths of all kinds in a batch, a long sequence's chunks are what the
+  // last SMs wait for (64 sequences of up to 4096 pages, D 256: 49 us at four
+  // an SM).
   p.chunks = 1;
   p.chunk_pages = lay.max_pages > 0 ? lay.max_pages : 1;
   if (items < 4ll * sms) {
-    long long want = (4ll * sms + items - 1) / items;
+    long long want = (16ll * sms + items - 1) / items;
     const long long most = (lay.max_pages + 63) / 64;
     if (want > most) want = most;
     if (want > kSelMaxChunks) want = kSelMaxChunks;
@@ -667,12 +948,16 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
     }
   }
   if (items * p.chunks > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
-  p.smem_pages = lay.max_pages < kSelSmemPages ? lay.max_pages : kSelSmemPages;
-  const size_t smem = (size_t)(p.smem_pages > 0 ? p.smem_pages : 1) * 4;
-  const void *fn = c.dtype == PA_DTYPE_F32    ? pick_select<float>(c.head_size)
-                   : c.dtype == PA_DTYPE_BF16 ? pick_select<__nv_bfloat16>(c.head_size)
-                                              : pick_select<__half>(c.head_size);
-  return host_launch(fn, (unsigned)(items * p.chunks), 1, kSelThreads, smem, c.stream, args,
+  p.smem_pages = p.chunks > 1 ? 0 : lay.max_pages < kSelSmemPages ? lay.max_pages : kSelSmemPages;
+  const size_t smem = (size_t)p.smem_pages * 4;
+  // Whole items: four warps, so that the items of a decode batch are all
+  // resident at once (1024 items: one wave, where eight warps took two).
+  // Chunks: eight, for the CTA that selects from all of an item's pages.
+  const int warps = p.chunks == 1 ? 4 : 8;
+  const void *fn = c.dtype == PA_DTYPE_F32    ? pick_select<float>(c.head_size, warps)
+                   : c.dtype == PA_DTYPE_BF16 ? pick_select<__nv_bfloat16>(c.head_size, warps)
+                                              : pick_select<__half>(c.head_size, warps);
+  return host_launch(fn, (unsigned)(items * p.chunks), 1, warps * 32, smem, c.stream, args,
                      "launch select kernel");
 }
 
