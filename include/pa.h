@@ -415,7 +415,8 @@ pa_status_t pa_append_kv(void *key_cache, void *value_cache, void *key_bounds,
  * always, the others by their score, ties to the lower page, num_selected in
  * all; every page if there are no more than that.
  * The selection is the one that exact scores give (nearly equal ones are
- * computed again in fp64); a NaN score ranks lowest.
+ * computed again to 45 bits of the sum's magnitude); a NaN score ranks lowest,
+ * one beyond fp32's range as infinite.
  *
  * Rows: one a sequence (q_start NULL, num_rows = num_seqs, the row sees the
  * sequence's seq_lens keys), or chunks as in pa_chunks_forward (row i of a

@@ -78,7 +78,7 @@ struct SelectParams {
   int *counters;           // [rows * Hkv] finished chunks, zero between calls
   float *sizes;            // [rows * Hkv][chunks] largest sum of magnitudes
   uint32_t *keys;          // [rows * Hkv][max_pages] scores as ordered integers
-  double *fine;            // [rows * Hkv][max_pages] scores in fp64, where needed
+  uint64_t *fine;          // [rows * Hkv][max_pages] keys of scores in pairs, where needed
   int *status;
   int num_seqs, num_rows, num_heads, num_kv_heads, num_blocks;
   int block_size, log2_block_size, max_blocks_per_seq, max_seq_len, max_pages;

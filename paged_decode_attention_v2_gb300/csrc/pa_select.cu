@@ -17,7 +17,12 @@
 // as the sum over lanes of the largest a lane saw on any page.  Where the
 // scores on the two sides of the cut are more than 2 eps apart, the cut is
 // the exact one.  Else the pages within 2 eps of the last one in are scored
-// again in fp64, where products of 16-bit numbers are exact.
+// again in pairs of fp32 numbers: sums and products with their exact rounding
+// errors carried along (the two-sum and two-product of T. J. Dekker, "A
+// floating-point technique for extending the available precision", 1971), 45
+// bits and more of the sum of magnitudes.  (fp64 instructions run at a
+// sixty-fourth of fp32's rate on GB300: the same in fp64 took a warp 10 us at
+// D 128, 20 us at D 256.)
 //
 // Layout of the work: an item is one (row, KV head); its pages are cut into
 // chunks, one CTA each, so that a single long sequence fills the GPU; the CTA
@@ -52,12 +57,6 @@ __device__ __forceinline__ void widen(const uint4 &c, float (&f)[16 / sizeof(T)]
   } else {
     chunk_to_float_f16(c, f);
   }
-}
-
-// An order-preserving map of doubles (no NaN) to unsigned integers; -0 is 0.
-__device__ __forceinline__ unsigned long long order64(double x) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-  return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
 // The item's row: its sequence and the keys it sees (0: none, or bad input).
@@ -110,13 +109,13 @@ __device__ __forceinline__ float unorder32(uint32_t u) {
   return __uint_as_float((u >> 31) ? u ^ 0x80000000u : ~u);
 }
 
-// Marks of pages whose order fp64 decided, outside the range of any float.
+// Marks of pages whose order the second scoring decided, outside the range of any float.
 constexpr uint32_t kKeyIn = 0xffffffffu, kKeyOut = 0u;
 
 struct SelShared {
   float w[512];           // Q+ then Q-, 2 D numbers
-  double wide[512];       // the same in fp64, where it is needed
-  double fine[kSelList];
+  float wide[2][512];     // the same in pairs, where needed
+  uint64_t fine[kSelList];
   int list[kSelList];
   uint32_t mark[kSelList];
   int counts[32 * kSelMaxWarps];
@@ -168,52 +167,90 @@ __device__ __forceinline__ float block_max(float v, SelShared &sh) {
   return v;
 }
 
-// Q+ and Q- in fp64 (exact: at most 16 numbers), for rescoring.
-template <typename T, int D, int WARPS>
-__device__ __forceinline__ void wide_weights(const T *q, int G, SelShared &sh) {
-  for (int d = threadIdx.x; d < D; d += WARPS * 32) {
-    double qp = 0.0, qn = 0.0;
-#pragma unroll
-    for (int g = 0; g < 16; ++g) {
-      const double f = g < G ? (double)to_float(q[(size_t)g * D + d]) : 0.0;
-      if (f > 0.0) qp += f;
-      if (f < 0.0) qn += f;
-    }
-    sh.wide[d] = qp;
-    sh.wide[D + d] = qn;
+// A sum and the rounding errors of its additions.
+struct PairSum {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+    c += __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z));
+    s = t;
   }
-  __syncthreads();
-}
-// A page's score in fp64, by a warp (every lane gets it).
+  // renormalised, as an integer of the same order (NaN lowest)
+  __device__ __forceinline__ uint64_t key() const {
+    float h = __fadd_rn(s, c), l = __fsub_rn(c, __fsub_rn(h, s));
+    if (!(fabsf(s) <= 3.402823466e38f)) {  // beyond fp32: infinite, or NaN
+      h = s != s ? -CUDART_INF_F : s;
+      l = 0.f;
+    }
+    return (uint64_t)order32(h) << 32 | order32(l);
+  }
+};
+
+// Q+ and Q- in pairs, for rescoring, by the threads from `start` in steps of
+// `step`; the caller synchronises.  (What few items reach is kept in short
+// loops: there, code costs its fetch.)
 template <typename T, int D>
-__device__ __forceinline__ double fine_score(const SelectParams &p, int blk, int h, const SelShared &sh) {
-  if ((unsigned)blk >= (unsigned)p.num_blocks) return -CUDART_INF;
-  const T *b = static_cast<const T *>(p.key_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D;
-  double s = 0.0;
+__device__ __forceinline__ void wide_weights(const T *q, int G, SelShared &sh, int start, int step) {
+#pragma unroll 1
+  for (int d = start; d < D; d += step) {
+    PairSum qp, qn;
 #pragma unroll 4
-  for (int d = threadIdx.x & 31; d < 2 * D; d += 32) s += sh.wide[d] * (double)to_float(b[d]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  return s != s ? -CUDART_INF : s;
+    for (int g = 0; g < G; ++g) {
+      const float f = to_float(q[(size_t)g * D + d]);
+      qp.add(fmaxf(f, 0.f));
+      qn.add(fminf(f, 0.f));
+    }
+    sh.wide[0][d] = qp.s;
+    sh.wide[1][d] = qp.c;
+    sh.wide[0][D + d] = qn.s;
+    sh.wide[1][D + d] = qn.c;
+  }
 }
-// The m pages listed in sh.list scored in fp64 and the `more` best of them (ties
+// A page's score in pairs, by a warp (every lane gets its key).
+template <typename T, int D>
+__device__ __forceinline__ uint64_t fine_score(const SelectParams &p, int blk, int h, const SelShared &sh) {
+  PairSum a;
+  if ((unsigned)blk >= (unsigned)p.num_blocks) {
+    a.s = -CUDART_INF_F;
+    return a.key();
+  }
+  const T *b = static_cast<const T *>(p.key_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D;
+#pragma unroll 4
+  for (int d = threadIdx.x & 31; d < 2 * D; d += 32) {
+    const float f = to_float(b[d]), w = sh.wide[0][d];
+    const float prod = __fmul_rn(w, f);
+    a.add(prod);
+    a.c += fmaf(sh.wide[1][d], f, fmaf(w, f, -prod));
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const float s2 = __shfl_xor_sync(0xffffffffu, a.s, d);
+    const float c2 = __shfl_xor_sync(0xffffffffu, a.c, d);
+    a.c = __fadd_rn(a.c, c2);
+    a.add(s2);
+  }
+  return a.key();
+}
+// The m pages listed in sh.list scored in pairs and the `more` best of them (ties
 // to the lower page) marked, kKeyIn or kKeyOut, in sh.mark.
 template <typename T, int D, int WARPS>
 __device__ __forceinline__ void rescore_list(const SelectParams &p, const T *q, const int32_t *bt, int h,
                                              int G, int m, int more, SelShared &sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  wide_weights<T, D, WARPS>(q, G, sh);  // its barrier also publishes the list
+  wide_weights<T, D>(q, G, sh, tid, WARPS * 32);
+  __syncthreads();  // (also publishes the list)
+#pragma unroll 1
   for (int j = warp; j < m; j += WARPS) {
-    const double s = fine_score<T, D>(p, __ldg(bt + sh.list[j]), h, sh);
+    const uint64_t s = fine_score<T, D>(p, __ldg(bt + sh.list[j]), h, sh);
     if (lane == 0) sh.fine[j] = s;
   }
   __syncthreads();
   for (int j0 = tid; j0 < m; j0 += WARPS * 32) {
-    const double s = sh.fine[j0];
+    const uint64_t s = sh.fine[j0];
     const int i = sh.list[j0];
     int rank = 0;
     for (int j = 0; j < m; ++j) {
-      const double t = sh.fine[j];
+      const uint64_t t = sh.fine[j];
       rank += t > s || (t == s && sh.list[j] < i);
     }
     sh.mark[j0] = rank < more ? kKeyIn : kKeyOut;
@@ -298,13 +335,13 @@ __device__ __forceinline__ bool select_in_registers(const SelectParams &p, const
     if (m <= kSelList) {
 #pragma unroll
       for (int v = 0; v < REGS; ++v) {
-          if (key[v] >= lo && key[v] <= hi)
+        if (key[v] >= lo && key[v] <= hi)
           sh.list[atomicAdd(&sh.count, 1)] = first + tid + v * THREADS;
       }
       rescore_list<T, D, WARPS>(p, q, bt, h, G, m, more, sh);
 #pragma unroll
       for (int v = 0; v < REGS; ++v) {
-          if (key[v] >= lo && key[v] <= hi)
+        if (key[v] >= lo && key[v] <= hi)
           for (int j = 0; j < m; ++j)
             if (sh.list[j] == first + tid + v * THREADS) {
               key[v] = sh.mark[j];
@@ -565,39 +602,22 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
           }
           const int more = need - __reduce_add_sync(0xffffffffu, c);
           if (m <= 32) {
-            double wp[D / 32], wn[D / 32];
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-              wp[d] = wn[d] = 0.0;
-#pragma unroll 8
-              for (int g = 0; g < G; ++g) {
-                const double f = (double)to_float(q[(size_t)g * D + lane + 32 * d]);
-                if (f > 0.0) wp[d] += f;
-                if (f < 0.0) wn[d] += f;
-              }
-            }
-            double score = 0.0;
+            wide_weights<T, D>(q, G, sh, lane, 32);
+            __syncwarp();
+            uint64_t score = 0;
+#pragma unroll 1
             for (int j = 0; j < m; ++j) {
-              const int blk = __ldg(bt + first + __shfl_sync(0xffffffffu, mine, j));
-              double sum = -CUDART_INF;
-              if ((unsigned)blk < (unsigned)p.num_blocks) {
-                const T *b = static_cast<const T *>(p.key_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D;
-                sum = 0.0;
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-                  sum += wp[d] * (double)to_float(b[lane + 32 * d]) +
-                         wn[d] * (double)to_float(b[D + lane + 32 * d]);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (sum != sum) sum = -CUDART_INF;
-              }
-              if (lane == j) score = sum;
+              const uint64_t t =
+                  fine_score<T, D>(p, __ldg(bt + first + __shfl_sync(0xffffffffu, mine, j)), h, sh);
+              if (lane == j) score = t;
             }
             int rank = 0;
+#pragma unroll 1
             for (int j = 0; j < m; ++j) {
-              const double t = __shfl_sync(0xffffffffu, score, j);
+              const uint64_t t = __shfl_sync(0xffffffffu, score, j);
               rank += t > score || (t == score && j < lane);  // in page order already
             }
+#pragma unroll 1
             for (int j = 0; j < m; ++j) {
               const int i = __shfl_sync(0xffffffffu, mine, j);
               const uint32_t mark = __shfl_sync(0xffffffffu, rank, j) < more ? kKeyIn : kKeyOut;
@@ -664,7 +684,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       const float tau = unorder32(ka);
       if (!(have == need && tau - unorder32(kb) > 2.f * eps)) {
         // Pages above hi are in, pages below lo out; those between (all of
-        // them, if eps is not finite) are scored again in fp64.
+        // them, if eps is not finite) are scored again in pairs.
         const float fhi = tau + 2.f * eps, flo = tau - 2.f * eps;
         const uint32_t hi = fhi == fhi ? order32(fhi) : kKeyIn - 1;
         const uint32_t lo = flo == flo ? order32(flo) : kKeyOut + 1;
@@ -683,32 +703,33 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
           rescore_list<T, D, WARPS>(p, q, bt, h, G, m, more, sh);
           for (int j = tid; j < m; j += THREADS) kc[sh.list[j]] = sh.mark[j];
         } else {
-          double *gfine = p.fine + (size_t)item * p.max_pages;
-          wide_weights<T, D, WARPS>(q, G, sh);
+          uint64_t *gfine = p.fine + (size_t)item * p.max_pages;
+          wide_weights<T, D>(q, G, sh, tid, THREADS);
+          __syncthreads();
           for (int i = first + warp; i < last; i += WARPS) {
             if (kc[i] > hi || kc[i] < lo) continue;
-            const double s = fine_score<T, D>(p, __ldg(bt + i), h, sh);
+            const uint64_t s = fine_score<T, D>(p, __ldg(bt + i), h, sh);
             if (lane == 0) gfine[i] = s;
           }
           __syncthreads();
           // the more-th largest by bisection, then its ties in page order
-          unsigned long long t = 0;
+          uint64_t t = 0;
           for (int b = 63; b >= 0; --b) {
-            const unsigned long long mid = t | (1ull << b);
+            const uint64_t mid = t | (1ull << b);
             int cnt = 0;
             for (int i = first + tid; i < last; i += THREADS)
-              if (kc[i] >= lo && kc[i] <= hi) cnt += order64(gfine[i]) >= mid;
+              if (kc[i] >= lo && kc[i] <= hi) cnt += gfine[i] >= mid;
             if (block_sum<WARPS>(cnt, sh, turn) >= more) t = mid;
           }
           int cnt = 0;
           for (int i = first + tid; i < last; i += THREADS)
-            if (kc[i] >= lo && kc[i] <= hi) cnt += order64(gfine[i]) > t;
+            if (kc[i] >= lo && kc[i] <= hi) cnt += gfine[i] > t;
           int ties = more - block_sum<WARPS>(cnt, sh, turn);
           if (warp == 0) {
             for (int i0 = first; i0 < last; i0 += 32) {
               const int i = i0 + lane;
               const bool in = i < last && kc[i] >= lo && kc[i] <= hi;
-              const unsigned long long u = in ? order64(gfine[i]) : 0;
+              const uint64_t u = in ? gfine[i] : 0;
               const unsigned eq = __ballot_sync(0xffffffffu, in && u == t);
               const bool keep = in && (u > t || (u == t && __popc(eq & ((1u << lane) - 1u)) < ties));
               ties = max(0, ties - __popc(eq));
@@ -909,7 +930,7 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
   p.counters = reinterpret_cast<int *>(ws + lay.counters);
   p.sizes = reinterpret_cast<float *>(ws + lay.sizes);
   p.keys = reinterpret_cast<uint32_t *>(ws + lay.keys);
-  p.fine = reinterpret_cast<double *>(ws + lay.fine);
+  p.fine = reinterpret_cast<uint64_t *>(ws + lay.fine);
   p.status = reinterpret_cast<int *>(ws);
   p.num_seqs = c.num_seqs;
   p.num_rows = c.num_rows;
