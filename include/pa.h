@@ -358,7 +358,8 @@ pa_status_t pa_v2_forward_noalloc(void *out, const void *query,
  * with q_start NULL there is one row a sequence (num_rows = num_seqs), its
  * last token, and a sequence of length 0 is an empty slot, skipped.  seq_lens
  * are the lengths AFTER the append.  Rows from q_start[num_seqs] on are
- * padding: nothing of theirs is read, and their query_out is left as it was.
+ * padding: they need no positions, nothing is appended for them, and their
+ * query_out is left as it was.
  *
  *   key, value         [num_rows][num_kv_heads][head_size]; rows key_stride /
  *                      value_stride elements apart (16-byte multiples), so

@@ -155,8 +155,15 @@ def _check(status: int, what: str) -> int:
     return status
 
 
+# The current stream's handle without the Stream object (3 us a call) where torch
+# offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -332,26 +339,27 @@ def _check_call(dtype, device, same, ints) -> None:
         raise ValueError(f"unsupported dtype {dtype}")
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"tensors on {device}: libpa runs on the current CUDA device")
+    index = device.index
     for t in same:
-        if t is not None and (t.dtype != dtype or t.device != device):
+        if t is not None and (t.dtype is not dtype or t.get_device() != index):
             raise ValueError("libpa takes caches, queries and outputs of one dtype on one device")
     for t in ints:
-        if t is not None and (t.dtype != torch.int32 or t.device != device):
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != index):
             raise ValueError("libpa takes int32 tables, lengths and starts on the caches' device")
 
 
 def _rows(t, heads: int, head_size: int):
     """(pointer, elements between rows) of a [rows, heads, head_size] tensor whose
     rows are contiguous."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size:
+    if t.dim() != 3:
         raise ValueError(f"expected [rows, {heads}, {head_size}], got {list(t.shape)}")
-    if t.is_contiguous() or t.shape[0] < 2:
-        if not t[:1].is_contiguous():
-            raise ValueError("libpa takes rows of contiguous heads")
-        return t.data_ptr(), heads * head_size
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_size):
+    rows, h, d = t.shape
+    if h != heads or d != head_size:
+        raise ValueError(f"expected [rows, {heads}, {head_size}], got {list(t.shape)}")
+    step, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError("libpa takes rows of contiguous heads")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), step if rows > 1 else h * d
 
 
 def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, workspace,
@@ -402,7 +410,7 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
         max_seq_len = block_tables.shape[1] * bs
     kp, kst = _rows(key, hkv, D)
     vp, vst = _rows(value, hkv, D)
-    _check(load_library().pa_append_kv(
+    _check((_lib or load_library()).pa_append_kv(
         _ptr(key_cache), _ptr(value_cache), _ptr(key_bounds), qop, qp, kp, vp, qst, kst, vst,
         _ptr(cos_sin), _ptr(positions), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R,
         H, hkv, D, nb, bs, block_tables.shape[1], int(max_seq_len), int(rotary_dim or 0),
@@ -457,7 +465,7 @@ def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens
         max_prefix_len = prefix_tables.shape[1] * bs
     opts = pa_options_t(PA_VARIANT_V2, PA_MATH_AUTO, num_stages, debug_flags, wait_limit_ns, None,
                         ctas_per_sm, 0, 0)
-    _check(load_library().pa_prefix_forward(
+    _check((_lib or load_library()).pa_prefix_forward(
         _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
         _ptr(seq_lens), _ptr(prefix_tables), _ptr(prefix_lens), _ptr(prefix_start), B, G, H, hkv,
         D, nb, bs, block_tables.shape[1], prefix_tables.shape[1], int(max_seq_len),
@@ -513,7 +521,7 @@ def pa_select_blocks(selected, query, key_bounds, block_tables, seq_lens, block_
     R, H, D, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * block_size
-    _check(load_library().pa_select_blocks(
+    _check((_lib or load_library()).pa_select_blocks(
         _ptr(selected), _ptr(query), _ptr(key_bounds), _ptr(block_tables), _ptr(seq_lens),
         _ptr(q_start), B, R, H, hkv, D, nb, block_size, block_tables.shape[1], int(max_seq_len),
         selected.shape[2], sink_blocks, recent_blocks, int(partition_size), _DTYPES[query.dtype],
@@ -543,7 +551,7 @@ def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables
         raise ValueError("num_selected or a selected tensor is needed")
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * bs
-    _check(load_library().pa_sparse_forward(
+    _check((_lib or load_library()).pa_sparse_forward(
         _ptr(out), _ptr(selected), _ptr(query), _ptr(key_cache), _ptr(value_cache),
         _ptr(key_bounds), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R, H, hkv, D, nb,
         bs, block_tables.shape[1], int(max_seq_len), int(num_selected), sink_blocks, recent_blocks,

@@ -11,14 +11,19 @@
 // A thread's unit of work is two 16-byte chunks of a head that hold both
 // halves of its pairs (half-split: chunk u and the one rotary_dim / 2 further
 // on; adjacent pairs: chunks 2u and 2u + 1), so no pair crosses threads.  A
-// CTA takes a tile of rows: all its threads rotate the rows' queries, and its
+// CTA takes up to four rows: all its threads rotate the rows' queries, and its
 // warps take the (page, KV head) pairs whose first appended token is one of
 // its rows.  So exactly one warp touches a page's bounds: they need no
 // atomics, and the result does not depend on the order of anything.
 //
-// Bound: bytes (each input read once, each output written once); a decode
-// step's are a few MB or less, where the launch and one dependent chain of
-// loads (lengths, table, key) are all there is.
+// Bound: bytes (each input read once, each output written once): 8946 ragged
+// prompt rows (32/4 heads, D 128, bf16, with bounds), 189 MB, take 34.9 us,
+// 5.4 TB/s, 0.80 of the copy peak.  A decode step's bytes are a few MB or
+// less; there the launch and one dependent chain of loads (lengths, table,
+// key) are all there is: 3.2 us for one row, 3.9 us for 256, one launch after
+// another.  So what can be is read before a row is located: its queries, and
+// its keys and values as far as L2.  A row is found in q_start by a warp, 32
+// entries at a time.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -30,8 +35,9 @@
 namespace pa {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendHeads = 4;  // of a row's queries, a thread
 
 template <typename T>
 struct Chunk2 {  // two 16-byte chunks
@@ -71,82 +77,124 @@ __device__ __forceinline__ void unit_chunks(int u, int rot, bool interleaved, in
   }
 }
 
-// Rotate a unit in place (fp32 arithmetic, one rounding); cs: the row's
-// [cos | sin] of rotary_dim / 2 angles each.
+// The cosines and sines of a unit's angles; cs: the row's [cos | sin] of
+// `half` angles each.
+template <int N>
+struct Angles {
+  float c[N], s[N];
+  __device__ __forceinline__ void load(const float *cs, int u, int half) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 cv = __ldg(reinterpret_cast<const float4 *>(cs + u * N + i));
+      const float4 sv = __ldg(reinterpret_cast<const float4 *>(cs + half + u * N + i));
+      c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
+      s[i] = sv.x, s[i + 1] = sv.y, s[i + 2] = sv.z, s[i + 3] = sv.w;
+    }
+  }
+};
+
+// Rotate a unit in place (fp32 arithmetic, one rounding).
 template <typename T>
-__device__ __forceinline__ void rotate_unit(Chunk2<T> &x, const float *cs, int u, int half,
+__device__ __forceinline__ void rotate_unit(Chunk2<T> &x, const Angles<Chunk2<T>::N> &r,
                                             bool interleaved) {
   constexpr int N = Chunk2<T>::N;
-  float c[N], s[N];
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 cv = __ldg(reinterpret_cast<const float4 *>(cs + u * N + i));
-    const float4 sv = __ldg(reinterpret_cast<const float4 *>(cs + half + u * N + i));
-    c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
-    s[i] = sv.x, s[i + 1] = sv.y, s[i + 2] = sv.z, s[i + 3] = sv.w;
-  }
   float a[N], b[N], ya[N], yb[N];
   widen<T>(x.a, a);
   widen<T>(x.b, b);
   if (!interleaved) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      ya[i] = a[i] * c[i] - b[i] * s[i];
-      yb[i] = b[i] * c[i] + a[i] * s[i];
+      ya[i] = a[i] * r.c[i] - b[i] * r.s[i];
+      yb[i] = b[i] * r.c[i] + a[i] * r.s[i];
     }
   } else {
     // pairs (0,1), (2,3) ... of the 2N consecutive elements; pair j has angle j
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) {
-      ya[2 * j] = a[2 * j] * c[j] - a[2 * j + 1] * s[j];
-      ya[2 * j + 1] = a[2 * j + 1] * c[j] + a[2 * j] * s[j];
-      yb[2 * j] = b[2 * j] * c[N / 2 + j] - b[2 * j + 1] * s[N / 2 + j];
-      yb[2 * j + 1] = b[2 * j + 1] * c[N / 2 + j] + b[2 * j] * s[N / 2 + j];
+      ya[2 * j] = a[2 * j] * r.c[j] - a[2 * j + 1] * r.s[j];
+      ya[2 * j + 1] = a[2 * j + 1] * r.c[j] + a[2 * j] * r.s[j];
+      yb[2 * j] = b[2 * j] * r.c[N / 2 + j] - b[2 * j + 1] * r.s[N / 2 + j];
+      yb[2 * j + 1] = b[2 * j + 1] * r.c[N / 2 + j] + b[2 * j] * r.s[N / 2 + j];
     }
   }
   x.a = narrow<T>(ya);
   x.b = narrow<T>(yb);
 }
 
+// Element-wise maximum (minimum) of the words of stored keys: one fp32 value
+// or two 16-bit ones a word, NaN passed over.
+template <typename T>
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 r = __hmax2(*reinterpret_cast<const T2 *>(&a), *reinterpret_cast<const T2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t word_min(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 r = __hmin2(*reinterpret_cast<const T2 *>(&a), *reinterpret_cast<const T2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  }
+}
+// -inf in every element of a word (its sign flipped: +inf)
+template <typename T>
+__device__ __forceinline__ uint32_t word_low() {
+  return sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+}
+
 // A row's sequence, token and chunk end; false: nothing to do for it (a
 // padding row, an empty slot) or bad input (reported).
 struct RowInfo {
   int seq, tok, tok_end;  // tok_end: the chunk's end, L
+  bool starts;            // its chunk's first row
 };
+// (by a warp, for one row)
 __device__ __forceinline__ bool locate_row(const AppendParams &p, int row, RowInfo &o) {
+  const int lane = threadIdx.x & 31;
   int s = row, i = 0, n = 1;
   if (p.q_start) {
-    if (row < __ldg(p.q_start)) {  // rows before the first chunk: q_start[0] must be 0
-      report(p.status, kStatusBadInput);
-      return false;
-    }
-    int lo = 0, hi = p.num_seqs + 1;  // the first entry above row
+    // the first of q_start's entries above row, 32 tried at a time
+    int lo = 0, hi = p.num_seqs + 1;  // it is in [lo, hi]
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.q_start + mid) > row)
-        hi = mid;
-      else
-        lo = mid + 1;
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + lane * step;
+      const unsigned above = __ballot_sync(0xffffffffu, at < hi && __ldg(p.q_start + min(at, hi - 1)) > row);
+      const int f = above ? __ffs(above) - 1 : 32;  // lanes below f are not above
+      const int last = min(f, (hi - lo + step - 1) / step);  // lanes tried and not above
+      if (f < 32) hi = lo + f * step;
+      if (last > 0) lo = lo + (last - 1) * step + 1;
     }
     if (lo > p.num_seqs) return false;  // behind the last sequence
+    if (lo == 0) {                      // before the first chunk: q_start[0] must be 0
+      if (lane == 0) report(p.status, kStatusBadInput);
+      return false;
+    }
     s = lo - 1;
     const int q0 = __ldg(p.q_start + s), q1 = __ldg(p.q_start + lo);
     i = row - q0;
     n = q1 - q0;
     if (q0 < 0 || i < 0 || i >= n || q1 > p.num_rows) {  // decreasing, or past the rows
-      report(p.status, kStatusBadInput);
+      if (lane == 0) report(p.status, kStatusBadInput);
       return false;
     }
   }
   const int L = __ldg(p.seq_lens + s);
   if (!p.q_start && L == 0) return false;  // an empty slot of a decode batch
   if (L < n || L > p.max_seq_len) {
-    report(p.status, kStatusBadInput);
+    if (lane == 0) report(p.status, kStatusBadInput);
     return false;
   }
   o.seq = s;
   o.tok = L - n + i;
   o.tok_end = L;
+  o.starts = i == 0;
   return true;
 }
 
@@ -163,15 +211,14 @@ __device__ __forceinline__ int row_position(const AppendParams &p, int row, int 
 }  // namespace
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 6)
     pa_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int N = Chunk2<T>::N;             // elements of a 16-byte chunk
   constexpr int UNITS = D / (2 * N);          // units of a head
   constexpr int LANES = 32 / UNITS;           // tokens a warp takes at a time
   __shared__ int s_pos[kAppendMaxRows];       // -1: no work for the row
-  __shared__ int s_task_row[kAppendMaxRows];  // rows that start a page of their chunk
+  __shared__ bool s_first[kAppendMaxRows];    // the row starts a page of its chunk
   __shared__ RowInfo s_row[kAppendMaxRows];
-  __shared__ int s_tasks;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * p.tile_rows;
@@ -179,39 +226,82 @@ __global__ void __launch_bounds__(kAppendThreads)
   const bool il = p.interleaved != 0;
   const int rot = p.rotary_dim / (2 * N), half = p.rotary_dim / 2;
 
+  // keys and values on their way to L2 while the rows are located
+  {
+    const int lines = p.num_kv_heads * D * (int)sizeof(T) / 128;  // of a row
+    for (int i = threadIdx.x; i < 2 * rows * lines; i += kAppendThreads) {
+      const int r = i / 2 / lines;
+      const T *src = static_cast<const T *>(i & 1 ? p.value : p.key) +
+                     (row0 + r) * (i & 1 ? p.value_stride : p.key_stride);
+      prefetch_l2(reinterpret_cast<const char *>(src) + (i / 2 - r * lines) * 128);
+    }
+  }
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (warp == 0) {
+
+  // queries: a thread takes its unit of kAppendHeads heads of a row, whose
+  // angles it loads once; the first ones are read while the rows are located
+  const int u = threadIdx.x % UNITS;
+  int ca, cb;
+  unit_chunks(u, rot, il, ca, cb);
+  const int groups = (p.num_heads + kAppendHeads - 1) / kAppendHeads;
+  const int queries = p.query ? rows * groups : 0;
+  Chunk2<T> q[kAppendHeads];  // query_out may be the query: no read-only path
+  auto load_queries = [&](int j) {
+    const int lr = j / groups, h0 = (j - lr * groups) * kAppendHeads;
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) +
+                                                       (row0 + lr) * p.query_stride + (size_t)h0 * D);
+#pragma unroll
+    for (int e = 0; e < kAppendHeads; ++e)
+      if (h0 + e < p.num_heads) q[e] = {src[e * (D / N) + ca], src[e * (D / N) + cb]};
+  };
+  int j = threadIdx.x / UNITS;
+  if (j < queries) load_queries(j);
+
+  if (warp < rows) {
+    RowInfo o;
+    int pos = -1;
     bool first = false;
-    if (lane < rows) {
-      RowInfo o;
-      int pos = -1;
-      if (locate_row(p, row0 + lane, o)) {
-        pos = row_position(p, row0 + lane, o.tok);
-        // the first row of its chunk, or a page's first token (the chunk's
-        // first row is row - (tok - (L - n)): its predecessor is another's)
-        first = o.tok % p.block_size == 0;
-        if (!first) {
-          const int q0 = p.q_start ? __ldg(p.q_start + o.seq) : row0 + lane;
-          first = q0 == row0 + lane;
-        }
-        s_row[lane] = o;
-      }
-      s_pos[lane] = pos;
+    if (locate_row(p, row0 + warp, o)) {
+      pos = row_position(p, row0 + warp, o.tok);
+      first = o.starts || o.tok % p.block_size == 0;  // the first token of its page here
+      if (lane == 0) s_row[warp] = o;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, first);
-    if (first) s_task_row[__popc(m & ((1u << lane) - 1u))] = lane;
-    if (lane == 0) s_tasks = __popc(m);
+    if (lane == 0) {
+      s_pos[warp] = pos;
+      s_first[warp] = first;
+    }
   }
   __syncthreads();
 
+  while (j < queries) {
+    const int lr = j / groups, h0 = (j - lr * groups) * kAppendHeads;
+    const int pos = s_pos[lr];
+    if (pos >= 0) {
+      if (u < rot) {
+        Angles<N> r;
+        r.load(p.cos_sin + (size_t)pos * p.rotary_dim, u, half);
+#pragma unroll
+        for (int e = 0; e < kAppendHeads; ++e) rotate_unit(q[e], r, il);
+      }
+      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.query_out) +
+                                             ((size_t)(row0 + lr) * p.num_heads + h0) * D);
+#pragma unroll
+      for (int e = 0; e < kAppendHeads; ++e)
+        if (h0 + e < p.num_heads) {
+          dst[e * (D / N) + ca] = q[e].a;
+          dst[e * (D / N) + cb] = q[e].b;
+        }
+    }
+    j += kAppendThreads / UNITS;
+    if (j < queries) load_queries(j);
+  }
+
   // keys and values: a warp takes one page of one KV head
-  const int u = lane % UNITS, tl = lane / UNITS;
-  int ca, cb;
-  unit_chunks(u, rot, il, ca, cb);
-  const int tasks = s_tasks * p.num_kv_heads;
-  for (int task = warp; task < tasks; task += kAppendWarps) {
-    const int lr = s_task_row[task / p.num_kv_heads], h = task % p.num_kv_heads;
+  const int tl = lane / UNITS;
+  for (int task = warp; task < rows * p.num_kv_heads; task += kAppendWarps) {
+    const int lr = task / p.num_kv_heads, h = task - lr * p.num_kv_heads;
+    if (!s_first[lr]) continue;
     const RowInfo o = s_row[lr];
     const int page = o.tok >> p.log2_block_size;
     const int blk = __ldg(p.block_tables + (size_t)o.seq * p.max_blocks_per_seq + page);
@@ -224,17 +314,25 @@ __global__ void __launch_bounds__(kAppendThreads)
     const size_t slot0 = ((size_t)blk * p.num_kv_heads + h) * p.block_size + off0;
     uint4 *kdst = reinterpret_cast<uint4 *>(static_cast<T *>(p.key_cache) + slot0 * D);
     uint4 *vdst = reinterpret_cast<uint4 *>(static_cast<T *>(p.value_cache) + slot0 * D);
-    float hi[2 * N], lo[2 * N];
+    // the page's bounds so far, in words of the stored type
+    uint32_t hi[8], lo[8];
     uint4 *bnd = nullptr;
     if (p.key_bounds) {
       bnd = reinterpret_cast<uint4 *>(static_cast<T *>(p.key_bounds) +
                                       ((size_t)blk * p.num_kv_heads + h) * 2 * D);
 #pragma unroll
-      for (int e = 0; e < 2 * N; ++e) {
-        hi[e] = -CUDART_INF_F;
-        lo[e] = CUDART_INF_F;
+      for (int e = 0; e < 8; ++e) {
+        hi[e] = word_low<T>();
+        lo[e] = word_low<T>() ^ (sizeof(T) == 4 ? 0x80000000u : 0x80008000u);
       }
     }
+    auto join = [&](const uint4 &x, const uint4 &y, int e) {  // words e .. e + 3 of both
+      hi[e] = word_max<T>(hi[e], x.x), lo[e] = word_min<T>(lo[e], y.x);
+      hi[e + 1] = word_max<T>(hi[e + 1], x.y), lo[e + 1] = word_min<T>(lo[e + 1], y.y);
+      hi[e + 2] = word_max<T>(hi[e + 2], x.z), lo[e + 2] = word_min<T>(lo[e + 2], y.z);
+      hi[e + 3] = word_max<T>(hi[e + 3], x.w), lo[e + 3] = word_min<T>(lo[e + 3], y.w);
+    };
+#pragma unroll 1
     for (int i = tl; i < n; i += LANES) {
       const int row = row0 + lr + i;
       const int pos = row_position(p, row, o.tok + i);
@@ -245,75 +343,38 @@ __global__ void __launch_bounds__(kAppendThreads)
                                                         row * p.value_stride + (size_t)h * D);
       Chunk2<T> k{__ldg(ks + ca), __ldg(ks + cb)};
       const Chunk2<T> v{__ldg(vs + 2 * u), __ldg(vs + 2 * u + 1)};
-      if (u < rot) rotate_unit(k, p.cos_sin + (size_t)pos * p.rotary_dim, u, half, il);
+      if (u < rot) {
+        Angles<N> r;
+        r.load(p.cos_sin + (size_t)pos * p.rotary_dim, u, half);
+        rotate_unit(k, r, il);
+      }
       kdst[i * (D / N) + ca] = k.a;
       kdst[i * (D / N) + cb] = k.b;
       vdst[i * (D / N) + 2 * u] = v.a;
       vdst[i * (D / N) + 2 * u + 1] = v.b;
       if (bnd) {
-        float f[N];
-        widen<T>(k.a, f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          hi[e] = fmaxf(hi[e], f[e]);
-          lo[e] = fminf(lo[e], f[e]);
-        }
-        widen<T>(k.b, f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          hi[N + e] = fmaxf(hi[N + e], f[e]);
-          lo[N + e] = fminf(lo[N + e], f[e]);
-        }
+        join(k.a, k.a, 0);
+        join(k.b, k.b, 4);
       }
     }
     if (!bnd) continue;
 #pragma unroll
     for (int d = UNITS; d < 32; d <<= 1)
 #pragma unroll
-      for (int e = 0; e < 2 * N; ++e) {
-        hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
-        lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+      for (int e = 0; e < 8; ++e) {
+        hi[e] = word_max<T>(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
+        lo[e] = word_min<T>(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
       }
     if (tl == 0) {
-      float ha[N], hb[N], la[N], lb[N];
       if (off0 > 0) {  // the page held tokens before: their bounds join
-        widen<T>(bnd[ca], ha);
-        widen<T>(bnd[cb], hb);
-        widen<T>(bnd[D / N + ca], la);
-        widen<T>(bnd[D / N + cb], lb);
+        join(bnd[ca], bnd[D / N + ca], 0);
+        join(bnd[cb], bnd[D / N + cb], 4);
       }
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        ha[e] = off0 > 0 ? fmaxf(hi[e], ha[e]) : hi[e];
-        hb[e] = off0 > 0 ? fmaxf(hi[N + e], hb[e]) : hi[N + e];
-        la[e] = off0 > 0 ? fminf(lo[e], la[e]) : lo[e];
-        lb[e] = off0 > 0 ? fminf(lo[N + e], lb[e]) : lo[N + e];
-      }
-      bnd[ca] = narrow<T>(ha);
-      bnd[cb] = narrow<T>(hb);
-      bnd[D / N + ca] = narrow<T>(la);
-      bnd[D / N + cb] = narrow<T>(lb);
+      bnd[ca] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      bnd[cb] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+      bnd[D / N + ca] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      bnd[D / N + cb] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
     }
-  }
-
-  // queries: a thread keeps its unit of the head, over the tile's rows and heads
-  if (!p.query) return;
-  const int qu = threadIdx.x % UNITS;
-  unit_chunks(qu, rot, il, ca, cb);
-  const int total = rows * p.num_heads;
-  for (int j = threadIdx.x / UNITS; j < total; j += kAppendThreads / UNITS) {
-    const int lr = j / p.num_heads, h = j - lr * p.num_heads;
-    const int pos = s_pos[lr];
-    if (pos < 0) continue;
-    const int row = row0 + lr;
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) +
-                                                       row * p.query_stride + (size_t)h * D);
-    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.query_out) +
-                                           ((size_t)row * p.num_heads + h) * D);
-    Chunk2<T> q{src[ca], src[cb]};  // query_out may be the query: no read-only path
-    if (qu < rot) rotate_unit(q, p.cos_sin + (size_t)pos * p.rotary_dim, qu, half, il);
-    dst[ca] = q.a;
-    dst[cb] = q.b;
   }
 }
 
@@ -404,10 +465,11 @@ extern "C" pa_status_t pa_append_kv(
   int sms = 0;
   st = host_sm_count(&sms);
   if (st != PA_OK) return st;
-  // One row a CTA until every SM has four, then larger tiles, whose rows
-  // share the CTA's start-up.
+  // One row a CTA until every SM has four, then up to four, which share the
+  // CTA's start-up (8193 rows: 48.7 us with one, 39.1 with two, 36.1 with
+  // four, 36.6 with eight; 256 rows: 4.4 us with one, 6.2 with four).
   p.tile_rows = 1;
-  while (p.tile_rows < kAppendMaxRows / 2 && num_rows > 4ll * sms * p.tile_rows) p.tile_rows *= 2;
+  while (p.tile_rows < kAppendMaxRows && num_rows > 4ll * sms * p.tile_rows) p.tile_rows *= 2;
   const void *fn = dtype == PA_DTYPE_F32    ? pick_head<float>(head_size)
                    : dtype == PA_DTYPE_BF16 ? pick_head<__nv_bfloat16>(head_size)
                                             : pick_head<__half>(head_size);

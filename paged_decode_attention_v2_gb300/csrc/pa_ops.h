@@ -8,7 +8,7 @@
 
 namespace pa {
 
-constexpr int kAppendMaxRows = 32;  // rows of a CTA's tile, one lane each
+constexpr int kAppendMaxRows = 4;  // rows of a CTA
 
 struct AppendParams {
   void *key_cache, *value_cache;  // [num_blocks][Hkv][bs][D]
