@@ -400,9 +400,11 @@ __device__ __forceinline__ bool select_in_registers(const SelectParams &p, const
 // Dynamic shared memory: the keys (order32 of the scores) of p.smem_pages
 // pages.
 template <typename T, int D, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 4 ? 8 : 3)
     pa_select_kernel(const __grid_constant__ SelectParams p) {
-  // (32 warps an SM: at most 64 registers a thread)
+  // (at most 64 registers a thread with four warps, whose items should all be
+  // resident; 80 with eight, which hold more keys: 61 against 65 us a call for
+  // 64 sequences of up to 4096 pages at D 256)
   constexpr int THREADS = WARPS * 32;
   constexpr int N = 16 / (int)sizeof(T);       // elements of a 16-byte piece
   constexpr int PIECES = 2 * D / N;            // of a page's bounds
@@ -470,16 +472,23 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       for (int e = 0; e < N; ++e) w[v][e] = sh.w[(v * LPP + lp) * N + e];
     float size = 0.f;  // the largest sum |Q| |bound| of this lane's part of a page
     const int c_end = min(n, (chunk + 1) * p.chunk_pages);
-    for (int p0 = chunk * p.chunk_pages + warp * SEG; p0 < c_end; p0 += WARPS * SEG) {
-      int blk = -1;  // also past the chunk: those lanes load nothing
-      if (lane < SEG && p0 + lane < c_end) {
-        blk = __ldg(bt + p0 + lane);
-        if ((unsigned)blk >= (unsigned)p.num_blocks) {
-          report(p.status, kStatusBadInput);
-          blk = -1;
-        }
+    constexpr int STEPS = SEG / PPW;
+    // the page whose score this lane ends up with (below), of the warp's SEG
+    constexpr int SPLIT = STEPS == 8 ? 3 : STEPS == 4 ? 2 : STEPS == 2 ? 1 : 0;
+    const int my_page = (lp >> (LPP == 32 ? 5 - SPLIT : 4 - SPLIT)) * PPW + lane / LPP;
+    const bool my_turn = (lp & ((LPP >> SPLIT) - 1)) == 0;
+    auto entry = [&](int p0) -> int {  // -1 past the chunk: those lanes load nothing
+      return lane < SEG && p0 + lane < c_end ? __ldg(bt + p0 + lane) : -1;
+    };
+    const int p_first = chunk * p.chunk_pages + warp * SEG;
+    int next = entry(p_first);
+    for (int p0 = p_first; p0 < c_end; p0 += WARPS * SEG) {
+      int blk = next;
+      next = entry(p0 + WARPS * SEG);
+      if ((unsigned)blk >= (unsigned)p.num_blocks) {
+        if (lane < SEG && p0 + lane < c_end) report(p.status, kStatusBadInput);
+        blk = -1;
       }
-      constexpr int STEPS = SEG / PPW;
       float acc[STEPS];
       uint4 x[STEPS][VPL];
 #pragma unroll
@@ -507,19 +516,24 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         }
         size = fmaxf(size, mag);
       }
+      // The sums over a page's lanes, the STEPS pages' together: halves of the
+      // lanes exchange halves of the pages until each holds one.
+      int off = LPP / 2;
 #pragma unroll
-      for (int d = LPP / 2; d > 0; d >>= 1)
+      for (int c = STEPS / 2; c > 0; c >>= 1) {
+        const bool up = (lane & off) != 0;
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], d);
-      // lane j PPW + i takes the score of that page
-      float mine = 0.f;
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        const float t = __shfl_sync(0xffffffffu, acc[j], (lane % PPW) * LPP);
-        if (lane / PPW == j) mine = t;
+        for (int j = 0; j < c; ++j) {
+          const float give = up ? acc[j] : acc[j + c];
+          acc[j] = (up ? acc[j + c] : acc[j]) + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+        off >>= 1;
       }
-      if (lane < SEG && p0 + lane < c_end)
-        kc[p0 + lane] = order32(blk < 0 || mine != mine ? -CUDART_INF_F : mine);
+#pragma unroll
+      for (int d = LPP >> (SPLIT + 1); d > 0; d >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], d);
+      const int b = __shfl_sync(0xffffffffu, blk, my_page);
+      if (my_turn && p0 + my_page < c_end)
+        kc[p0 + my_page] = order32(b < 0 || acc[0] != acc[0] ? -CUDART_INF_F : acc[0]);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) size += __shfl_xor_sync(0xffffffffu, size, d);
@@ -952,14 +966,14 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
                        (unsigned)((items + 3) / 4), 1, 128, 0, c.stream, args,
                        "launch given-blocks kernel");
   // One CTA an item if that gives every SM four.  Otherwise chunks of at
-  // least 64 pages (a round of the CTA's warps) towards sixteen an SM: with
-  // lengths of all kinds in a batch, a long sequence's chunks are what the
-  // last SMs wait for (64 sequences of up to 4096 pages, D 256: 49 us at four
-  // an SM).
+  // least 64 pages (a round of the CTA's warps) towards 32 an SM: with lengths
+  // of all kinds in a batch, a long sequence's chunks are what the last SMs
+  // wait for (64 sequences of up to 4096 pages, D 256, a call: 77 us at eight
+  // an SM, 65 at 16, 63 at 32, 67 at 64).
   p.chunks = 1;
   p.chunk_pages = lay.max_pages > 0 ? lay.max_pages : 1;
   if (items < 4ll * sms) {
-    long long want = (16ll * sms + items - 1) / items;
+    long long want = (32ll * sms + items - 1) / items;
     const long long most = (lay.max_pages + 63) / 64;
     if (want > most) want = most;
     if (want > kSelMaxChunks) want = kSelMaxChunks;
