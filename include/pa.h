@@ -431,8 +431,9 @@ pa_status_t pa_append_kv(void *key_cache, void *value_cache, void *key_bounds,
  * 0 <= sink_blocks, 1 <= recent_blocks, sink_blocks + recent_blocks <=
  * num_selected.  query, block_tables, seq_lens and the limits on sizes as in
  * pa_forward, f32 included; query contiguous [num_rows][num_heads][head_size].
- * The workspace holds pa_sparse_workspace_bytes(...) bytes, zeroed once by
- * pa_workspace_init; partition_size is the one it was sized with.  A bad table
+ * The workspace holds pa_sparse_workspace_bytes(...) bytes, initialised once by
+ * pa_workspace_init (one sized for the largest call serves smaller ones too);
+ * partition_size is the one it was sized with.  A bad table
  * entry, length or chunk is reported as PA_ERR_DEVICE_BAD_INPUT: a page with a
  * bad entry scores lowest, a row with a bad length selects nothing. */
 pa_status_t pa_select_blocks(int32_t *selected, const void *query,
@@ -497,7 +498,8 @@ size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
  * bound (0 if no sequence has any).  Sequences with no tokens at all get
  * zeros.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); the other arguments and
  * limits as pa_v2_forward.  The workspace holds pa_prefix_workspace_bytes(...)
- * bytes, zeroed once by pa_workspace_init.  Bad tables, lengths or groups are
+ * bytes, initialised once by pa_workspace_init (any workspace that is large
+ * enough serves calls of any shape, one after another).  Bad tables, lengths or groups are
  * reported as PA_ERR_DEVICE_BAD_INPUT; the rows in question then hold no
  * meaningful values.  opts as in pa_forward (variant V2 or auto; no fused
  * combine, no CUDA-core path). */

@@ -157,13 +157,14 @@ def _check(status: int, what: str) -> int:
 
 # The current stream's handle without the Stream object (3 us a call) where torch
 # offers it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               if hasattr(torch._C, "_cuda_getDevice") else None)
 
 
 def _stream_handle(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -332,7 +333,7 @@ def pa_chunks_forward(out, query, key_cache, value_cache, block_tables, seq_lens
         ctypes.byref(opts)), "pa_chunks_forward")
 
 
-def _check_call(dtype, device, same, ints) -> None:
+def _check_call(dtype, device, workspace, same, ints) -> None:
     """Every tensor on the current CUDA device, `same` of one dtype, `ints` int32
     (None entries are absent arguments)."""
     if dtype not in _DTYPES:
@@ -340,6 +341,8 @@ def _check_call(dtype, device, same, ints) -> None:
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"tensors on {device}: libpa runs on the current CUDA device")
     index = device.index
+    if workspace.get_device() != index:
+        raise ValueError("the workspace is on another device than the tensors")
     for t in same:
         if t is not None and (t.dtype is not dtype or t.get_device() != index):
             raise ValueError("libpa takes caches, queries and outputs of one dtype on one device")
@@ -349,8 +352,8 @@ def _check_call(dtype, device, same, ints) -> None:
 
 
 def _rows(t, heads: int, head_size: int):
-    """(pointer, elements between rows) of a [rows, heads, head_size] tensor whose
-    rows are contiguous."""
+    """(pointer, elements between rows, rows) of a [rows, heads, head_size] tensor
+    whose rows are contiguous."""
     if t.dim() != 3:
         raise ValueError(f"expected [rows, {heads}, {head_size}], got {list(t.shape)}")
     rows, h, d = t.shape
@@ -359,7 +362,7 @@ def _rows(t, heads: int, head_size: int):
     step, s1, s2 = t.stride()
     if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError("libpa takes rows of contiguous heads")
-    return t.data_ptr(), step if rows > 1 else h * d
+    return t.data_ptr(), step if rows > 1 else h * d, rows
 
 
 def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, workspace,
@@ -371,34 +374,40 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
     and query [rows, H, D] rotated into query_out; key_bounds [num_blocks, Hkv,
     2, D] follows the keys (see include/pa.h).  seq_lens are the lengths after
     the append.  rotary_dim defaults to cos_sin's width."""
-    nb, hkv, bs, D = key_cache.shape
-    _check_call(key_cache.dtype, key_cache.device,
+    shape = key_cache.shape
+    nb, hkv, bs, D = shape
+    dtype = key_cache.dtype
+    _check_call(dtype, key_cache.device, workspace,
                 (value_cache, key, value, query, query_out, key_bounds),
                 (block_tables, seq_lens, q_start, positions))
-    R = key.shape[0]
+    kp, kst, R = _rows(key, hkv, D)
+    vp, vst, rows = _rows(value, hkv, D)
     B = seq_lens.numel()
-    if value_cache.shape != key_cache.shape or value.shape[0] != R:
+    if value_cache.shape != shape or rows != R:
         raise ValueError("key and value (and their caches) differ in shape")
     if q_start is not None and q_start.numel() != B + 1:
         raise ValueError("q_start must be int32 [num_seqs + 1]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if block_tables.dim() != 2 or len(block_tables) != B:
         raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    blocks = block_tables.shape[1]
     if positions is not None and positions.numel() != R:
         raise ValueError("positions must be int32 [rows]")
     if key_bounds is not None and key_bounds.shape != (nb, hkv, 2, D):
         raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
     H, qp, qst, qop = hkv, 0, 0, 0
     if query is not None:
-        if query_out is None or query_out.shape != query.shape or query.shape[0] != R:
+        if query.dim() != 3 or query_out is None or query_out.shape != query.shape:
             raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
         H = query.shape[1]
-        qp, qst = _rows(query, H, D)
+        qp, qst, rows = _rows(query, H, D)
+        if rows != R:
+            raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
         qop = _ptr(query_out)
     elif query_out is not None:
         raise ValueError("query_out without a query")
     max_position = 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.device != key_cache.device \
+        if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != key_cache.get_device() \
                 or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
         max_position, width = cos_sin.shape
@@ -407,15 +416,13 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
         if rotary_dim not in (0, width):
             raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
     if max_seq_len is None:
-        max_seq_len = block_tables.shape[1] * bs
-    kp, kst = _rows(key, hkv, D)
-    vp, vst = _rows(value, hkv, D)
+        max_seq_len = blocks * bs
     _check((_lib or load_library()).pa_append_kv(
         _ptr(key_cache), _ptr(value_cache), _ptr(key_bounds), qop, qp, kp, vp, qst, kst, vst,
         _ptr(cos_sin), _ptr(positions), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R,
-        H, hkv, D, nb, bs, block_tables.shape[1], int(max_seq_len), int(rotary_dim or 0),
-        int(interleaved), max_position, _DTYPES[key_cache.dtype], _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
+        H, hkv, D, nb, bs, blocks, int(max_seq_len), int(rotary_dim or 0), int(interleaved),
+        max_position, _DTYPES[dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "pa_append_kv")
 
 
 def pa_prefix_workspace_bytes(num_seqs: int, num_prefixes: int, num_heads: int, num_kv_heads: int,
@@ -449,7 +456,7 @@ def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens
     seq_lens are the sequences' own tokens."""
     B, H, D = query.shape
     nb, hkv, bs, D2 = key_cache.shape
-    _check_call(query.dtype, query.device, (out, key_cache, value_cache),
+    _check_call(query.dtype, query.device, workspace, (out, key_cache, value_cache),
                 (block_tables, seq_lens, prefix_tables, prefix_lens, prefix_start))
     G = prefix_lens.numel()
     if out.shape != query.shape or D2 != D or value_cache.shape != key_cache.shape:
@@ -517,7 +524,8 @@ def pa_select_blocks(selected, query, key_bounds, block_tables, seq_lens, block_
     """Choose the blocks that each (row, KV head) attends to from the pages' key
     bounds into selected, int32 [rows, Hkv, num_selected] (see include/pa.h)."""
     nb, hkv = key_bounds.shape[:2]
-    _check_call(query.dtype, query.device, (key_bounds,), (selected, block_tables, seq_lens, q_start))
+    _check_call(query.dtype, query.device, workspace, (key_bounds,),
+                (selected, block_tables, seq_lens, q_start))
     R, H, D, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * block_size
@@ -537,7 +545,7 @@ def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables
     are selected in the call and written to `selected` (None: not wanted, give
     num_selected); without, `selected` is read."""
     nb, hkv, bs, D = key_cache.shape
-    _check_call(query.dtype, query.device, (out, key_cache, value_cache, key_bounds),
+    _check_call(query.dtype, query.device, workspace, (out, key_cache, value_cache, key_bounds),
                 (selected, block_tables, seq_lens, q_start))
     R, H, D2, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
     if out.shape != query.shape or D2 != D or value_cache.shape != key_cache.shape \

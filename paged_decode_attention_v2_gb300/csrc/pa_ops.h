@@ -68,6 +68,10 @@ void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads
                  int max_seq_len, int max_prefix_len, int partition_size, int *split_tokens,
                  int *max_splits);
 
+// An item scored and selected from in one CTA, or scored by several and
+// selected from in a second launch.
+enum SelectMode { kSelBoth, kSelScore, kSelPick };
+
 struct SelectParams {
   const void *query;       // [rows][H][D]
   const void *key_bounds;  // [num_blocks][Hkv][2][D]
@@ -75,7 +79,6 @@ struct SelectParams {
   int32_t *selected;       // [rows][Hkv][num_selected] or null
   const int32_t *given;    // a given selection instead
   int32_t *table, *lens;   // the view's block table and lengths, or null
-  int *counters;           // [rows * Hkv] finished chunks, zero between calls
   float *sizes;            // [rows * Hkv][chunks] largest sum of magnitudes
   uint32_t *keys;          // [rows * Hkv][max_pages] scores as ordered integers
   uint64_t *fine;          // [rows * Hkv][max_pages] keys of scores in pairs, where needed
@@ -83,7 +86,8 @@ struct SelectParams {
   int num_seqs, num_rows, num_heads, num_kv_heads, num_blocks;
   int block_size, log2_block_size, max_blocks_per_seq, max_seq_len, max_pages;
   int num_selected, sinks, recent;
-  int chunks, chunk_pages;  // CTAs of an item, pages of each
+  int mode;                 // SelectMode
+  int chunks, chunk_pages;  // CTAs that score an item, pages of each
   int smem_pages;           // keys that the shared memory holds
 };
 

@@ -24,9 +24,11 @@
 // sixty-fourth of fp32's rate on GB300: the same in fp64 took a warp 10 us at
 // D 128, 20 us at D 256.)
 //
-// Layout of the work: an item is one (row, KV head); its pages are cut into
-// chunks, one CTA each, so that a single long sequence fills the GPU; the CTA
-// that finishes an item's last chunk selects.  The selected pages come out in
+// Layout of the work: an item is one (row, KV head).  Enough items: one CTA
+// scores an item's pages and selects.  Few: the pages are cut into chunks, one
+// CTA each, so that a single long sequence fills the GPU, and a second launch
+// selects, one CTA an item (no counters to keep at zero between calls, whose
+// shapes may change).  The selected pages come out in
 // page order with the last page last, as a block table of the view in which
 // every (row, KV head) is a sequence of one KV head: the attention kernels
 // then need nothing new.
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 4 ? 8 : 3)
   extern __shared__ __align__(16) uint32_t s_keys[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int item = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int parts = p.mode == kSelPick ? 1 : p.chunks;
+  const int item = blockIdx.x / parts, chunk = blockIdx.x % parts;
   const int row = item / p.num_kv_heads, h = item % p.num_kv_heads;
   const int G = p.num_heads / p.num_kv_heads;
 
@@ -437,18 +440,19 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 4 ? 8 : 3)
   const int32_t *bt = p.block_tables + (size_t)seq * p.max_blocks_per_seq;
   const int k = p.num_selected;
   const bool all = n <= k;
-  const int nch = all ? 1 : (n + p.chunk_pages - 1) / p.chunk_pages;
-  if (chunk >= nch) return;
+  const int nch = (n + p.chunk_pages - 1) / p.chunk_pages;
+  if (p.mode == kSelScore && (all || chunk >= nch)) return;
   const int first = p.sinks, last = n - p.recent;  // pages [first, last) go by their score
   const int need = k - p.sinks - p.recent;         // of them
   // the keys: in shared memory if the CTA scores them all and they fit
-  uint32_t *kc = p.chunks == 1 && n <= p.smem_pages ? s_keys : p.keys + (size_t)item * p.max_pages;
+  uint32_t *kc = p.mode == kSelBoth && n <= p.smem_pages ? s_keys : p.keys + (size_t)item * p.max_pages;
   int32_t *selected = p.selected ? p.selected + (size_t)item * k : nullptr;
   int32_t *table = p.table ? p.table + (size_t)item * k : nullptr;
   // where the chosen candidates' pages are listed, in page order
   int32_t *list = need <= kSelList ? sh.list : (table ? table : selected) + p.sinks;
 
-  if (!all) {
+  float size = 0.f;  // the largest sum |Q| |bound| of a page
+  if (!all && p.mode != kSelPick) {
     // ---- Q+ and Q-: the group's loads all in flight ----
     for (int d = tid; d < D; d += THREADS) {
       float qp = 0.f, qn = 0.f;
@@ -470,7 +474,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 4 ? 8 : 3)
     for (int v = 0; v < VPL; ++v)
 #pragma unroll
       for (int e = 0; e < N; ++e) w[v][e] = sh.w[(v * LPP + lp) * N + e];
-    float size = 0.f;  // the largest sum |Q| |bound| of this lane's part of a page
     const int c_end = min(n, (chunk + 1) * p.chunk_pages);
     constexpr int STEPS = SEG / PPW;
     // the page whose score this lane ends up with (below), of the warp's SEG
@@ -538,17 +541,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 4 ? 8 : 3)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) size += __shfl_xor_sync(0xffffffffu, size, d);
     size = block_max<WARPS>(size, sh);  // (its barriers also publish the keys)
-    if (p.chunks > 1) {
-      if (tid == 0) {
-        p.sizes[(size_t)item * p.chunks + chunk] = size;
-        sh.flag = atomic_add_acq_rel_gpu(p.counters + item, 1) == nch - 1;
-      }
-      __syncthreads();
-      if (!sh.flag) return;
-      if (tid == 0) p.counters[item] = 0;  // every chunk is in: ready for the next call
-      size = 0.f;
+    if (p.mode == kSelScore) {
+      if (tid == 0) p.sizes[(size_t)item * p.chunks + chunk] = size;
+      return;
+    }
+  }
+  if (!all) {
+    if (p.mode == kSelPick) {
       for (int c = tid; c < nch; c += THREADS)
-        size = fmaxf(size, __ldcg(p.sizes + (size_t)item * p.chunks + c));
+        size = fmaxf(size, p.sizes[(size_t)item * p.chunks + c]);
       size = block_max<WARPS>(size, sh);
     }
     const float eps = (float)(G + VPL * N + 7) * 5.9604644775390625e-8f * size + 1e-36f;
@@ -854,10 +855,10 @@ const void *pick_select(int head_size, int warps) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// The workspace: the attention's over the view, then table, lengths, counters
+// The workspace: the attention's over the view, then table, lengths
 // and what the selection keeps a page.
 struct SparseLayout {
-  size_t table, lens, counters, sizes, keys, fine, total;
+  size_t table, lens, sizes, keys, fine, total;
   int max_pages, view_len;
 };
 constexpr int kSelMaxChunks = 1024;  // of an item
@@ -877,8 +878,7 @@ bool sparse_layout(int num_rows, int num_heads, int num_kv_heads, int head_size,
   if (attn == 0) return false;
   o->table = align256(attn);
   o->lens = o->table + align256((size_t)items * num_selected * 4);
-  o->counters = o->lens + align256((size_t)items * 4);
-  o->sizes = o->counters + align256((size_t)items * 4);
+  o->sizes = o->lens + align256((size_t)items * 4);
   const int chunks = (o->max_pages + 63) / 64;
   o->keys = o->sizes + align256((size_t)items * (chunks < kSelMaxChunks ? chunks : kSelMaxChunks) * 4);
   o->fine = o->keys + align256((size_t)items * o->max_pages * 4);
@@ -941,7 +941,6 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
   p.given = c.given;
   p.table = table ? reinterpret_cast<int32_t *>(ws + lay.table) : nullptr;
   p.lens = table ? reinterpret_cast<int32_t *>(ws + lay.lens) : nullptr;
-  p.counters = reinterpret_cast<int *>(ws + lay.counters);
   p.sizes = reinterpret_cast<float *>(ws + lay.sizes);
   p.keys = reinterpret_cast<uint32_t *>(ws + lay.keys);
   p.fine = reinterpret_cast<uint64_t *>(ws + lay.fine);
@@ -987,13 +986,17 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
   const size_t smem = (size_t)p.smem_pages * 4;
   // Whole items: four warps, so that the items of a decode batch are all
   // resident at once (1024 items: one wave, where eight warps took two).
-  // Chunks: eight, for the CTA that selects from all of an item's pages.
+  // Chunks: eight, for the launch that selects from all of an item's pages.
   const int warps = p.chunks == 1 ? 4 : 8;
   const void *fn = c.dtype == PA_DTYPE_F32    ? pick_select<float>(c.head_size, warps)
                    : c.dtype == PA_DTYPE_BF16 ? pick_select<__nv_bfloat16>(c.head_size, warps)
                                               : pick_select<__half>(c.head_size, warps);
-  return host_launch(fn, (unsigned)(items * p.chunks), 1, warps * 32, smem, c.stream, args,
-                     "launch select kernel");
+  p.mode = p.chunks == 1 ? kSelBoth : kSelScore;
+  st = host_launch(fn, (unsigned)(items * p.chunks), 1, warps * 32, smem, c.stream, args,
+                   "launch select kernel");
+  if (st != PA_OK || p.chunks == 1) return st;
+  p.mode = kSelPick;
+  return host_launch(fn, (unsigned)items, 1, warps * 32, 0, c.stream, args, "launch select kernel");
 }
 
 }  // namespace

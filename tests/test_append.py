@@ -371,3 +371,30 @@ def test_captured_and_replayed_with_new_lengths():
         page = kc[bt[i, 0].long(), :, :n]
         assert torch.equal(kb[bt[i, 0].long(), :, 0], page.amax(1))
         assert torch.equal(kb[bt[i, 0].long(), :, 1], page.amin(1))
+
+
+@pytest.mark.gpu
+def test_cache_beyond_32_bits():
+    """Pages at the end of caches of more than 2^32 bytes."""
+    c = Case(16, torch.bfloat16, 4, 4, 128, 16, [40], [9], 128)
+    dev, blocks = "cuda", 300_000
+    pages = c.bt[0].long()
+    far = torch.arange(blocks - len(pages), blocks)
+    kc = torch.empty(blocks, 4, 16, 128, dtype=c.dtype, device=dev)
+    vc, kb = torch.empty_like(kc), torch.empty(blocks, 4, 2, 128, dtype=c.dtype, device=dev)
+    for t, s in ((kc, c.kc), (vc, c.vc), (kb, c.kb)):
+        t[far.cuda()] = s[pages].cuda()
+    q, k, v = c.split(c.qkv.to(dev))
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    pa.pa_append_kv(kc, vc, k, v, far.to(torch.int32)[None].cuda(),
+                    torch.tensor([49], dtype=torch.int32, device=dev), ws, key_bounds=kb,
+                    cos_sin=c.cs.to(dev), q_start=torch.tensor([0, 40], dtype=torch.int32, device=dev))
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    tok = torch.arange(9, 49)
+    ref, size = c.rotate(c.split(c.qkv)[1])
+    got = kc[far[tok // 16].cuda(), :, (tok % 16).cuda()].cpu()
+    c.check(got, ref, size, "far keys")
+    assert torch.equal(vc[far[tok // 16].cuda(), :, (tok % 16).cuda()].cpu(), c.split(c.qkv)[2])
+    for j, page in enumerate(far.tolist()):
+        held = kc[page, :, :min(16, 49 - 16 * j)]
+        assert torch.equal(kb[page, :, 0], held.amax(1)) and torch.equal(kb[page, :, 1], held.amin(1))

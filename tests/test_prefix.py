@@ -338,3 +338,57 @@ def test_captured_replayed_and_on_another_stream():
             g.replay()
             assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
             assert_close(d["out"], c.reference(), c.dtype, f"replay {prefix} {start}")
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_of_many_shapes():
+    """A workspace sized for the largest call serves calls of other shapes in
+    between; only its status block is initialised."""
+    cases = [Case(20, torch.bfloat16, 8, 2, 128, 16, [5, 9], [900, 1500], [7 * i for i in range(14)]),
+             Case(21, torch.float16, 4, 1, 64, 8, [1], [70], [900], P=256),
+             Case(22, torch.bfloat16, 4, 2, 256, 32, [30], [400], [i for i in range(30)], P=64)]
+    n = max(pa.pa_prefix_workspace_bytes(c.B, len(c.prefix), c.H, c.K, c.D, max(c.own), max(c.prefix), c.P)
+            for c in cases)
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    state = [(c, c.device(), c.reference()) for c in cases]
+    for _ in range(2):
+        for c, d, ref in state:
+            d["ws"] = ws
+            d["out"].fill_(math.nan)
+            c.run(d)
+            assert pa.pa_read_device_status(ws) == pa.PA_OK
+            assert_close(d["out"], ref, c.dtype, "shared workspace")
+
+
+@pytest.mark.gpu
+def test_cache_beyond_32_bits():
+    """Pages at the end of caches of more than 2^32 bytes."""
+    c = Case(23, torch.bfloat16, 8, 4, 128, 16, [3], [300], [5, 0, 33])
+    d = c.device()
+    blocks, pool = 300_000, c.kc.shape[0]
+    for name in ("kc", "vc"):
+        t = torch.empty((blocks,) + tuple(d[name].shape[1:]), dtype=c.dtype, device="cuda")
+        t[blocks - pool:] = d[name]
+        d[name] = t
+    for name in ("bt", "pt"):
+        d[name] = torch.where(d[name] >= 0, d[name] + (blocks - pool), -1).to(torch.int32)
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    assert_close(d["out"], c.reference(), c.dtype, "far pages")
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls with their own workspaces on two streams, overlapping."""
+    a = Case(24, torch.bfloat16, 16, 2, 128, 16, [60], [3000], [i for i in range(60)])
+    b = Case(25, torch.float16, 8, 1, 64, 16, [9, 30], [2000, 700], [3 * i for i in range(39)])
+    state = [(c, c.device(), c.reference(), torch.cuda.Stream()) for c in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, d, _, s in state:
+            c.run(d, stream=s)
+    torch.cuda.synchronize()
+    for c, d, ref, s in state:
+        assert pa.pa_read_device_status(d["ws"], s) == pa.PA_OK
+        assert_close(d["out"], ref, c.dtype, "two streams")

@@ -386,3 +386,49 @@ def test_captured_replayed_and_on_another_stream():
             assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
             assert torch.equal(d["sel"].cpu(), c2.select())
             assert_close(d["out"], c2.attend(c2.select()), c.dtype, f"replay {lens}")
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_of_many_shapes():
+    """A workspace sized for the largest call, used by calls of other shapes in
+    between (their layouts overlap each other's leftovers), on both the
+    whole-item and the cut path."""
+    cases = [Case(20, torch.bfloat16, 8, 2, 128, 16, [3000, 70, 5], 20, 1, 2),
+             Case(21, torch.float16, 4, 1, 64, 8, [9000, 100, 33, 8, 700], 7),
+             Case(22, torch.float32, 4, 2, 64, 16, [50], 2),
+             Case(23, torch.bfloat16, 4, 2, 64, 8, [40 + i for i in range(320)], 3)]
+    n = max(pa.pa_sparse_workspace_bytes(c.rows, c.H, c.K, c.D, c.bs, max(c.lens), c.k, c.P) for c in cases)
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0  # the status block alone is initialised
+    state = [(c, c.device(), c.select()) for c in cases]
+    want = [c.attend(sel) for c, _, sel in state]
+    for _ in range(2):
+        for (c, d, sel), out in zip(state, want):
+            d["ws"] = ws
+            d["sel"].fill_(99)
+            c.run(d)
+            assert pa.pa_read_device_status(ws) == pa.PA_OK
+            assert torch.equal(d["sel"].cpu(), sel)
+            assert_close(d["out"], out, c.dtype, "shared workspace")
+
+
+@pytest.mark.gpu
+def test_cache_beyond_32_bits():
+    """Pages at the end of caches of more than 2^32 bytes (and bounds of more
+    than 2^31), where 32-bit element or byte offsets would wrap."""
+    K, D, bs = 4, 128, 16
+    blocks = 300_000  # 4.9 GB a cache, 0.6 GB of bounds
+    c = Case(24, torch.bfloat16, 8, K, D, bs, [130], 4, 1, 1)
+    d = c.device()
+    pages = c.bt[0].long()
+    far = torch.arange(blocks - len(pages), blocks)
+    for name in ("kc", "vc", "kb"):
+        t = torch.empty((blocks,) + tuple(d[name].shape[1:]), dtype=c.dtype, device="cuda")
+        t[far.cuda()] = d[name][pages.cuda()]
+        d[name] = t
+    d["bt"] = far.to(torch.int32)[None].cuda()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    sel = c.select()
+    assert torch.equal(d["sel"].cpu(), sel)
+    assert_close(d["out"], c.attend(sel), c.dtype, "far pages")
