@@ -433,7 +433,8 @@ pa_status_t pa_append_kv(void *key_cache, void *value_cache, void *key_bounds,
  * pa_forward, f32 included; query contiguous [num_rows][num_heads][head_size].
  * The workspace holds pa_sparse_workspace_bytes(...) bytes, initialised once by
  * pa_workspace_init (one sized for the largest call serves smaller ones too);
- * partition_size is the one it was sized with.  A bad table
+ * partition_size is the one it was sized with, and the largest partition of
+ * the attention (with few rows the library takes smaller ones).  A bad table
  * entry, length or chunk is reported as PA_ERR_DEVICE_BAD_INPUT: a page with a
  * bad entry scores lowest, a row with a bad length selects nothing. */
 pa_status_t pa_select_blocks(int32_t *selected, const void *query,

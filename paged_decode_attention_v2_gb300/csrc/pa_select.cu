@@ -860,8 +860,21 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct SparseLayout {
   size_t table, lens, sizes, keys, fine, total;
   int max_pages, view_len;
+  int partition;  // of the view's attention
 };
 constexpr int kSelMaxChunks = 1024;  // of an item
+constexpr int kViewItems = 4 * 152;  // of the attention, four an SM
+
+// The partition of the view's attention: the caller's, halved while that still
+// gives at most four items an SM (32 rows of 4 KV heads, 48 blocks of 16: 29.9 us
+// a call in partitions of 256, 34.5 in 512, 31.0 in 128).
+int view_partition(long long items, int view_len, int partition_size, int block_size) {
+  int p = partition_size;
+  while (p % 2 == 0 && (p / 2) % 64 == 0 && (p / 2) % block_size == 0 && p / 2 < view_len &&
+         items * ((view_len + p / 2 - 1) / (p / 2)) <= kViewItems)
+    p /= 2;
+  return p;
+}
 
 bool sparse_layout(int num_rows, int num_heads, int num_kv_heads, int head_size, int block_size,
                    int max_seq_len, int num_selected, int partition_size, SparseLayout *o) {
@@ -873,9 +886,13 @@ bool sparse_layout(int num_rows, int num_heads, int num_kv_heads, int head_size,
   if (items > 0x7fffffffll || cap > 0x7fffffffll) return false;
   o->max_pages = (int)(((long long)max_seq_len + block_size - 1) / block_size);
   o->view_len = (int)(cap < max_seq_len ? cap : max_seq_len);
-  const size_t attn = pa_workspace_bytes((int)items, num_heads / num_kv_heads, head_size,
-                                         o->view_len, partition_size);
+  o->partition = view_partition(items, o->view_len, partition_size, block_size);
+  const int group = num_heads / num_kv_heads;
+  size_t attn = pa_workspace_bytes((int)items, group, head_size, o->view_len, o->partition);
   if (attn == 0) return false;
+  // never less than what a call with fewer rows, in smaller partitions, needs
+  const size_t few = pa_workspace_bytes(kViewItems, group, head_size, 1, 64);
+  if (attn < few) attn = few;
   o->table = align256(attn);
   o->lens = o->table + align256((size_t)items * num_selected * 4);
   o->sizes = o->lens + align256((size_t)items * 4);
@@ -1061,7 +1078,7 @@ pa_status_t pa_sparse_forward(void *out, int32_t *selected, const void *query,
   // The attention's own limits, before anything is enqueued: the view's items
   // fit its 31-bit counts.
   const long long items = (long long)num_rows * num_kv_heads;
-  const long long parts = (lay.view_len + partition_size - 1) / partition_size;
+  const long long parts = (lay.view_len + lay.partition - 1) / lay.partition;
   if (items * (parts > 0 ? parts : 1) >= (1ll << 31) || parts > (1 << 20))
     return PA_ERR_UNSUPPORTED;
   st = run_select(c, lay, true);
@@ -1071,7 +1088,7 @@ pa_status_t pa_sparse_forward(void *out, int32_t *selected, const void *query,
                     reinterpret_cast<const int32_t *>(ws + lay.table),
                     reinterpret_cast<const int32_t *>(ws + lay.lens), (int)items,
                     num_heads / num_kv_heads, 1, head_size, num_blocks * num_kv_heads, block_size,
-                    num_selected, lay.view_len, scale, partition_size, dtype, workspace,
+                    num_selected, lay.view_len, scale, lay.partition, dtype, workspace,
                     lay.table, stream, nullptr);
 }
 
