@@ -522,7 +522,9 @@ pa_status_t pa_prefix_forward(void *out, const void *query,
 
 /* Bytes of workspace for pa_prefix_forward (0 on bad arguments): as
  * pa_workspace_bytes with slots for the prefix's splits, which the library
- * chooses from these sizes, behind every row's own partitions. */
+ * chooses from these sizes, behind every row's own partitions.  Fewer
+ * sequences may get more splits: a workspace for batches of several sizes is
+ * the largest of their needs. */
 size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads,
                                  int num_kv_heads, int head_size,
                                  int max_seq_len, int max_prefix_len,

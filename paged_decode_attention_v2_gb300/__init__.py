@@ -157,14 +157,14 @@ def _check(status: int, what: str) -> int:
 
 # The current stream's handle without the Stream object (3 us a call) where torch
 # offers it.
-_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
-               if hasattr(torch._C, "_cuda_getDevice") else None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_handle(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch._C._cuda_getDevice())
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -333,29 +333,36 @@ def pa_chunks_forward(out, query, key_cache, value_cache, block_tables, seq_lens
         ctypes.byref(opts)), "pa_chunks_forward")
 
 
-def _check_call(dtype, device, workspace, same, ints) -> None:
-    """Every tensor on the current CUDA device, `same` of one dtype, `ints` int32
-    (None entries are absent arguments)."""
+def _pointers(first, workspace, same, ints):
+    """Data pointers of the workspace, of `same` (tensors of first's dtype) and of
+    `ints` (int32), in this order, 0 for None; all contiguous, on the current CUDA
+    device."""
+    dtype = first.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}: libpa runs on the current CUDA device")
-    index = device.index
-    if workspace.get_device() != index:
-        raise ValueError("the workspace is on another device than the tensors")
-    for t in same:
-        if t is not None and (t.dtype is not dtype or t.get_device() != index):
-            raise ValueError("libpa takes caches, queries and outputs of one dtype on one device")
-    for t in ints:
-        if t is not None and (t.dtype is not torch.int32 or t.get_device() != index):
-            raise ValueError("libpa takes int32 tables, lengths and starts on the caches' device")
+    index = first.get_device()
+    if index < 0 or index != _current_device():
+        raise ValueError(f"tensors on {first.device}: libpa runs on the current CUDA device")
+    out = []
+    for want, tensors in ((workspace.dtype, (workspace,)), (dtype, same), (torch.int32, ints)):
+        for t in tensors:
+            if t is None:
+                out.append(0)
+                continue
+            if t.dtype is not want or t.get_device() != index:
+                raise ValueError("libpa takes tensors of one dtype, and int32 tables, lengths and "
+                                 "starts, on one device")
+            if not t.is_contiguous():
+                raise ValueError("libpa takes contiguous tensors")
+            out.append(t.data_ptr())
+    return out
 
 
-def _rows(t, heads: int, head_size: int):
+def _rows(t, like, heads: int, head_size: int):
     """(pointer, elements between rows, rows) of a [rows, heads, head_size] tensor
-    whose rows are contiguous."""
-    if t.dim() != 3:
-        raise ValueError(f"expected [rows, {heads}, {head_size}], got {list(t.shape)}")
+    whose rows are contiguous, of the dtype and on the device of `like`."""
+    if t.dim() != 3 or t.dtype is not like.dtype or t.get_device() != like.get_device():
+        raise ValueError("libpa takes [rows, heads, head_size] tensors of the caches' dtype and device")
     rows, h, d = t.shape
     if h != heads or d != head_size:
         raise ValueError(f"expected [rows, {heads}, {head_size}], got {list(t.shape)}")
@@ -376,53 +383,50 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
     the append.  rotary_dim defaults to cos_sin's width."""
     shape = key_cache.shape
     nb, hkv, bs, D = shape
-    dtype = key_cache.dtype
-    _check_call(dtype, key_cache.device, workspace,
-                (value_cache, key, value, query, query_out, key_bounds),
-                (block_tables, seq_lens, q_start, positions))
-    kp, kst, R = _rows(key, hkv, D)
-    vp, vst, rows = _rows(value, hkv, D)
+    ws, kc, vc, kb, qo, bt, sl, qs, pos = _pointers(
+        key_cache, workspace, (key_cache, value_cache, key_bounds, query_out),
+        (block_tables, seq_lens, q_start, positions))
+    kp, kst, R = _rows(key, key_cache, hkv, D)
+    vp, vst, rows = _rows(value, key_cache, hkv, D)
     B = seq_lens.numel()
     if value_cache.shape != shape or rows != R:
         raise ValueError("key and value (and their caches) differ in shape")
-    if q_start is not None and q_start.numel() != B + 1:
+    if qs and q_start.numel() != B + 1:
         raise ValueError("q_start must be int32 [num_seqs + 1]")
-    if block_tables.dim() != 2 or len(block_tables) != B:
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
     blocks = block_tables.shape[1]
-    if positions is not None and positions.numel() != R:
+    if pos and positions.numel() != R:
         raise ValueError("positions must be int32 [rows]")
-    if key_bounds is not None and key_bounds.shape != (nb, hkv, 2, D):
+    if kb and key_bounds.shape != (nb, hkv, 2, D):
         raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
-    H, qp, qst, qop = hkv, 0, 0, 0
+    H, qp, qst = hkv, 0, 0
     if query is not None:
         if query.dim() != 3 or query_out is None or query_out.shape != query.shape:
             raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
         H = query.shape[1]
-        qp, qst, rows = _rows(query, H, D)
+        qp, qst, rows = _rows(query, key_cache, H, D)
         if rows != R:
             raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
-        qop = _ptr(query_out)
     elif query_out is not None:
         raise ValueError("query_out without a query")
-    max_position = 0
+    cs, max_position = 0, 0
     if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != key_cache.get_device() \
-                or cos_sin.dim() != 2:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 \
+                or cos_sin.get_device() != key_cache.get_device():
             raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
         max_position, width = cos_sin.shape
         if rotary_dim is None:
             rotary_dim = width
-        if rotary_dim not in (0, width):
+        elif rotary_dim != width and rotary_dim != 0:
             raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+        cs = _ptr(cos_sin)
     if max_seq_len is None:
         max_seq_len = blocks * bs
     _check((_lib or load_library()).pa_append_kv(
-        _ptr(key_cache), _ptr(value_cache), _ptr(key_bounds), qop, qp, kp, vp, qst, kst, vst,
-        _ptr(cos_sin), _ptr(positions), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R,
-        H, hkv, D, nb, bs, blocks, int(max_seq_len), int(rotary_dim or 0), int(interleaved),
-        max_position, _DTYPES[dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream_handle(stream)), "pa_append_kv")
+        kc, vc, kb, qo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv, D, nb, bs,
+        blocks, max_seq_len, rotary_dim or 0, interleaved, max_position, _DTYPES[key_cache.dtype],
+        ws, workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
 
 
 def pa_prefix_workspace_bytes(num_seqs: int, num_prefixes: int, num_heads: int, num_kv_heads: int,
@@ -456,8 +460,9 @@ def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens
     seq_lens are the sequences' own tokens."""
     B, H, D = query.shape
     nb, hkv, bs, D2 = key_cache.shape
-    _check_call(query.dtype, query.device, workspace, (out, key_cache, value_cache),
-                (block_tables, seq_lens, prefix_tables, prefix_lens, prefix_start))
+    ws, o, q, kc, vc, bt, sl, pt, pl, ps = _pointers(
+        query, workspace, (out, query, key_cache, value_cache),
+        (block_tables, seq_lens, prefix_tables, prefix_lens, prefix_start))
     G = prefix_lens.numel()
     if out.shape != query.shape or D2 != D or value_cache.shape != key_cache.shape:
         raise ValueError("query and out, or the caches, differ in shape")
@@ -466,19 +471,18 @@ def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens
     if prefix_tables.dim() != 2 or prefix_tables.shape[0] != G or prefix_start.numel() != G + 1:
         raise ValueError("prefix_tables must be int32 [num_prefixes, max_prefix_blocks], "
                          "prefix_start int32 [num_prefixes + 1]")
+    blocks, pblocks = block_tables.shape[1], prefix_tables.shape[1]
     if max_seq_len is None:
-        max_seq_len = block_tables.shape[1] * bs
+        max_seq_len = blocks * bs
     if max_prefix_len is None:
-        max_prefix_len = prefix_tables.shape[1] * bs
+        max_prefix_len = pblocks * bs
     opts = pa_options_t(PA_VARIANT_V2, PA_MATH_AUTO, num_stages, debug_flags, wait_limit_ns, None,
                         ctas_per_sm, 0, 0)
     _check((_lib or load_library()).pa_prefix_forward(
-        _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
-        _ptr(seq_lens), _ptr(prefix_tables), _ptr(prefix_lens), _ptr(prefix_start), B, G, H, hkv,
-        D, nb, bs, block_tables.shape[1], prefix_tables.shape[1], int(max_seq_len),
-        int(max_prefix_len), float(scale), int(partition_size), _DTYPES[query.dtype],
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream),
-        ctypes.byref(opts)), "pa_prefix_forward")
+        o, q, kc, vc, bt, sl, pt, pl, ps, B, G, H, hkv, D, nb, bs, blocks, pblocks, max_seq_len,
+        max_prefix_len, scale, partition_size, _DTYPES[query.dtype], ws,
+        workspace.numel() * workspace.element_size(), _stream_handle(stream), ctypes.byref(opts)),
+        "pa_prefix_forward")
 
 
 def pa_sparse_workspace_bytes(num_rows: int, num_heads: int, num_kv_heads: int, head_size: int,
@@ -509,11 +513,9 @@ def _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start,
         raise ValueError("q_start must be int32 [num_seqs + 1]")
     if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
-    if selected is not None and (selected.dim() != 3 or selected.shape[0] != R
-                                 or selected.shape[1] != hkv):
+    if selected is not None and (selected.dim() != 3 or selected.shape[:2] != (R, hkv)):
         raise ValueError("selected must be int32 [rows, num_kv_heads, num_selected]")
-    if key_bounds is not None and (key_bounds.dim() != 4 or key_bounds.shape[1] != hkv
-                                   or key_bounds.shape[2] != 2 or key_bounds.shape[3] != D):
+    if key_bounds is not None and (key_bounds.dim() != 4 or key_bounds.shape[1:] != (hkv, 2, D)):
         raise ValueError("key_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
     return R, H, D, B
 
@@ -524,17 +526,15 @@ def pa_select_blocks(selected, query, key_bounds, block_tables, seq_lens, block_
     """Choose the blocks that each (row, KV head) attends to from the pages' key
     bounds into selected, int32 [rows, Hkv, num_selected] (see include/pa.h)."""
     nb, hkv = key_bounds.shape[:2]
-    _check_call(query.dtype, query.device, workspace, (key_bounds,),
-                (selected, block_tables, seq_lens, q_start))
+    ws, q, kb, sel, bt, sl, qs = _pointers(query, workspace, (query, key_bounds),
+                                           (selected, block_tables, seq_lens, q_start))
     R, H, D, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * block_size
     _check((_lib or load_library()).pa_select_blocks(
-        _ptr(selected), _ptr(query), _ptr(key_bounds), _ptr(block_tables), _ptr(seq_lens),
-        _ptr(q_start), B, R, H, hkv, D, nb, block_size, block_tables.shape[1], int(max_seq_len),
-        selected.shape[2], sink_blocks, recent_blocks, int(partition_size), _DTYPES[query.dtype],
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream)),
-        "pa_select_blocks")
+        sel, q, kb, bt, sl, qs, B, R, H, hkv, D, nb, block_size, block_tables.shape[1], max_seq_len,
+        selected.shape[2], sink_blocks, recent_blocks, partition_size, _DTYPES[query.dtype], ws,
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_select_blocks")
 
 
 def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables, seq_lens, scale,
@@ -545,11 +545,12 @@ def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables
     are selected in the call and written to `selected` (None: not wanted, give
     num_selected); without, `selected` is read."""
     nb, hkv, bs, D = key_cache.shape
-    _check_call(query.dtype, query.device, workspace, (out, key_cache, value_cache, key_bounds),
-                (selected, block_tables, seq_lens, q_start))
+    ws, o, q, kc, vc, kb, sel, bt, sl, qs = _pointers(
+        query, workspace, (out, query, key_cache, value_cache, key_bounds),
+        (selected, block_tables, seq_lens, q_start))
     R, H, D2, B = _sparse_shapes(selected, query, key_bounds, block_tables, seq_lens, q_start, hkv)
     if out.shape != query.shape or D2 != D or value_cache.shape != key_cache.shape \
-            or (key_bounds is not None and key_bounds.shape[0] != nb):
+            or (kb and key_bounds.shape[0] != nb):
         raise ValueError("query and out, or the caches and their bounds, differ in shape")
     if selected is not None:
         if num_selected not in (None, selected.shape[2]):
@@ -557,13 +558,12 @@ def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables
         num_selected = selected.shape[2]
     elif num_selected is None:
         raise ValueError("num_selected or a selected tensor is needed")
+    blocks = block_tables.shape[1]
     if max_seq_len is None:
-        max_seq_len = block_tables.shape[1] * bs
+        max_seq_len = blocks * bs
     _check((_lib or load_library()).pa_sparse_forward(
-        _ptr(out), _ptr(selected), _ptr(query), _ptr(key_cache), _ptr(value_cache),
-        _ptr(key_bounds), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), B, R, H, hkv, D, nb,
-        bs, block_tables.shape[1], int(max_seq_len), int(num_selected), sink_blocks, recent_blocks,
-        float(scale), int(partition_size), _DTYPES[query.dtype], _ptr(workspace),
+        o, sel, q, kc, vc, kb, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks, max_seq_len,
+        num_selected, sink_blocks, recent_blocks, scale, partition_size, _DTYPES[query.dtype], ws,
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_sparse_forward")
 
 

@@ -878,6 +878,17 @@ bool device_view(void *host, void **dev) {
   return true;
 }
 
+// Workspace of a shared-prefix call with `splits` splits of the prefix: V2's,
+// with as many slots more a row, and the rows' slot counts (0: too large).
+size_t prefix_bytes(int num_seqs, int num_heads, int head_size, int max_seq_len,
+                    int partition_size, int splits) {
+  const long long parts = (long long)max_parts_of(max_seq_len, partition_size) + splits;
+  if (parts > kMaxReduceParts || parts * partition_size > INT_MAX - partition_size) return 0;
+  return pa_workspace_bytes(num_seqs, num_heads, head_size, (int)parts * partition_size,
+                            partition_size) +
+         align256((size_t)num_seqs * 4);
+}
+
 // Enqueue the kernel that copies pa_forward_host's inputs (three segments:
 // lengths, block tables, queries) from mapped host memory into staging.
 pa_status_t stage_in(const void *s0, void *d0, size_t b0, const void *s1, void *d1, size_t b1,
@@ -1122,11 +1133,7 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, 
   int split = 0, splits = 0;
   prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
               max_prefix_len, partition_size, &split, &splits);
-  const long long parts = (long long)max_parts_of(max_seq_len, partition_size) + splits;
-  if (parts > kMaxReduceParts || parts * partition_size > INT_MAX - partition_size) return 0;
-  return pa_workspace_bytes(num_seqs, num_heads, head_size, (int)parts * partition_size,
-                            partition_size) +
-         align256((size_t)num_seqs * 4);
+  return prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, splits);
 }
 
 pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cache,
@@ -1165,9 +1172,8 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   int split = 0, splits = 0;
   prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
               max_prefix_len, partition_size, &split, &splits);
-  const size_t need = pa_prefix_workspace_bytes(num_seqs, num_prefixes, num_heads, num_kv_heads,
-                                                head_size, max_seq_len, max_prefix_len,
-                                                partition_size);
+  const size_t need =
+      prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, splits);
   if (need == 0) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
   if (num_seqs == 0) return PA_OK;
