@@ -380,8 +380,8 @@ pa_status_t pa_v2_forward_noalloc(void *out, const void *query,
  * head_size) turn in pairs, in fp32 with one rounding to dtype:
  * y1 = x1 cos - x2 sin, y2 = x2 cos + x1 sin, the pairs being (j, j +
  * rotary_dim / 2) with interleaved = 0, (2j, 2j + 1) with 1; the rest and the
- * values are copied.  A page's bounds start anew with its first token and
- * otherwise only widen: tokens overwritten later (rejected drafts) leave
+ * values are copied.  A page's bounds start anew with its first token (so they
+ * are kept from there on or not at all) and otherwise only widen: tokens overwritten later (rejected drafts) leave
  * theirs in, so the bounds then still hold but are wider than need be.  NaN
  * keys are passed over.
  *

@@ -425,7 +425,7 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
         max_seq_len = blocks * bs
     _check((_lib or load_library()).pa_append_kv(
         kc, vc, kb, qo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv, D, nb, bs,
-        blocks, max_seq_len, rotary_dim or 0, interleaved, max_position, _DTYPES[key_cache.dtype],
+        blocks, int(max_seq_len), int(rotary_dim or 0), int(interleaved), max_position, _DTYPES[key_cache.dtype],
         ws, workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
 
 
@@ -479,8 +479,8 @@ def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens
     opts = pa_options_t(PA_VARIANT_V2, PA_MATH_AUTO, num_stages, debug_flags, wait_limit_ns, None,
                         ctas_per_sm, 0, 0)
     _check((_lib or load_library()).pa_prefix_forward(
-        o, q, kc, vc, bt, sl, pt, pl, ps, B, G, H, hkv, D, nb, bs, blocks, pblocks, max_seq_len,
-        max_prefix_len, scale, partition_size, _DTYPES[query.dtype], ws,
+        o, q, kc, vc, bt, sl, pt, pl, ps, B, G, H, hkv, D, nb, bs, blocks, pblocks,
+        int(max_seq_len), int(max_prefix_len), float(scale), int(partition_size), _DTYPES[query.dtype], ws,
         workspace.numel() * workspace.element_size(), _stream_handle(stream), ctypes.byref(opts)),
         "pa_prefix_forward")
 
@@ -532,8 +532,8 @@ def pa_select_blocks(selected, query, key_bounds, block_tables, seq_lens, block_
     if max_seq_len is None:
         max_seq_len = block_tables.shape[1] * block_size
     _check((_lib or load_library()).pa_select_blocks(
-        sel, q, kb, bt, sl, qs, B, R, H, hkv, D, nb, block_size, block_tables.shape[1], max_seq_len,
-        selected.shape[2], sink_blocks, recent_blocks, partition_size, _DTYPES[query.dtype], ws,
+        sel, q, kb, bt, sl, qs, B, R, H, hkv, D, nb, block_size, block_tables.shape[1],
+        int(max_seq_len), selected.shape[2], sink_blocks, recent_blocks, int(partition_size), _DTYPES[query.dtype], ws,
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_select_blocks")
 
 
@@ -562,8 +562,9 @@ def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables
     if max_seq_len is None:
         max_seq_len = blocks * bs
     _check((_lib or load_library()).pa_sparse_forward(
-        o, sel, q, kc, vc, kb, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks, max_seq_len,
-        num_selected, sink_blocks, recent_blocks, scale, partition_size, _DTYPES[query.dtype], ws,
+        o, sel, q, kc, vc, kb, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks,
+        int(max_seq_len), int(num_selected), sink_blocks, recent_blocks, float(scale),
+        int(partition_size), _DTYPES[query.dtype], ws,
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_sparse_forward")
 
 

@@ -1151,9 +1151,12 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   if (opts) opt = *opts;
   if (opt.variant != PA_VARIANT_AUTO && opt.variant != PA_VARIANT_V2) return PA_ERR_INVALID_ARG;
   opt.fuse_partitions = 0;
-  if (num_prefixes < 1 || max_prefix_blocks < 1 || max_prefix_len < 0 || !prefix_tables ||
-      !prefix_lens || !prefix_start || !aligned(prefix_tables, 4) || !aligned(prefix_lens, 4) ||
-      !aligned(prefix_start, 4))
+  if (num_prefixes < 1 || max_prefix_blocks < 1 || max_prefix_len < 0) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0)  // (empty tensors have no address)
+    return host_check_cache(dtype, num_heads, num_kv_heads, head_size, num_blocks, block_size,
+                            max_blocks_per_seq, max_seq_len);
+  if (!prefix_tables || !prefix_lens || !prefix_start || !aligned(prefix_tables, 4) ||
+      !aligned(prefix_lens, 4) || !aligned(prefix_start, 4))
     return PA_ERR_INVALID_ARG;
   if (block_size > 0 && (long long)max_prefix_len > (long long)max_prefix_blocks * block_size)
     return PA_ERR_INVALID_ARG;
@@ -1176,7 +1179,6 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
       prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, splits);
   if (need == 0) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
-  if (num_seqs == 0) return PA_OK;
   c.workspace_bytes = workspace_bytes;
   c.extra_parts = splits;
   size_t off[5];

@@ -160,17 +160,7 @@ __device__ __forceinline__ bool locate_row(const AppendParams &p, int row, RowIn
   const int lane = threadIdx.x & 31;
   int s = row, i = 0, n = 1;
   if (p.q_start) {
-    // the first of q_start's entries above row, 32 tried at a time
-    int lo = 0, hi = p.num_seqs + 1;  // it is in [lo, hi]
-    while (lo < hi) {
-      const int step = (hi - lo + 31) / 32;
-      const int at = lo + lane * step;
-      const unsigned above = __ballot_sync(0xffffffffu, at < hi && __ldg(p.q_start + min(at, hi - 1)) > row);
-      const int f = above ? __ffs(above) - 1 : 32;  // lanes below f are not above
-      const int last = min(f, (hi - lo + step - 1) / step);  // lanes tried and not above
-      if (f < 32) hi = lo + f * step;
-      if (last > 0) lo = lo + (last - 1) * step + 1;
-    }
+    const int lo = first_above(p.q_start, p.num_seqs + 1, row);
     if (lo > p.num_seqs) return false;  // behind the last sequence
     if (lo == 0) {                      // before the first chunk: q_start[0] must be 0
       if (lane == 0) report(p.status, kStatusBadInput);
@@ -409,6 +399,7 @@ extern "C" pa_status_t pa_append_kv(
   if (num_seqs < 0 || num_rows < 0 || (!q_start && num_rows != num_seqs)) return PA_ERR_INVALID_ARG;
   if (rotary_dim < 0 || rotary_dim > head_size || rotary_dim % 16) return PA_ERR_INVALID_ARG;
   if (interleaved != 0 && interleaved != 1) return PA_ERR_INVALID_ARG;
+  if (num_rows == 0 || num_seqs == 0) return PA_OK;  // (empty tensors have no address)
   if (rotary_dim > 0 && (!cos_sin || max_position < 1)) return PA_ERR_INVALID_ARG;
   if ((query == nullptr) != (query_out == nullptr)) return PA_ERR_INVALID_ARG;
   if (!key_cache || !value_cache || !key || !value || !block_tables || !seq_lens || !workspace)
@@ -430,7 +421,6 @@ extern "C" pa_status_t pa_append_kv(
   if (query && query == query_out && query_stride != (long long)num_heads * head_size)
     return PA_ERR_INVALID_ARG;
   if (workspace_bytes < (size_t)kStatusBytes) return PA_ERR_WORKSPACE_TOO_SMALL;
-  if (num_rows == 0 || num_seqs == 0) return PA_OK;
 
   AppendParams p{};
   p.key_cache = key_cache;

@@ -32,6 +32,23 @@ __device__ __forceinline__ void report(int *status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
 
+// The first of a[0 .. n-1], non-decreasing, that is above x (n if none), by a
+// warp, 32 entries tried at a time.  Every lane gets it; any contents end.
+__device__ __forceinline__ int first_above(const int32_t *a, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // it is in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned above = __ballot_sync(0xffffffffu, at < hi && __ldg(a + min(at, hi - 1)) > x);
+    const int f = above ? __ffs(above) - 1 : 32;           // lanes below f are not above
+    const int last = min(f, (hi - lo + step - 1) / step);  // lanes tried and not above
+    if (f < 32) hi = lo + f * step;
+    if (last > 0) lo = lo + (last - 1) * step + 1;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

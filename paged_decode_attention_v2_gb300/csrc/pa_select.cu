@@ -61,20 +61,14 @@ __device__ __forceinline__ void widen(const uint4 &c, float (&f)[16 / sizeof(T)]
   }
 }
 
-// The item's row: its sequence and the keys it sees (0: none, or bad input).
+// The item's row: its sequence and the keys it sees (0: none, or bad input).  By
+// a warp.
 __device__ __forceinline__ void locate(const SelectParams &p, int row, int &seq, int &vis) {
   seq = row;
   vis = 0;
   int before = 0, n = 1;  // the row's index in its chunk, the chunk's rows
   if (p.q_start) {
-    int lo = 0, hi = p.num_seqs + 1;  // the first entry above row
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.q_start + mid) > row)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
+    const int lo = first_above(p.q_start, p.num_seqs + 1, row);
     if (lo > p.num_seqs) {  // behind the last sequence: nothing to see
       seq = 0;
       return;
@@ -928,7 +922,8 @@ pa_status_t check_sparse(const SparseCall &c, SparseLayout *lay) {
   if (c.partition_size < 1) return PA_ERR_INVALID_ARG;
   if (c.partition_size % 64 || c.partition_size % c.block_size || c.partition_size > 8192)
     return PA_ERR_UNSUPPORTED;
-  if (!c.block_tables || !c.seq_lens || !c.workspace) return PA_ERR_INVALID_ARG;
+  if (c.num_rows == 0) return PA_OK;  // (empty tensors have no address)
+  if (!c.query || !c.block_tables || !c.seq_lens || !c.workspace) return PA_ERR_INVALID_ARG;
   if (!host_aligned(c.query, 16) || !host_aligned(c.key_bounds, 16) ||
       !host_aligned(c.block_tables, 4) || !host_aligned(c.seq_lens, 4) ||
       !host_aligned(c.q_start, 4) || !host_aligned(c.selected, 4) || !host_aligned(c.given, 4) ||
@@ -1044,10 +1039,10 @@ pa_status_t pa_select_blocks(int32_t *selected, const void *query, const void *k
                num_kv_heads, head_size,    num_blocks,   block_size,  max_blocks_per_seq,
                max_seq_len,  num_selected, sink_blocks,  recent_blocks, partition_size,
                dtype,        workspace,    workspace_bytes, stream};
-  if (!selected || !query || !key_bounds) return PA_ERR_INVALID_ARG;
   SparseLayout lay;
   pa_status_t st = check_sparse(c, &lay);
   if (st != PA_OK || num_rows == 0) return st;
+  if (!selected || !key_bounds) return PA_ERR_INVALID_ARG;
   return run_select(c, lay, false);
 }
 
@@ -1067,14 +1062,13 @@ pa_status_t pa_sparse_forward(void *out, int32_t *selected, const void *query,
                num_kv_heads, head_size,    num_blocks,   block_size,   max_blocks_per_seq,
                max_seq_len,  num_selected, sink_blocks,  recent_blocks, partition_size,
                dtype,        workspace,    workspace_bytes, stream};
-  if (!out || !query || !key_cache || !value_cache || (given && !selected))
-    return PA_ERR_INVALID_ARG;
-  if (!host_aligned(out, 16) || !host_aligned(key_cache, 16) || !host_aligned(value_cache, 16))
-    return PA_ERR_INVALID_ARG;
   if (!(scale - scale == 0.f)) return PA_ERR_INVALID_ARG;  // not finite
   SparseLayout lay;
   pa_status_t st = check_sparse(c, &lay);
   if (st != PA_OK || num_rows == 0) return st;
+  if (!out || !key_cache || !value_cache || (given && !selected)) return PA_ERR_INVALID_ARG;
+  if (!host_aligned(out, 16) || !host_aligned(key_cache, 16) || !host_aligned(value_cache, 16))
+    return PA_ERR_INVALID_ARG;
   // The attention's own limits, before anything is enqueued: the view's items
   // fit its 31-bit counts.
   const long long items = (long long)num_rows * num_kv_heads;

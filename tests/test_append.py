@@ -66,6 +66,8 @@ def test_refusals(lib, over, status):
 def test_no_rows_is_no_work(lib):
     a = dict(BASE, query_out=FAKE + 4096, num_rows=0)
     assert lib.pa_append_kv(*a.values()) == pa.PA_OK
+    a.update(key=0, value=0, query=0, query_out=0, positions=0)  # empty tensors
+    assert lib.pa_append_kv(*a.values()) == pa.PA_OK
 
 
 def test_binding_refuses_host_tensors():

@@ -68,6 +68,8 @@ def test_workspace_bytes(lib):
     assert lib.pa_prefix_forward(*dict(BASE, workspace_bytes=n - 1).values()) == \
         pa.PA_ERR_WORKSPACE_TOO_SMALL
     assert lib.pa_prefix_forward(*dict(BASE, num_seqs=0).values()) == pa.PA_OK
+    assert lib.pa_prefix_forward(*dict(BASE, num_seqs=0, query=0, out=0, seq_lens=0,
+                                       block_tables=0).values()) == pa.PA_OK
     assert f(3, 0, 8, 2, 128, 128, 512, 512) == 0 and f(3, 1, 8, 3, 128, 128, 512, 512) == 0
     assert f(3, 1, 8, 2, 128, 0, 0, 512) > 0
 

@@ -83,6 +83,8 @@ def test_workspace_bytes(lib):
     assert lib.pa_sparse_forward(*dict(BASE, workspace_bytes=small - 1).values()) == \
         pa.PA_ERR_WORKSPACE_TOO_SMALL
     assert lib.pa_sparse_forward(*dict(BASE, num_seqs=0, num_rows=0).values()) == pa.PA_OK
+    assert lib.pa_sparse_forward(*dict(BASE, num_seqs=0, num_rows=0, query=0, out=0, seq_lens=0,
+                                       block_tables=0, selected=0).values()) == pa.PA_OK
 
 
 # ---------------------------------------------------------------------------
@@ -432,3 +434,27 @@ def test_cache_beyond_32_bits():
     sel = c.select()
     assert torch.equal(d["sel"].cpu(), sel)
     assert_close(d["out"], c.attend(sel), c.dtype, "far pages")
+
+
+@pytest.mark.gpu
+def test_many_rows_with_long_ones_among_them():
+    """Whole-item CTAs (enough items for every SM) whose pages exceed what a
+    warp (256), the CTA's registers (1024) and its shared memory (8192) hold;
+    the long rows read one another's pages, so that the caches stay small."""
+    long = [9000, 8300, 4000, 1300, 1025, 700, 260]
+    lens = [8 * n - 3 for n in long] + [1 + i % 90 for i in range(603)]
+    c = Case(25, torch.bfloat16, 2, 1, 64, 8, [8 * long[0] - 3] + [90], 6, 1, 1)
+    c.lens, c.rows = lens, len(lens)
+    bt = c.bt[:1].expand(len(lens), -1).clone()
+    bt[len(long):] = c.bt[1]
+    c.bt = bt
+    c.q = torch.randn(c.rows, 2, 64, generator=torch.Generator().manual_seed(26)).to(c.dtype)
+    # a page's bounds for every row: those of all its tokens (a bound may be wide)
+    k = c.kc.clone()
+    c.kb = torch.stack([k.amax(2), k.amin(2)], 2)
+    d = c.device(poison=False)
+    ref = c.select()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    assert torch.equal(d["sel"].cpu(), ref)
+    assert_close(d["out"], c.attend(ref), c.dtype, "long rows among many")
