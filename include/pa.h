@@ -381,9 +381,9 @@ pa_status_t pa_v2_forward_noalloc(void *out, const void *query,
  * y1 = x1 cos - x2 sin, y2 = x2 cos + x1 sin, the pairs being (j, j +
  * rotary_dim / 2) with interleaved = 0, (2j, 2j + 1) with 1; the rest and the
  * values are copied.  A page's bounds start anew with its first token (so they
- * are kept from there on or not at all) and otherwise only widen: tokens overwritten later (rejected drafts) leave
- * theirs in, so the bounds then still hold but are wider than need be.  NaN
- * keys are passed over.
+ * are kept from there on or not at all) and otherwise only widen: tokens
+ * overwritten later (rejected drafts) leave theirs in, so the bounds then still
+ * hold but are wider than need be.  NaN keys are passed over.
  *
  * dtype as the caches; f32, bf16 and f16.  No two sequences may append to the
  * same page.  The workspace needs only its 256-byte status block (any
@@ -500,9 +500,9 @@ size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
  * zeros.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); the other arguments and
  * limits as pa_v2_forward.  The workspace holds pa_prefix_workspace_bytes(...)
  * bytes, initialised once by pa_workspace_init (any workspace that is large
- * enough serves calls of any shape, one after another).  Bad tables, lengths or groups are
- * reported as PA_ERR_DEVICE_BAD_INPUT; the rows in question then hold no
- * meaningful values.  opts as in pa_forward (variant V2 or auto; no fused
+ * enough serves calls of any shape, one after another).  Bad tables, lengths or
+ * groups are reported as PA_ERR_DEVICE_BAD_INPUT; the rows in question (with
+ * starts out of order, any row) then hold no meaningful values.  opts as in pa_forward (variant V2 or auto; no fused
  * combine, no CUDA-core path). */
 pa_status_t pa_prefix_forward(void *out, const void *query,
                               const void *key_cache, const void *value_cache,

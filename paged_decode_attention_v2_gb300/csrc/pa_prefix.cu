@@ -15,9 +15,9 @@
 // ring of slots (TMA, whole pages): K of stage j, V of stage j, K of stage
 // j + 1, ...  One thread issues the MMAs.  S lives in tensor memory, fp32, one
 // row a lane; a softmax thread owns a row: its maximum and sum need no
-// shuffles.  P goes back over S's columns, rounded to the input type (the sum
-// adds the unrounded exponentials; the two differ by 2^-9 relative at most,
-// unbiased), and is the PV product's A operand straight from tensor memory.
+// shuffles.  P goes back over S's columns, rounded to the input type (a weight
+// is off by 2^-8 of itself at most in bf16, 2^-11 in f16, with either sign; the
+// sum adds the unrounded exponentials), and is the PV product's A operand straight from tensor memory.
 //   D 64, 128: two row tiles (NT 2) share every stage of 128 keys; while the
 //     softmax of one runs, the tensor cores work on the other:
 //     PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) ...
@@ -131,23 +131,27 @@ struct PrefixItem {
 };
 
 // Group g's first sequence, sequences and prefix length, clamped to what the
-// buffers hold.
-__device__ __forceinline__ void prefix_group(const PrefixParams &p, int g, int &seq0, int &n,
+// buffers hold; false if its starts were out of order or range.
+__device__ __forceinline__ bool prefix_group(const PrefixParams &p, int g, int &seq0, int &n,
                                              int &len) {
   seq0 = __ldg(p.prefix_start + g);
   int end = __ldg(p.prefix_start + g + 1);
   len = __ldg(p.prefix_lens + g);
-  if (seq0 < 0 || end < seq0 || end > p.num_seqs || len < 0 || len > p.max_prefix_len) {
+  const bool ok = seq0 >= 0 && end >= seq0 && end <= p.num_seqs;
+  if (!ok || len < 0 || len > p.max_prefix_len) {
     report(p.status, kStatusBadInput);
     seq0 = max(0, min(seq0, p.num_seqs));
     end = max(seq0, min(end, p.num_seqs));
     len = max(0, min(len, p.max_prefix_len));
   }
   n = end - seq0;
+  return ok;
 }
 
 // Walks the item list in order (the same list in every role): find() must be
-// called by a whole warp with non-decreasing indices.
+// called by a whole warp with non-decreasing indices.  The list ends before the
+// first 32 groups with a start out of order or range, so groups never overlap
+// and the items are never more than the sequences allow.
 template <int ROWS>
 struct ItemWalk {
   int base = 0, first_group = 0;      // items before, and first of, the 32 groups held
@@ -160,12 +164,14 @@ struct ItemWalk {
       if (!loaded) {
         cnt = seq0 = n = len = 0;
         const int g = first_group + lane;
+        bool ok = true;
         if (g < p.num_prefixes) {
-          prefix_group(p, g, seq0, n, len);
+          ok = prefix_group(p, g, seq0, n, len);
           const int tiles = (n * p.group + ROWS - 1) / ROWS;
           const int splits = (len + p.split_tokens - 1) / p.split_tokens;
           cnt = tiles * splits * p.num_kv_heads;
         }
+        if (!__all_sync(0xffffffffu, ok)) return false;
         incl = cnt;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -290,207 +296,207 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
 
   // NT 2: 3 warpgroups at 168 registers, 2 x 208 + 80 <= 3 x 168
   if (warp >= Z::SOFTMAX_WARPS) {
-  if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == Z::SOFTMAX_WARPS) {
-    // ======================= producer warp =======================
-    if (lane == 0) {
-      prefetch_tmap(&tmap_k);
-      prefetch_tmap(&tmap_v);
-    }
-    bool ok = true;
-    int op = 0;  // copies issued: K and V of each stage, in turn
-    const int U = p.block_size;
-    for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
-      const int32_t *bt = p.prefix_tables + (size_t)it.group * p.max_prefix_blocks;
-      const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
-      // lane's page of a stage; the next stage's entries load while this one waits
-      auto entry = [&](int j) -> int {
-        const int tok = it.tok0 + j * KEYS + lane * U;
-        return j < stages && lane < KEYS / U && tok < it.tok1 ? __ldg(bt + (tok >> p.log2_block_size)) : -1;
-      };
-      int blk = entry(0);
-      for (int j = 0; ok && j < stages; ++j) {
-        const int next = entry(j + 1);
-        const int tok = it.tok0 + j * KEYS + lane * U;
-        int y = -1;
-        if (lane < KEYS / U && tok < it.tok1) {
-          if ((unsigned)blk >= (unsigned)p.num_blocks)
-            report(p.status, kStatusBadInput);
-          else
-            y = (blk * p.num_kv_heads + it.kvh) * U;
-        }
-        blk = next;
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, y >= 0)) * U * D * 2u;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int sl = op % NS;
-          if (op >= NS) {
-            bool w = true;
-            if (lane == 0) w = mbar_wait(empty0 + 8 * sl, ((op / NS) - 1) & 1, limit, flags);
-            ok = __shfl_sync(0xffffffffu, w, 0);
-            if (!ok) break;
+    if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == Z::SOFTMAX_WARPS) {
+      // ======================= producer warp =======================
+      if (lane == 0) {
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+      }
+      bool ok = true;
+      int op = 0;  // copies issued: K and V of each stage, in turn
+      const int U = p.block_size;
+      for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
+        const int32_t *bt = p.prefix_tables + (size_t)it.group * p.max_prefix_blocks;
+        const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
+        // lane's page of a stage; the next stage's entries load while this one waits
+        auto entry = [&](int j) -> int {
+          const int tok = it.tok0 + j * KEYS + lane * U;
+          return j < stages && lane < KEYS / U && tok < it.tok1 ? __ldg(bt + (tok >> p.log2_block_size)) : -1;
+        };
+        int blk = entry(0);
+        for (int j = 0; ok && j < stages; ++j) {
+          const int next = entry(j + 1);
+          const int tok = it.tok0 + j * KEYS + lane * U;
+          int y = -1;
+          if (lane < KEYS / U && tok < it.tok1) {
+            if ((unsigned)blk >= (unsigned)p.num_blocks)
+              report(p.status, kStatusBadInput);
+            else
+              y = (blk * p.num_kv_heads + it.kvh) * U;
           }
-          if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * sl, bytes);
-          __syncwarp();
-          if (y >= 0)
-            tma_load_4d(ring_u32 + (uint32_t)sl * Z::SLOT + (uint32_t)(lane * U / 8) * Z::GROUP,
-                        kv == 0 ? &tmap_k : &tmap_v, 0, 0, 0, y >> 3, full0 + 8 * sl);
-          ++op;
-        }
-      }
-    }
-    // the partitions of every row, for Phase 2: its own, then its prefix's
-    for (int s = blockIdx.x * 32 + lane; s < p.num_seqs; s += gridDim.x * 32) {
-      int lo = 0, hi = p.num_prefixes + 1;  // the first start above s
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.prefix_start + mid) > s)
-          hi = mid;
-        else
-          lo = mid + 1;
-      }
-      int splits = 0;
-      if (lo == 0 || lo > p.num_prefixes) {  // in no group
-        report(p.status, kStatusBadInput);
-      } else {
-        int s0, n, len;
-        prefix_group(p, lo - 1, s0, n, len);
-        splits = (len + p.split_tokens - 1) / p.split_tokens;
-      }
-      p.row_limit[s] = (own_parts(p, s) + splits) * p.partition_size;
-    }
-    if (!ok && lane == 0) {
-      report(p.status, kStatusTimeout);
-      flags[0] = 1;
-    }
-    if (lane == 0)  // every copy lands before the CTA retires
-      for (int i = op > NS ? op - NS : 0; i < op; ++i)
-        mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, kDrainLimitNs, nullptr);
-    __syncwarp();
-  } else if (warp == Z::SOFTMAX_WARPS + 1) {
-    // ======================= MMA warp =======================
-    // The whole warp runs the loop, so that descriptors and control stay in
-    // uniform registers; one elected lane issues.
-    const uint32_t leader = elect_one();
-    bool ok = true;
-    int sk = 0, par = 0;        // ring slot of the next stage's K, its phase
-    int items[2] = {0, 0};      // items of each tile
-    int done[2] = {0, 0};       // stages of each tile (NT 1: [0], over both buffers)
-    // The tile and ring descriptors' constant parts; a k-step adds to the
-    // address field (16-byte units) only.
-    const uint64_t q_desc = smem_desc(q_u32, 16, 1024);
-    const uint64_t k_desc = smem_desc(ring_u32, 16, Z::GROUP);
-    const uint64_t v_desc = smem_desc(ring_u32, 1024, Z::GROUP);
-    auto wait_slot = [&](int sl, int ph) -> bool {
-      return mbar_wait(full0 + 8 * sl, (uint32_t)ph, limit, flags);
-    };
-    auto advance = [&](int &sl, int &ph) {
-      if (++sl == NS) {
-        sl = 0;
-        ph ^= 1;
-      }
-    };
-    // S = Q K^T: D / 16 k-steps of 32 bytes inside a panel
-    auto issue_s = [&](int sl, int t, int buf) {
-      const uint64_t db0 = k_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
-      const uint64_t da0 = q_desc + (uint32_t)t * (uint32_t)(Z::QTILE >> 4);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        tc_mma_if(leader, tmem + 128u * (uint32_t)buf,
-                  da0 + (uint32_t)(((ks >> 2) * Z::QPANEL + (ks & 3) * 32) >> 4),
-                  db0 + (uint32_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
-      tc_commit_if(leader, s_full + 8u * (uint32_t)buf);
-    };
-    // O += P V: k-steps of 16 keys; P two keys a column, V MN-major
-    auto issue_pv = [&](int sl, int t, int buf, bool first, int k0, int k1) {
-      const uint64_t db0 = v_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
-#pragma unroll
-      for (int kk = k0; kk < k1; ++kk)
-        tc_mma_ts_if(leader, tmem_o + (uint32_t)(t * D), tmem + 128u * (uint32_t)buf + 8u * (uint32_t)kk,
-                     db0 + (uint32_t)((kk * 2 * Z::GROUP) >> 4), kIdescPV, first && kk == 0 ? 0u : 1u);
-    };
-    for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
-      const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
-      const int nt = (it.rows + kTileRows - 1) / kTileRows;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (ok && t < nt) ok = mbar_wait(q_full + 8 * t, items[t] & 1, limit, flags);
-      if (ok) ok = wait_slot(sk, par);
-      if (ok) {
-        tc_fence_after();
-        if constexpr (NT == 2) {
-          issue_s(sk, 0, 0);
-          if (nt == 2) issue_s(sk, 1, 1);
-        } else {
-          issue_s(sk, 0, done[0] & 1);
-        }
-        tc_commit_if(leader, empty0 + 8 * sk);
-      }
-      for (int j = 0; ok && j < stages; ++j) {
-        const bool more = j + 1 < stages;
-        int sv = sk, pv = par;  // V's slot, then the next K's
-        advance(sv, pv);
-        int sn = sv, pn = pv;
-        advance(sn, pn);
-        sk = sn;
-        par = pn;
-        if constexpr (NT == 2) {
-          // this V and the next K are in long before P, as a rule: awaited
-          // first, they cost nothing between P and its MMAs
-          ok = wait_slot(sv, pv) && (!more || wait_slot(sn, pn));
-          if (!ok) break;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t >= nt) break;
-            ok = mbar_wait(p_half + 8 * t, done[t] & 1, limit, flags);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(sv, t, t, j == 0, 0, KEYS / 32);
-            ok = mbar_wait(p_full + 8 * t, done[t] & 1, limit, flags);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(sv, t, t, false, KEYS / 32, KEYS / 16);
-            if (t == nt - 1) tc_commit_if(leader, empty0 + 8 * sv);
-            if (more) {
-              issue_s(sn, t, t);
-              if (t == nt - 1) tc_commit_if(leader, empty0 + 8 * sn);
-            } else {
-              tc_commit_if(leader, o_done + 8 * t);
+          blk = next;
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, y >= 0)) * U * D * 2u;
+  #pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int sl = op % NS;
+            if (op >= NS) {
+              bool w = true;
+              if (lane == 0) w = mbar_wait(empty0 + 8 * sl, ((op / NS) - 1) & 1, limit, flags);
+              ok = __shfl_sync(0xffffffffu, w, 0);
+              if (!ok) break;
             }
-            ++done[t];
+            if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * sl, bytes);
+            __syncwarp();
+            if (y >= 0)
+              tma_load_4d(ring_u32 + (uint32_t)sl * Z::SLOT + (uint32_t)(lane * U / 8) * Z::GROUP,
+                          kv == 0 ? &tmap_k : &tmap_v, 0, 0, 0, y >> 3, full0 + 8 * sl);
+            ++op;
           }
-        } else {
-          const int b = done[0] & 1;
-          if (more) {
-            ok = wait_slot(sn, pn);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(sn, 0, b ^ 1);
-            tc_commit_if(leader, empty0 + 8 * sn);
-          }
-          ok = mbar_wait(p_full + 8 * b, (done[0] >> 1) & 1, limit, flags) && wait_slot(sv, pv);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(sv, 0, b, j == 0, 0, KEYS / 16);
-          tc_commit_if(leader, empty0 + 8 * sv);
-          tc_commit_if(leader, pv_done);
-          if (!more) tc_commit_if(leader, o_done);
-          ++done[0];
         }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) items[t] += t < nt;
-      ok = __all_sync(0xffffffffu, ok);
+      // the partitions of every row, for Phase 2: its own, then its prefix's
+      for (int s = blockIdx.x * 32 + lane; s < p.num_seqs; s += gridDim.x * 32) {
+        int lo = 0, hi = p.num_prefixes + 1;  // the first start above s
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(p.prefix_start + mid) > s)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        int splits = 0;
+        if (lo == 0 || lo > p.num_prefixes) {  // in no group
+          report(p.status, kStatusBadInput);
+        } else {
+          int s0, n, len;
+          prefix_group(p, lo - 1, s0, n, len);
+          splits = (len + p.split_tokens - 1) / p.split_tokens;
+        }
+        p.row_limit[s] = (own_parts(p, s) + splits) * p.partition_size;
+      }
+      if (!ok && lane == 0) {
+        report(p.status, kStatusTimeout);
+        flags[0] = 1;
+      }
+      if (lane == 0)  // every copy lands before the CTA retires
+        for (int i = op > NS ? op - NS : 0; i < op; ++i)
+          mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, kDrainLimitNs, nullptr);
+      __syncwarp();
+    } else if (warp == Z::SOFTMAX_WARPS + 1) {
+      // ======================= MMA warp =======================
+      // The whole warp runs the loop, so that descriptors and control stay in
+      // uniform registers; one elected lane issues.
+      const uint32_t leader = elect_one();
+      bool ok = true;
+      int sk = 0, par = 0;        // ring slot of the next stage's K, its phase
+      int items[2] = {0, 0};      // items of each tile
+      int done[2] = {0, 0};       // stages of each tile (NT 1: [0], over both buffers)
+      // The tile and ring descriptors' constant parts; a k-step adds to the
+      // address field (16-byte units) only.
+      const uint64_t q_desc = smem_desc(q_u32, 16, 1024);
+      const uint64_t k_desc = smem_desc(ring_u32, 16, Z::GROUP);
+      const uint64_t v_desc = smem_desc(ring_u32, 1024, Z::GROUP);
+      auto wait_slot = [&](int sl, int ph) -> bool {
+        return mbar_wait(full0 + 8 * sl, (uint32_t)ph, limit, flags);
+      };
+      auto advance = [&](int &sl, int &ph) {
+        if (++sl == NS) {
+          sl = 0;
+          ph ^= 1;
+        }
+      };
+      // S = Q K^T: D / 16 k-steps of 32 bytes inside a panel
+      auto issue_s = [&](int sl, int t, int buf) {
+        const uint64_t db0 = k_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
+        const uint64_t da0 = q_desc + (uint32_t)t * (uint32_t)(Z::QTILE >> 4);
+  #pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc_mma_if(leader, tmem + 128u * (uint32_t)buf,
+                    da0 + (uint32_t)(((ks >> 2) * Z::QPANEL + (ks & 3) * 32) >> 4),
+                    db0 + (uint32_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), kIdescS, ks > 0 ? 1u : 0u);
+        tc_commit_if(leader, s_full + 8u * (uint32_t)buf);
+      };
+      // O += P V: k-steps of 16 keys; P two keys a column, V MN-major
+      auto issue_pv = [&](int sl, int t, int buf, bool first, int k0, int k1) {
+        const uint64_t db0 = v_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
+  #pragma unroll
+        for (int kk = k0; kk < k1; ++kk)
+          tc_mma_ts_if(leader, tmem_o + (uint32_t)(t * D), tmem + 128u * (uint32_t)buf + 8u * (uint32_t)kk,
+                       db0 + (uint32_t)((kk * 2 * Z::GROUP) >> 4), kIdescPV, first && kk == 0 ? 0u : 1u);
+      };
+      for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
+        const int stages = (it.tok1 - it.tok0 + KEYS - 1) / KEYS;
+        const int nt = (it.rows + kTileRows - 1) / kTileRows;
+  #pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (ok && t < nt) ok = mbar_wait(q_full + 8 * t, items[t] & 1, limit, flags);
+        if (ok) ok = wait_slot(sk, par);
+        if (ok) {
+          tc_fence_after();
+          if constexpr (NT == 2) {
+            issue_s(sk, 0, 0);
+            if (nt == 2) issue_s(sk, 1, 1);
+          } else {
+            issue_s(sk, 0, done[0] & 1);
+          }
+          tc_commit_if(leader, empty0 + 8 * sk);
+        }
+        for (int j = 0; ok && j < stages; ++j) {
+          const bool more = j + 1 < stages;
+          int sv = sk, pv = par;  // V's slot, then the next K's
+          advance(sv, pv);
+          int sn = sv, pn = pv;
+          advance(sn, pn);
+          sk = sn;
+          par = pn;
+          if constexpr (NT == 2) {
+            // this V and the next K are in long before P, as a rule: awaited
+            // first, they cost nothing between P and its MMAs
+            ok = wait_slot(sv, pv) && (!more || wait_slot(sn, pn));
+            if (!ok) break;
+  #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t >= nt) break;
+              ok = mbar_wait(p_half + 8 * t, done[t] & 1, limit, flags);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(sv, t, t, j == 0, 0, KEYS / 32);
+              ok = mbar_wait(p_full + 8 * t, done[t] & 1, limit, flags);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(sv, t, t, false, KEYS / 32, KEYS / 16);
+              if (t == nt - 1) tc_commit_if(leader, empty0 + 8 * sv);
+              if (more) {
+                issue_s(sn, t, t);
+                if (t == nt - 1) tc_commit_if(leader, empty0 + 8 * sn);
+              } else {
+                tc_commit_if(leader, o_done + 8 * t);
+              }
+              ++done[t];
+            }
+          } else {
+            const int b = done[0] & 1;
+            if (more) {
+              ok = wait_slot(sn, pn);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(sn, 0, b ^ 1);
+              tc_commit_if(leader, empty0 + 8 * sn);
+            }
+            ok = mbar_wait(p_full + 8 * b, (done[0] >> 1) & 1, limit, flags) && wait_slot(sv, pv);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(sv, 0, b, j == 0, 0, KEYS / 16);
+            tc_commit_if(leader, empty0 + 8 * sv);
+            tc_commit_if(leader, pv_done);
+            if (!more) tc_commit_if(leader, o_done);
+            ++done[0];
+          }
+        }
+  #pragma unroll
+        for (int t = 0; t < NT; ++t) items[t] += t < nt;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      // nothing may still run when the memory is freed
+      tc_commit_if(leader, drain);
+      mbar_wait(drain, 0, kDrainLimitNs, nullptr);
+      if (!ok && lane == 0) {
+        report(p.status, kStatusTimeout);
+        flags[0] = 1;
+      }
+      __syncwarp();
     }
-    // nothing may still run when the memory is freed
-    tc_commit_if(leader, drain);
-    mbar_wait(drain, 0, kDrainLimitNs, nullptr);
-    if (!ok && lane == 0) {
-      report(p.status, kStatusTimeout);
-      flags[0] = 1;
-    }
-    __syncwarp();
-  }
   } else {
     // ======================= softmax warps: thread = row =======================
     if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");

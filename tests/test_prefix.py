@@ -303,6 +303,21 @@ def test_bad_data_is_reported(what):
 
 
 @pytest.mark.gpu
+def test_groups_that_overlap_are_reported():
+    """Starts that go up and down over many groups: no group of them is served
+    twice, and the call ends as any other."""
+    n = 200
+    c = Case(12, torch.bfloat16, 4, 1, 64, 16, [6] + [0] * (n - 1), [300] * n, [5, 50, 0, 7, 20, 1])
+    d = c.device()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    assert_close(d["out"], c.reference(), c.dtype, "one group of many in use")
+    d["ps"].copy_(torch.tensor([0, 6] * (n // 2) + [6]))
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_BAD_INPUT
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_a_wait_that_runs_out_is_reported(D):
     """Softmax warps that never come: the bounded waits end, the kernel frees
