@@ -985,20 +985,23 @@ pa_status_t run_select(const SparseCall &c, const SparseLayout &lay, bool table)
     return host_launch(reinterpret_cast<const void *>(&pa_given_blocks_kernel),
                        (unsigned)((items + 3) / 4), 1, 128, 0, c.stream, args,
                        "launch given-blocks kernel");
-  // One CTA an item if that gives every SM four.  Otherwise chunks of at
-  // least 64 pages (a round of the CTA's warps) towards 32 an SM: with lengths
-  // of all kinds in a batch, a long sequence's chunks are what the last SMs
-  // wait for (64 sequences of up to 4096 pages, D 256, a call: 77 us at eight
-  // an SM, 65 at 16, 63 at 32, 67 at 64).
+  // One CTA an item if that gives every SM four.  Otherwise chunks, towards 32
+  // CTAs an SM: with lengths of all kinds in a batch, a long sequence's chunks
+  // are what the last SMs wait for (64 sequences of up to 4096 pages, D 256, a
+  // call: 77 us at eight an SM, 65 at 16, 63 at 32, 67 at 64).  A chunk is at
+  // least two rounds of the CTA's warps (128 pages; 32 rows of up to 512 pages:
+  // 29.3 us a call, 30.9 in chunks of one round), or one where that leaves SMs
+  // with less than two CTAs (one row of 6250 pages: 23.5 us, 24.1 with two).
   p.chunks = 1;
   p.chunk_pages = lay.max_pages > 0 ? lay.max_pages : 1;
   if (items < 4ll * sms) {
+    const int least = items * ((lay.max_pages + 127) / 128) >= 2ll * sms ? 128 : 64;
     long long want = (32ll * sms + items - 1) / items;
-    const long long most = (lay.max_pages + 63) / 64;
+    const long long most = (lay.max_pages + least - 1) / least;
     if (want > most) want = most;
     if (want > kSelMaxChunks) want = kSelMaxChunks;
     if (want > 1) {
-      p.chunk_pages = (int)(((lay.max_pages + want - 1) / want + 63) / 64 * 64);
+      p.chunk_pages = (int)(((lay.max_pages + want - 1) / want + least - 1) / least * least);
       p.chunks = (lay.max_pages + p.chunk_pages - 1) / p.chunk_pages;
     }
   }
