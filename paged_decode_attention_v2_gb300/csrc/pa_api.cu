@@ -228,6 +228,7 @@ struct Call {
   // partitions for its prefix's, and the rows' slot counts x partition_size
   int extra_parts = 0;
   const int *row_limit = nullptr;
+  bool check_only = false;  // launch(): what it can refuse, and nothing enqueued
 };
 
 // Rows of query (and output) and of the V2 workspace: sequences, or the query
@@ -745,6 +746,7 @@ pa_status_t launch(const Call &c, bool v2, const pa_options_t &opt) {
   long long grid = (long long)per_sm * dev->sm_count;
   if (grid > max_items) grid = max_items;
   grid = grid / cl * cl;  // whole clusters
+  if (c.check_only) return PA_OK;
   if (phase1 && grid > 0) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -1172,6 +1174,8 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   if (dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;  // tensor path only
   if ((long long)num_seqs * (num_heads / num_kv_heads) >= (1ll << 28)) return PA_ERR_UNSUPPORTED;
   if (opt.math == PA_MATH_SIMT) return PA_ERR_UNSUPPORTED;
+  if (opt.math != PA_MATH_AUTO && opt.math != PA_MATH_TENSOR) return PA_ERR_INVALID_ARG;
+  if (opt.num_stages > 0 && (opt.num_stages < 2 || opt.num_stages > 16)) return PA_ERR_INVALID_ARG;
   int split = 0, splits = 0;
   prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
               max_prefix_len, partition_size, &split, &splits);
@@ -1233,6 +1237,12 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   p.debug_flags = opt.debug_flags;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.wait_limit_ns = opt.wait_limit_ns ? opt.wait_limit_ns : kDefaultWaitLimitNs;
+  if (opt.num_stages > 0) {  // may be more than fit: refused before anything is enqueued
+    c.check_only = true;
+    st = launch(c, true, opt);
+    if (st != PA_OK) return st;
+    c.check_only = false;
+  }
   // one CTA an SM (its shared memory), never more than there can be items
   const long long tiles = (long long)num_seqs * p.group / k.tile_rows +
                           (num_prefixes < num_seqs ? num_prefixes : num_seqs);

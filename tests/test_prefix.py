@@ -57,6 +57,9 @@ def test_refused_variants(lib):
     for kw in (dict(variant=pa.PA_VARIANT_V1), dict(variant=7)):
         o = pa.pa_options_t(**kw)
         assert lib.pa_prefix_forward(*dict(BASE, opts=o).values()) == pa.PA_ERR_INVALID_ARG
+    for kw in (dict(math=7), dict(num_stages=1), dict(num_stages=17)):
+        o = pa.pa_options_t(**kw)
+        assert lib.pa_prefix_forward(*dict(BASE, opts=o).values()) == pa.PA_ERR_INVALID_ARG
     o = pa.pa_options_t(math=pa.PA_MATH_SIMT)
     assert lib.pa_prefix_forward(*dict(BASE, opts=o).values()) == pa.PA_ERR_UNSUPPORTED
 
@@ -300,6 +303,21 @@ def test_bad_data_is_reported(what):
     assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_BAD_INPUT
     if what != "order":
         assert_close(d["out"][2:5], ref[2:5], c.dtype, "the second group")
+
+
+@pytest.mark.gpu
+def test_refused_depth_enqueues_nothing():
+    """A ring that does not fit is refused before the prefix kernel is enqueued:
+    the workspace stays as it was."""
+    c = Case(13, torch.bfloat16, 4, 1, 256, 16, [3], [300], [5, 50, 20])
+    d = c.device()
+    d["ws"][256:] = 77
+    with pytest.raises(pa.PAError):
+        c.run(d, num_stages=16)
+    torch.cuda.synchronize()
+    assert (d["ws"][256:] == 77).all()
+    c.run(d, num_stages=2)
+    assert_close(d["out"], c.reference(), c.dtype, "two stages")
 
 
 @pytest.mark.gpu
