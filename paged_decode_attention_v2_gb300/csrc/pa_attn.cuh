@@ -897,7 +897,14 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) __maxnreg__((attn_max_regs<M
     // item is located.
     int takers = (int)gridDim.x;
     int item = blockIdx.x;
-    if (p.write_partials && p.num_seqs <= 32) {
+    if (p.late_wait) {
+      // Beside the prefix kernel only some CTAs are placed, and the others
+      // when it ends.  So an item waits for no CTA of its own, and a CTA takes
+      // its next item as late as it can: those that come late find work left
+      // (256 sequences behind a prefix in 4 splits: 68.0 -> 64.5 us; 64 at D
+      // 256 in 10 splits: 51 -> 39.7 us).
+      takers = 0;
+    } else if (p.write_partials && p.num_seqs <= 32) {
       // A batch of at most 32 sequences is counted in one chunk, so every CTA
       // knows the number of items N.  When N is not a multiple of the grid
       // (say 1.7 items per CTA) the CTAs that take one more item than the
@@ -916,6 +923,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) __maxnreg__((attn_max_regs<M
     auto grab_value = [&](int raw) -> int {
       return takers + __shfl_sync(0xffffffffu, raw, 0);
     };
+    if (p.late_wait) item = grab_value(grab_issue());
     int i = 0;  // stages issued by this CTA
     bool ok = true;
     while (true) {
@@ -1086,7 +1094,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) __maxnreg__((attn_max_regs<M
           bulk_load(ring_u32 + (uint32_t)st * STAGE_BYTES + 2 * HALF_BYTES, q, (uint32_t)qbytes,
                     full0 + 8 * st);
         }
-        if (j == 0) next_raw = grab_issue();
+        if (j == (p.late_wait ? n_st - 1 : 0)) next_raw = grab_issue();
         ++i;
         const int next_rel = ((stage_tok0 + ST) >> p.log2_block_size) - win0;
         if (next_rel >= 32) {

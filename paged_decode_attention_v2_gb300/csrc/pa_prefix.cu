@@ -767,14 +767,16 @@ PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size) {
 //   - the prefix kernel: waves of items on 152 SMs, each an item's stages at
 //     the tensor cores' pace or that of the keys' bytes, plus 10 us an item
 //     (start, queries, epilogue);
-//   - the own tokens run on the SMs left free meanwhile, 40 GB/s each; what
-//     is left then takes as long on those, or 5 us and 5.7 TB/s on all of
-//     them.  So it pays to leave SMs free (8 sequences behind 100,000 tokens:
-//     37 splits, 148 items, 49.5 us, against 38 splits, 152 items, 53.2 us;
-//     256 behind 8192 with 264 of their own: 3 splits, 96 items, 61.5 us,
-//     against 4 splits, 128 items, 67.4 us and 2 splits, 64 items, 68.3 us; D
-//     256, 64 behind two of 12,000 with 455 of their own: 9 splits, 90 items,
-//     40.8 us, against 8 splits, 43.7 us, and 12 splits, 52.9 us);
+//   - the own tokens run on the SMs left free meanwhile, 50 GB/s each (57
+//     with items of 512 tokens; what a single SM's copies of pages reach);
+//     what is left then takes as long on those, or 3 us and 5.7 TB/s on all
+//     of them.  So it pays to leave SMs free (256 sequences behind 8192 tokens
+//     with 264 of their own: 3 splits, 96 items, 61.6 us, against 4 splits,
+//     128 items, 64.5 us and 2 splits, 64 items, 68.4 us; D 256, 64 behind two
+//     of 12,000 with 455 of their own: 9 splits, 90 items, 40.9 us, against 8
+//     splits, 43.7 us, 11 splits, 43.9 us and 12 splits, 51.0 us), unless
+//     there is little else to do (8 behind 100,000: 37 splits, 148 items, 48.8
+//     us, 38 splits, 152 items, 48.7 us, 34 splits, 49.9 us);
 //   - Phase 2: every split is another partial of every row.
 void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
                  int max_seq_len, int max_prefix_len, int partition_size, int *split_tokens,
@@ -802,9 +804,9 @@ void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads
     const long long active = items < kSms ? items : kSms;
     const double bytes_pace = (double)active * groups / tiles * stage_us;
     const double t = waves * (per * (bytes_pace > pace ? bytes_pace : pace) + 10.);
-    const double beside = waves == 1 ? (kSms - active) * 0.04 : 0.;  // MB a us
+    const double beside = waves == 1 ? (kSms - active) * 0.05 : 0.;  // MB a us
     const double left_mb = own_mb - t * beside;
-    double after = left_mb > 0. ? 5. + left_mb / 5.7 : 0.;
+    double after = left_mb > 0. ? 3. + left_mb / 5.7 : 0.;
     if (left_mb > 0. && left_mb < after * beside) after = left_mb / beside;
     const double cost = t + after +
                         (double)num_seqs * num_heads * (n + own_parts) * head_size * 4. / 3e6;
