@@ -30,13 +30,13 @@
 // stage exceeds it by more than 2^8, which the final sum undoes exactly.
 //
 // Measured on GB300 (a whole call, one after another; 32/4 heads, bf16, D 128):
-//   256 sequences behind 8192 tokens, 16 to 512 of their own: 61.7 us, of
-//     which this kernel takes 45 alone (96 items of 22 stages; the own tokens'
-//     Phase 1 runs beside it).  In the steady state a stage of both tiles takes
-//     2950 clocks against 2048 of its MMAs: a tile's chain S, softmax, PV is
-//     what bounds it, with the tensor pipe 0.69 busy; an item's start and
-//     epilogue add 6 us, Phase 2 takes 6 to 12.
-//   8 sequences behind 100,000 tokens (205 MB): 49.8 us, 4.1 TB/s; a stage takes
+//   256 sequences behind 8192 tokens, 16 to 512 of their own: 61.6 us (96
+//     items of 22 stages; the own tokens' Phase 1 runs beside them).  First
+//     scores at 5 us, the items' ends at 42 to 45, the own tokens' last item at
+//     55, Phase 2 from 56 to 60.  In the steady state a stage of both tiles
+//     takes 2950 clocks against 2048 of its MMAs: a tile's chain S, softmax, PV
+//     is what bounds it, with the tensor pipe 0.69 busy.
+//   8 sequences behind 100,000 tokens (205 MB): 49.5 us, 4.1 TB/s; a stage takes
 //     2850 clocks against 2790 that its bytes take at the copy rate, and the
 //     rest is start, epilogue and Phase 2.
 // Two softmax threads a row were slower (3200 clocks a stage and more: the
