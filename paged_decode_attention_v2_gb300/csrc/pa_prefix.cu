@@ -17,7 +17,8 @@
 // row a lane; a softmax thread owns a row: its maximum and sum need no
 // shuffles.  P goes back over S's columns, rounded to the input type (a weight
 // is off by 2^-8 of itself at most in bf16, 2^-11 in f16, with either sign; the
-// sum adds the unrounded exponentials), and is the PV product's A operand straight from tensor memory.
+// sum adds the unrounded exponentials), and is the PV product's A operand
+// straight from tensor memory.
 //   D 64, 128: two row tiles (NT 2) share every stage of 128 keys; while the
 //     softmax of one runs, the tensor cores work on the other:
 //     PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) ...
