@@ -37,7 +37,7 @@
 //     55, Phase 2 from 56 to 60.  In the steady state a stage of both tiles
 //     takes 2950 clocks against 2048 of its MMAs: a tile's chain S, softmax, PV
 //     is what bounds it, with the tensor pipe 0.69 busy.
-//   8 sequences behind 100,000 tokens (205 MB): 49.5 us, 4.1 TB/s; a stage takes
+//   8 sequences behind 100,000 tokens (205 MB): 48.2 us, 4.2 TB/s; a stage takes
 //     2850 clocks against 2790 that its bytes take at the copy rate, and the
 //     rest is start, epilogue and Phase 2.
 // Two softmax threads a row were slower (3200 clocks a stage and more: the
@@ -66,9 +66,10 @@ struct PrefixShape {
   static constexpr int QPANEL = kTileRows * 128;
   static constexpr int QTILE = PANELS * QPANEL;
   static constexpr int SOFTMAX_WARPS = 4 * NT;
-  // NT 2: a third warpgroup (two idle warps) whose registers the softmax
-  // warps take over: a row's 128 scores stay in registers
-  static constexpr int THREADS = (SOFTMAX_WARPS + (NT == 2 ? 4 : 2)) * 32;
+  // K's producer, the MMA warp, V's producer.  NT 2: a whole third warpgroup
+  // (one idle warp) whose registers the softmax warps take over: a row's 128
+  // scores stay in registers
+  static constexpr int THREADS = (SOFTMAX_WARPS + (NT == 2 ? 4 : 3)) * 32;
   // full and empty of each slot, Q ready a tile, S, P and (NT 2) half of P
   // ready a buffer, O done a tile, PV done (NT 1), drain, never
   static constexpr int BARS = 2 * SLOTS + 2 + 2 + 2 + 2 + 2 + 3;
@@ -306,14 +307,17 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
   // NT 2: 3 warpgroups at 168 registers, 2 x 208 + 80 <= 3 x 168
   if (warp >= Z::SOFTMAX_WARPS) {
     if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == Z::SOFTMAX_WARPS) {
-      // ======================= producer warp =======================
-      if (lane == 0) {
-        prefetch_tmap(&tmap_k);
-        prefetch_tmap(&tmap_v);
-      }
+    if (warp == Z::SOFTMAX_WARPS || warp == Z::SOFTMAX_WARPS + 2) {
+      // ======================= producer warps =======================
+      // One for K, one for V: a warp's copies of pages leave one after another,
+      // some 50 ns each, and a stage has 32 of them with pages of 8 (D 64, two
+      // sequences behind 60,000 tokens: 50.1 us a call with one warp, 40.7 with
+      // two; 8 behind 100,000, D 128, pages of 16: 49.5, 48.2).
+      const int kv = warp == Z::SOFTMAX_WARPS ? 0 : 1;
+      const CUtensorMap *tmap = kv == 0 ? &tmap_k : &tmap_v;
+      if (lane == 0) prefetch_tmap(tmap);
       bool ok = true;
-      int op = 0;  // copies issued: K and V of each stage, in turn
+      int op = kv;  // the next copy: K and V of each stage, in turn
       const int U = p.block_size;
       for (int item = blockIdx.x; ok && walk.find(p, item, it); item += gridDim.x) {
         const int32_t *bt = p.prefix_tables + (size_t)it.group * p.max_prefix_blocks;
@@ -336,26 +340,23 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
           }
           blk = next;
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, y >= 0)) * U * D * 2u;
-  #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const int sl = op % NS;
-            if (op >= NS) {
-              bool w = true;
-              if (lane == 0) w = mbar_wait(empty0 + 8 * sl, ((op / NS) - 1) & 1, limit, flags);
-              ok = __shfl_sync(0xffffffffu, w, 0);
-              if (!ok) break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * sl, bytes);
-            __syncwarp();
-            if (y >= 0)
-              tma_load_4d(ring_u32 + (uint32_t)sl * Z::SLOT + (uint32_t)(lane * U / 8) * Z::GROUP,
-                          kv == 0 ? &tmap_k : &tmap_v, 0, 0, 0, y >> 3, full0 + 8 * sl);
-            ++op;
+          const int sl = op % NS;
+          if (op >= NS) {
+            bool w = true;
+            if (lane == 0) w = mbar_wait(empty0 + 8 * sl, ((op / NS) - 1) & 1, limit, flags);
+            ok = __shfl_sync(0xffffffffu, w, 0);
+            if (!ok) break;
           }
+          if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * sl, bytes);
+          __syncwarp();
+          if (y >= 0)
+            tma_load_4d(ring_u32 + (uint32_t)sl * Z::SLOT + (uint32_t)(lane * U / 8) * Z::GROUP, tmap,
+                        0, 0, 0, y >> 3, full0 + 8 * sl);
+          op += 2;
         }
       }
       // the partitions of every row, for Phase 2: its own, then its prefix's
-      for (int s = blockIdx.x * 32 + lane; s < p.num_seqs; s += gridDim.x * 32) {
+      for (int s = blockIdx.x * 32 + lane; kv == 0 && s < p.num_seqs; s += gridDim.x * 32) {
         int lo = 0, hi = p.num_prefixes + 1;  // the first start above s
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
@@ -378,9 +379,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
         report(p.status, kStatusTimeout);
         flags[0] = 1;
       }
-      if (lane == 0)  // every copy lands before the CTA retires
-        for (int i = op > NS ? op - NS : 0; i < op; ++i)
-          mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1, kDrainLimitNs, nullptr);
+      if (lane == 0) flags[2 + kv] = op;
       __syncwarp();
     } else if (warp == Z::SOFTMAX_WARPS + 1) {
       // ======================= MMA warp =======================
@@ -737,6 +736,16 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (flags[0] && warp == Z::SOFTMAX_WARPS && lane < NS) {
+    // given up midway: every copy lands before the CTA retires (else the MMA
+    // warp has awaited them all).  Lane: the last copy into its slot
+    const int k_end = flags[2], v_end = flags[3], end = max(k_end, v_end);
+    for (int i = end - 1; i >= 0 && i > end - 1 - 2 * NS; --i)
+      if (i % NS == lane && i < ((i & 1) ? v_end : k_end)) {
+        mbar_wait(full0 + 8 * lane, (i / NS) & 1, kDrainLimitNs, nullptr);
+        break;
+      }
+  }
 }
 
 namespace {
@@ -792,8 +801,9 @@ void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads
   if (tiles < 1) tiles = 1;
   const long long heads = tiles * num_kv_heads;
   const int stages = (max_prefix_len + k.stage_keys - 1) / k.stage_keys;
-  const double pace = head_size == 64 ? 0.9 : head_size == 128 ? 1.4 : 0.65;
-  const double stage_us = (double)k.stage_keys * head_size * 4. / 6.3e6;  // of its bytes alone
+  const double pace = head_size == 64 ? 0.9 : head_size == 128 ? 1.5 : 0.87;
+  // of its bytes alone; several prefixes are taken as 0.8 of the bound on average
+  const double stage_us = (groups > 1 ? 0.8 : 1.) * k.stage_keys * head_size * 4. / 6.3e6;
   const double own_mb = (double)num_seqs * max_seq_len * 0.5 * num_kv_heads * head_size * 4e-6;
   const double own_parts = 0.7 * ((max_seq_len + partition_size - 1) / partition_size);
   int best = 1;
