@@ -160,6 +160,7 @@ __device__ __forceinline__ bool locate_row(const AppendParams &p, int row, RowIn
   const int lane = threadIdx.x & 31;
   int s = row, i = 0, n = 1;
   if (p.q_start) {
+    check_starts(p.q_start, p.num_seqs, row, p.num_rows, p.status);
     const int lo = first_above(p.q_start, p.num_seqs + 1, row);
     if (lo > p.num_seqs) return false;  // behind the last sequence
     if (lo == 0) {                      // before the first chunk: q_start[0] must be 0

@@ -49,6 +49,14 @@ __device__ __forceinline__ int first_above(const int32_t *a, int n, int x) {
   return lo;
 }
 
+// Reports starts that decrease; between them the rows of a call see every pair.
+__device__ __forceinline__ void check_starts(const int32_t *q_start, int num_seqs, int row,
+                                             int num_rows, int *status) {
+#pragma unroll 1
+  for (int s = row; s < num_seqs; s += num_rows)
+    if (__ldg(q_start + s + 1) < __ldg(q_start + s)) report(status, kStatusBadInput);
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

@@ -77,6 +77,7 @@ __device__ __forceinline__ void locate(const SelectParams &p, int row, int &seq,
   vis = 0;
   int before = 0, n = 1;  // the row's index in its chunk, the chunk's rows
   if (p.q_start) {
+    check_starts(p.q_start, p.num_seqs, row, p.num_rows, p.status);
     const int lo = first_above(p.q_start, p.num_seqs + 1, row);
     if (lo > p.num_seqs) {  // behind the last sequence: nothing to see
       seq = 0;
@@ -91,7 +92,7 @@ __device__ __forceinline__ void locate(const SelectParams &p, int row, int &seq,
     const int q0 = __ldg(p.q_start + seq);
     before = row - q0;
     n = __ldg(p.q_start + lo) - q0;
-    if (q0 < 0 || before < 0 || before >= n) {
+    if (q0 < 0 || before < 0 || before >= n || n > p.num_rows - q0) {
       report(p.status, kStatusBadInput);
       return;
     }

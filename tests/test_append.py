@@ -294,6 +294,20 @@ def test_infinite_keys_and_nan():
 
 
 @pytest.mark.gpu
+def test_starts_that_decrease_out_of_any_rows_sight_are_reported():
+    """Every row finds a chunk that holds it, but the chunks overlap."""
+    c = Case(16, torch.bfloat16, 2, 1, 64, 16, [4, 3, 3], [10, 10, 10], 64, offsets=[0, 0, 0])
+    dev = "cuda"
+    q, k, v = c.split(c.qkv.to(dev))
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    for qs, status in (([0, 4, 7, 10], pa.PA_OK), ([0, 6, 4, 10], pa.PA_ERR_DEVICE_BAD_INPUT)):
+        pa.pa_append_kv(c.kc.to(dev), c.vc.to(dev), k, v, c.bt.to(dev),
+                        torch.tensor(c.lens, dtype=torch.int32, device=dev), ws, cos_sin=c.cs.to(dev),
+                        q_start=torch.tensor(qs, dtype=torch.int32, device=dev))
+        assert pa.pa_read_device_status(ws) == status
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("what", ["block", "length", "negative", "chunk", "position", "rows", "order"])
 def test_bad_data_is_reported(what):
     """Each is found by the kernel's own checks before an address is formed; the

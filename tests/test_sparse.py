@@ -458,3 +458,51 @@ def test_many_rows_with_long_ones_among_them():
     assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
     assert torch.equal(d["sel"].cpu(), ref)
     assert_close(d["out"], c.attend(ref), c.dtype, "long rows among many")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("D,bs,G,K", [(64, 8, 3, 2), (128, 8, 8, 1), (256, 16, 2, 2)])
+def test_long_tables_and_chunks_of_many_lengths(dtype, D, bs, G, K):
+    """Chunks of no row, of one and of many; sequences that select every page
+    beside long ones; a row that sees a page more than the one before it."""
+    lens = [190 * bs + 1, 40, 140 * bs - 3, 30, 100 * bs + 8, 16, 21, 150 * bs]
+    chunks = [5, 2, 19, 0, 16, 1, 20, 8]
+    c = Case(30 + D, dtype, G * K, K, D, bs, lens, 9, 1, 2, chunks=chunks)
+    c.check()
+    c.check(calls=1, max_seq_len=190 * bs + 1)
+
+
+@pytest.mark.gpu
+def test_many_sequences_of_two_rows():
+    lens = [2 + (i * 37) % 1023 for i in range(99)] + [1024]
+    Case(31, torch.float16, 8, 4, 64, 8, lens, 7, 1, 1, chunks=[2] * 100).check(calls=1)
+
+
+@pytest.mark.gpu
+def test_padded_rows_and_bad_chunks():
+    c = Case(32, torch.bfloat16, 4, 2, 64, 8, [1100, 900, 300], 6, 1, 1, chunks=[9, 3, 2])
+    d = c.device()
+    ref, want = c.select(), c.attend(c.select())
+    for name in ("q", "out", "sel"):
+        d[name] = torch.cat([d[name], d[name][:11]])
+    d["ws"] = pa.alloc_sparse_workspace(25, 4, 2, 64, 8, d["m"], 6, c.P)
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    assert torch.equal(d["sel"][:14].cpu(), ref) and (d["sel"][14:] == -1).all()
+    assert_close(d["out"][:14], want, c.dtype, "rows of the chunks")
+    assert (d["out"][14:] == 0).all()
+    good = d["qs"].clone()
+    for bad in ([0, 9, 12, 99], [0, 12, 9, 14], [-4, 9, 12, 14], [3, 9, 12, 14], [9, 9, 9, 9]):
+        d["qs"].copy_(torch.tensor(bad))
+        c.run(d)
+        if bad != [9, 9, 9, 9]:  # (rows in no chunk, as padding is)
+            assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_BAD_INPUT
+        pa.pa_workspace_init(d["ws"])
+    for n in (1101, -1, 8):
+        d["qs"].copy_(good)
+        d["sl"][0] = n
+        c.run(d)
+        assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_BAD_INPUT
+        assert torch.equal(d["sel"][9:14].cpu(), ref[9:])
+        assert_close(d["out"][9:14], want[9:], c.dtype, "the other sequences")
