@@ -16,9 +16,11 @@
 // j + 1, ...  One thread issues the MMAs.  S lives in tensor memory, fp32, one
 // row a lane; a softmax thread owns a row: its maximum and sum need no
 // shuffles.  P goes back over S's columns, rounded to the input type (a weight
-// is off by 2^-8 of itself at most in bf16, 2^-11 in f16, with either sign; the
-// sum adds the unrounded exponentials), and is the PV product's A operand
-// straight from tensor memory.
+// is off by 2^-8 of itself at most in bf16, 2^-11 in f16, with either sign), and
+// is the PV product's A operand straight from tensor memory.  The sum adds the
+// rounded weights, so that those that V is multiplied with sum to one: with the
+// lazy maximum below a weight that outweighs all others is any number up to
+// 2^8, and its rounding would be the result's.
 //   D 64, 128: two row tiles (NT 2) share every stage of 128 keys; while the
 //     softmax of one runs, the tensor cores work on the other:
 //     PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) ...
@@ -44,6 +46,8 @@
 // exchange of their maxima joins the chain), an epilogue in full lines through
 // shared memory the same.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_ops.h"
@@ -122,10 +126,19 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// lo += the low half of x (two numbers of type T), hi += the high half, in fp32
+template <typename T>
+__device__ __forceinline__ void add_halves(uint32_t x, float &lo, float &hi) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.rn.f32.f16 %0, l, %0;\n"
+        " add.rn.f32.f16 %1, h, %1;\n}"
+        : "+f"(lo), "+f"(hi)
+        : "r"(x));
+  else
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.rn.f32.bf16 %0, l, %0;\n"
+        " add.rn.f32.bf16 %1, h, %1;\n}"
+        : "+f"(lo), "+f"(hi)
+        : "r"(x));
 }
 // eight floats in one store (32-byte aligned)
 __device__ __forceinline__ void store8(float *dst, const float (&v)[8]) {
@@ -657,7 +670,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
           }
           const float mb = m_run == -CUDART_INF_F ? 0.f : -m_run;
           const uint64_t sc2 = pair(sc, sc), mb2 = pair(mb, mb);
-          uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
           // P over the scores' own registers (word e holds keys 2e, 2e + 1), so
           // that no register waits for a store in flight
           auto weights = [&](int h, int e0, int e1) {
@@ -665,9 +678,8 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
             for (int e = e0; e < e1; ++e) {
               const int k = 64 * h + 2 * e;
               const float2 y = unpair(fma2(pair(x(k), x(k + 1)), sc2, mb2));
-              const float p0 = ex2(y.x), p1 = ex2(y.y);
-              l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
-              s[h][e] = MmaOp<T>::pack(p0, p1);
+              s[h][e] = MmaOp<T>::pack(ex2(y.x), ex2(y.y));
+              add_halves<T>(s[h][e], ls[2 * (e & 1)], ls[2 * (e & 1) + 1]);
             }
           };
           weights(0, 0, 32);
@@ -682,8 +694,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
             weights(1, 8, 32);
             tmem_st32(sbuf + 32, s[1]);
           }
-          const float2 ls = unpair(add2(l2[0], l2[1]));
-          l = fmaf(l, alpha, ls.x + ls.y);
+          l = fmaf(l, alpha, (ls[0] + ls[2]) + (ls[1] + ls[3]));
           tmem_st_wait();
         } else if (NT == 2) {
           if (lane == 0) mbar_arrive(p_half + 8 * buf);

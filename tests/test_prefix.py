@@ -427,3 +427,52 @@ def test_two_streams_at_once():
     for c, d, ref, s in state:
         assert pa.pa_read_device_status(d["ws"], s) == pa.PA_OK
         assert_close(d["out"], ref, c.dtype, "two streams")
+
+
+def ramp(dtype, D, stages, v):
+    """Keys whose logits step up by 4.1 to 5.4 from stage to stage of the kernel,
+    less than its lazy maximum's margin of 8 ln 2: the largest weight, of the
+    last stage, is any number up to 2^8, another one for every row.  Every value
+    is v."""
+    step = 64 if D == 256 else 128
+    c = Case(30, dtype, 4, 1, D, 16, [8], [stages * step], list(range(8)), scale=1.0)
+    c.q.zero_()
+    c.q[..., 0] = torch.linspace(0.85, 1.1, 32).view(8, 4)
+    c.kc[..., 0] = -60.0
+    for j in range(stages):
+        t = j * step
+        c.kc[c.pt[0, t // 16], :, t % 16, 0] = max(-40.0, 4.875 * (j - stages + 1))
+    c.vc.fill_(v)
+    return c
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("stages", [384, 383, 300])
+def test_weights_sum_to_one(dtype, D, stages):
+    """Values that are all alike come out as they are, whatever the weights: the
+    rounded ones are what is divided by.  Sums and quotients in fp32, of at most
+    200 terms each in a split and 65 splits, are off by less than 2^-14, less
+    than the 2^-9 (bf16) or 2^-12 (f16) that would round to another value."""
+    v = 2.0 - torch.finfo(dtype).eps
+    d = (c := ramp(dtype, D, stages, v)).device()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    assert (d["out"] == v).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_peaky_logits_within_the_parity_bar(dtype, D):
+    """Growing keys, where few carry all the weight: the bar of every other call
+    of the library holds."""
+    c = Case(6, dtype, 4, 1, D, 16, [40], [1500], [9] * 40, k_mult=1.0)
+    for j in range(c.pt.shape[1]):
+        c.kc[c.pt[0, j]] *= 0.1 * (1 + j)
+    c.check()
+    c = ramp(dtype, D, 20, 0.0)
+    g = torch.Generator().manual_seed(31)
+    c.vc.copy_(torch.randn(c.vc.shape, generator=g))
+    c.check()
