@@ -16,11 +16,12 @@
 // j + 1, ...  One thread issues the MMAs.  S lives in tensor memory, fp32, one
 // row a lane; a softmax thread owns a row: its maximum and sum need no
 // shuffles.  P goes back over S's columns, rounded to the input type (a weight
-// is off by 2^-8 of itself at most in bf16, 2^-11 in f16, with either sign), and
-// is the PV product's A operand straight from tensor memory.  The sum adds the
-// rounded weights, so that those that V is multiplied with sum to one: with the
-// lazy maximum below a weight that outweighs all others is any number up to
-// 2^8, and its rounding would be the result's.
+// is off by 2^-8 of itself at most in bf16; in f16 by 2^-11, or 2^-32 of the
+// split's largest weight where that is more), and is the PV product's A operand
+// straight from tensor memory.  The sum adds the rounded weights, so that those
+// that V is multiplied with sum to one: with the lazy maximum below a weight
+// that outweighs all others is any number up to 2^8, and its rounding would be
+// the result's.
 //   D 64, 128: two row tiles (NT 2) share every stage of 128 keys; while the
 //     softmax of one runs, the tensor cores work on the other:
 //     PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) ...
@@ -58,6 +59,11 @@ namespace {
 
 constexpr int kTileRows = 128;      // the MMA's M
 constexpr float kLazyMargin = 8.f;  // log2 units
+// Weights are 2^(s - m + this): a weight below f16's normal range loses bits
+// and below 2^-25 becomes zero, so f16's start 2^7 higher (with the margin
+// 2^15, below its largest number).  The sum takes the factor out again.
+template <typename T>
+constexpr float kWeightShift = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 template <int D>
 struct PrefixShape {
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
             }
             tmem_st_wait();
           }
-          const float mb = m_run == -CUDART_INF_F ? 0.f : -m_run;
+          const float mb = m_run == -CUDART_INF_F ? 0.f : kWeightShift<T> - m_run;
           const uint64_t sc2 = pair(sc, sc), mb2 = pair(mb, mb);
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
           // P over the scores' own registers (word e holds keys 2e, 2e + 1), so
@@ -729,7 +735,8 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
           }
         }
         if (live) {
-          p.max_logits[slot] = m_run * 0.69314718055994530942f;  // natural-log units
+          // what the weights are relative to, in natural-log units
+          p.max_logits[slot] = (m_run - kWeightShift<T>) * 0.69314718055994530942f;
           p.exp_sums[slot] = l;
         }
       }

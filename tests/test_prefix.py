@@ -476,3 +476,19 @@ def test_peaky_logits_within_the_parity_bar(dtype, D):
     g = torch.Generator().manual_seed(31)
     c.vc.copy_(torch.randn(c.vc.shape, generator=g))
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_f16_weights(D):
+    """Weights of 2^-26 beside one of 1, every 64 keys, whose values make up for
+    it: f16's smallest number is 2^-24.  A weight is off by at most 2^-32 of the
+    largest, so the result by 63 x 2^-32 x 57344 = 8e-4, inside the bar."""
+    c = Case(32, torch.float16, 4, 1, D, 16, [3], [640], [0, 1, 5], scale=1.0)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.kc[..., 0], c.vc[:] = -18.25, 57344.0
+    for t in range(0, 640, 64):
+        page = c.pt[0, t // 16]
+        c.kc[page, :, t % 16, 0], c.vc[page, :, t % 16] = 0.0, 0.0
+    c.check()
