@@ -500,10 +500,13 @@ size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
  * zeros.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); the other arguments and
  * limits as pa_v2_forward.  The workspace holds pa_prefix_workspace_bytes(...)
  * bytes, initialised once by pa_workspace_init (any workspace that is large
- * enough serves calls of any shape, one after another).  Bad tables, lengths or
- * groups are reported as PA_ERR_DEVICE_BAD_INPUT; the rows in question (with
- * starts out of order, any row) then hold no meaningful values.  opts as in pa_forward (variant V2 or auto; no fused
- * combine, no CUDA-core path). */
+ * enough serves calls of any shape, one after another).  The prefix is split as
+ * these sizes and the workspace's suggest, and the splits' sums are rounded
+ * apart: the same call on workspaces of other sizes may differ in last bits.
+ * Bad tables, lengths or groups are reported as PA_ERR_DEVICE_BAD_INPUT; the
+ * rows in question (with starts out of order, any row) then hold no meaningful
+ * values.  opts as in pa_forward (variant V2 or auto; no fused combine, no
+ * CUDA-core path). */
 pa_status_t pa_prefix_forward(void *out, const void *query,
                               const void *key_cache, const void *value_cache,
                               const int32_t *block_tables,
@@ -521,10 +524,10 @@ pa_status_t pa_prefix_forward(void *out, const void *query,
                               const pa_options_t *opts);
 
 /* Bytes of workspace for pa_prefix_forward (0 on bad arguments): as
- * pa_workspace_bytes with slots for the prefix's splits, which the library
- * chooses from these sizes, behind every row's own partitions.  Fewer
- * sequences may get more splits: a workspace for batches of several sizes is
- * the largest of their needs. */
+ * pa_workspace_bytes with slots for the prefix's splits behind every row's own
+ * partitions.  A workspace for the largest num_seqs, num_prefixes, max_seq_len
+ * and max_prefix_len serves calls with smaller ones (the other sizes alike):
+ * they take as many splits as it holds. */
 size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads,
                                  int num_kv_heads, int head_size,
                                  int max_seq_len, int max_prefix_len,

@@ -440,7 +440,7 @@ def pa_prefix_workspace_bytes(num_seqs: int, num_prefixes: int, num_heads: int, 
 def alloc_prefix_workspace(num_seqs: int, num_prefixes: int, num_heads: int, num_kv_heads: int,
                            head_size: int, max_seq_len: int, max_prefix_len: int,
                            partition_size: int, device=None, stream=None) -> torch.Tensor:
-    """A zeroed workspace for pa_prefix_forward."""
+    """A zeroed workspace for pa_prefix_forward, with these sizes or smaller ones."""
     n = pa_prefix_workspace_bytes(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size,
                                   max_seq_len, max_prefix_len, partition_size)
     if n == 0:

@@ -880,15 +880,36 @@ bool device_view(void *host, void **dev) {
   return true;
 }
 
-// Workspace of a shared-prefix call with `splits` splits of the prefix: V2's,
-// with as many slots more a row, and the rows' slot counts (0: too large).
+// Workspace of a shared-prefix call: V2's with slots for `slots` splits'
+// partials behind the rows' own, and the rows' slot counts (0: too large).
 size_t prefix_bytes(int num_seqs, int num_heads, int head_size, int max_seq_len,
-                    int partition_size, int splits) {
-  const long long parts = (long long)max_parts_of(max_seq_len, partition_size) + splits;
+                    int partition_size, long long slots) {
+  const long long own = max_parts_of(max_seq_len, partition_size);
+  const long long rows = (long long)num_seqs * num_heads;
+  const long long parts = own + (rows > 0 ? (slots + rows - 1) / rows : 0);
   if (parts > kMaxReduceParts || parts * partition_size > INT_MAX - partition_size) return 0;
-  return pa_workspace_bytes(num_seqs, num_heads, head_size, (int)parts * partition_size,
-                            partition_size) +
-         align256((size_t)num_seqs * 4);
+  const size_t n = (size_t)(rows * own + slots);
+  return kStatusBytes + 2 * align256(n * 4) + align256(n * head_size * 4) +
+         align256((size_t)rows * 4) + align256((size_t)num_seqs * 4);
+}
+
+// What a call of these sizes asks for.  It grows with every size, so that a
+// workspace for larger sizes serves smaller ones, whose best number of splits
+// may be larger: slots for the rows of one wave of the prefix kernel's items
+// (or two splits of every row, with more rows than that), and no more than the
+// prefix has stages.  With more than one wave of items the best number may lie
+// above it: pa_prefix_workspace_bytes then gives that, and a call takes as many
+// splits as its workspace holds.
+size_t prefix_least_bytes(int num_seqs, int num_heads, int head_size, int max_seq_len,
+                          int max_prefix_len, int partition_size) {
+  const PrefixKernelInfo k = prefix_kernel(1, head_size);
+  const long long rows = (long long)num_seqs * num_heads;
+  long long splits = (max_prefix_len + k.stage_keys - 1) / k.stage_keys;
+  if (splits > kMaxPrefixSplits) splits = kMaxPrefixSplits;
+  long long most = (long long)kPrefixSms * k.tile_rows;
+  if (most < 2 * rows) most = 2 * rows;
+  const long long slots = rows * splits < most ? rows * splits : most;
+  return prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, slots);
 }
 
 // Enqueue the kernel that copies pa_forward_host's inputs (three segments:
@@ -1134,8 +1155,12 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, 
     return 0;
   int split = 0, splits = 0;
   prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
-              max_prefix_len, partition_size, &split, &splits);
-  return prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, splits);
+              max_prefix_len, partition_size, kMaxPrefixSplits, &split, &splits);
+  const size_t least = prefix_least_bytes(num_seqs, num_heads, head_size, max_seq_len,
+                                          max_prefix_len, partition_size);
+  const size_t best = prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size,
+                                   (long long)num_seqs * num_heads * splits);
+  return best > least ? best : least;
 }
 
 pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cache,
@@ -1176,11 +1201,21 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   if (opt.math == PA_MATH_SIMT) return PA_ERR_UNSUPPORTED;
   if (opt.math != PA_MATH_AUTO && opt.math != PA_MATH_TENSOR) return PA_ERR_INVALID_ARG;
   if (opt.num_stages > 0 && (opt.num_stages < 2 || opt.num_stages > 16)) return PA_ERR_INVALID_ARG;
+  const size_t least = prefix_least_bytes(num_seqs, num_heads, head_size, max_seq_len,
+                                          max_prefix_len, partition_size);
+  if (least == 0) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < least) return PA_ERR_WORKSPACE_TOO_SMALL;
+  // the most splits that the workspace holds
+  const long long rows_out = (long long)num_seqs * num_heads;
+  auto bytes = [&](int n) {
+    return prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, rows_out * n);
+  };
+  int cap = kMaxPrefixSplits;
+  while (cap > 1 && (bytes(cap) == 0 || bytes(cap) > workspace_bytes)) --cap;
   int split = 0, splits = 0;
   prefix_plan(num_seqs, num_prefixes, num_heads, num_kv_heads, head_size, max_seq_len,
-              max_prefix_len, partition_size, &split, &splits);
-  const size_t need =
-      prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size, splits);
+              max_prefix_len, partition_size, cap, &split, &splits);
+  const size_t need = bytes(splits);
   if (need == 0) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
   c.workspace_bytes = workspace_bytes;

@@ -35,6 +35,7 @@ __host__ __device__ __forceinline__ int view_block(int blk, int kv_head, int num
 }
 
 constexpr int kMaxPrefixSplits = 64;
+constexpr int kPrefixSms = 152;  // what the splits are planned for
 constexpr int kPrefixDebugStall = 1;  // PA_DEBUG_STALL_CONSUMERS
 
 struct PrefixParams {
@@ -65,8 +66,8 @@ struct PrefixKernelInfo {
 };
 PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size);
 void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
-                 int max_seq_len, int max_prefix_len, int partition_size, int *split_tokens,
-                 int *max_splits);
+                 int max_seq_len, int max_prefix_len, int partition_size, int most_splits,
+                 int *split_tokens, int *max_splits);
 
 // An item scored and selected from in one CTA, or scored by several and
 // selected from in a second launch.

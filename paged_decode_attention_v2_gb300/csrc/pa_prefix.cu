@@ -788,7 +788,7 @@ PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size) {
   return dtype_bf16 ? pick<__nv_bfloat16>(head_size) : pick<__half>(head_size);
 }
 
-// Splits of the prefix, from a model of the call's time in microseconds
+// Splits of the prefix, at most most_splits, from a model of the call's time in microseconds
 // (coefficients measured on GB300; the sizes of the groups are not known on
 // the host, so a row tile is counted as half empty a group, and own lengths as
 // half their bound):
@@ -807,9 +807,8 @@ PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size) {
 //     us, 38 splits, 152 items, 48.7 us, 34 splits, 49.9 us);
 //   - Phase 2: every split is another partial of every row.
 void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads, int head_size,
-                 int max_seq_len, int max_prefix_len, int partition_size, int *split_tokens,
-                 int *max_splits) {
-  constexpr int kSms = 152;
+                 int max_seq_len, int max_prefix_len, int partition_size, int most_splits,
+                 int *split_tokens, int *max_splits) {
   const PrefixKernelInfo k = prefix_kernel(1, head_size);
   const double rows = (double)num_seqs * (num_heads / num_kv_heads);
   const int groups = num_prefixes < num_seqs ? num_prefixes : (num_seqs > 0 ? num_seqs : 1);
@@ -826,14 +825,14 @@ void prefix_plan(int num_seqs, int num_prefixes, int num_heads, int num_kv_heads
   const double own_parts = 0.7 * ((max_seq_len + partition_size - 1) / partition_size);
   int best = 1;
   double best_cost = 0.;
-  for (int n = 1; n <= kMaxPrefixSplits && (n == 1 || n <= stages); ++n) {
+  for (int n = 1; n <= most_splits && (n == 1 || n <= stages); ++n) {
     const int per = (stages + n - 1) / n;
     const long long items = heads * (per > 0 ? (stages + per - 1) / per : 1);
-    const long long waves = (items + kSms - 1) / kSms;
-    const long long active = items < kSms ? items : kSms;
+    const long long waves = (items + kPrefixSms - 1) / kPrefixSms;
+    const long long active = items < kPrefixSms ? items : kPrefixSms;
     const double bytes_pace = (double)active * groups / tiles * stage_us;
     const double t = waves * (per * (bytes_pace > pace ? bytes_pace : pace) + 10.);
-    const double beside = waves == 1 ? (kSms - active) * 0.05 : 0.;  // MB a us
+    const double beside = waves == 1 ? (kPrefixSms - active) * 0.05 : 0.;  // MB a us
     const double left_mb = own_mb - t * beside;
     double after = left_mb > 0. ? 3. + left_mb / 5.7 : 0.;
     if (left_mb > 0. && left_mb < after * beside) after = left_mb / beside;

@@ -77,6 +77,33 @@ def test_workspace_bytes(lib):
     assert f(3, 1, 8, 2, 128, 0, 0, 512) > 0
 
 
+def test_a_workspace_serves_every_smaller_call(lib):
+    """Sized for the largest batch, prefix and own lengths, a workspace is
+    refused by no call of smaller ones, whose best number of splits may be
+    larger.  (Without a device a call that passes its checks ends right behind
+    them.)"""
+    if torch.cuda.is_available():
+        pytest.skip("for the host's checks alone: the addresses are made up")
+    rng = random.Random(1)
+    log = lambda lo, hi: round(math.exp(rng.uniform(math.log(lo), math.log(hi))))  # noqa: E731
+    pairs = [((256, 1, 512, 32768), (224, 1, 512, 32768), 4, 8, 128)]
+    for _ in range(3000):
+        large = (log(1, 3000), rng.choice([1, 1, 2, 5, 30]), rng.choice([0, 64, 512, 5000]), log(64, 400_000))
+        small = tuple(n if rng.random() < 0.4 else max(lo, n - rng.randint(0, n) if rng.random() < 0.5
+                                                       else n - min(n, rng.randint(0, 9)))
+                      for n, lo in zip(large, (1, 1, 0, 0)))
+        pairs.append((large, small, rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 4, 8, 16]),
+                      rng.choice([64, 128, 256])))
+    for (B, G, own, prefix), (b, g, o, p), K, heads, D in pairs:
+        P = rng.choice([64, 256, 512])
+        n = pa.pa_prefix_workspace_bytes(B, G, heads * K, K, D, own, prefix, P)
+        a = dict(BASE, num_seqs=b, num_prefixes=g, num_heads=heads * K, num_kv_heads=K, head_size=D,
+                 max_seq_len=o, max_prefix_len=p, partition_size=P, max_blocks_per_seq=1 << 15,
+                 max_prefix_blocks=1 << 15, workspace_bytes=n)
+        assert n > 0 and lib.pa_prefix_forward(*a.values()) == pa.PA_ERR_CUDA, \
+            (B, G, own, prefix, b, g, o, p, K, heads, D, P)
+
+
 # ---------------------------------------------------------------------------
 
 class Case:
@@ -492,3 +519,24 @@ def test_small_f16_weights(D):
         page = c.pt[0, t // 16]
         c.kc[page, :, t % 16, 0], c.vc[page, :, t % 16] = 0.0, 0.0
     c.check()
+
+
+@pytest.mark.gpu
+def test_fewer_splits_in_the_workspace_of_a_larger_batch():
+    """132 sequences ask for less than 125, which would have more splits: these
+    run with as many as there is room for."""
+    counts = [3, 2, 90, 5, 0, 15, 0, 10]
+    c = Case(33, torch.bfloat16, 64, 8, 256, 16, counts, [6000, 30, 700, 1, 5, 300, 9, 2049],
+             [i % 65 for i in range(125)])
+    sizes = (8, 64, 8, 256, 64, 6000, 512)
+    assert pa.pa_prefix_workspace_bytes(132, *sizes) < pa.pa_prefix_workspace_bytes(125, *sizes)
+    d, ref = c.device(), c.reference()
+    n = pa.pa_prefix_workspace_bytes(132, *sizes)
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    d["ws"] = buf[:n]
+    d["ws"][:256] = 0
+    for _ in range(2):
+        c.run(d)
+        assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+        assert_close(d["out"], ref, c.dtype, "the larger batch's workspace")
+    assert (buf[n:] == 0xA5).all()
