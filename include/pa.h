@@ -430,7 +430,7 @@ pa_status_t pa_append_kv(void *key_cache, void *value_cache, void *key_bounds,
  *               the sequence, ascending, -1 behind the last
  * 0 <= sink_blocks, 1 <= recent_blocks, sink_blocks + recent_blocks <=
  * num_selected.  query, block_tables, seq_lens and the limits on sizes as in
- * pa_forward, f32 included; query contiguous [num_rows][num_heads][head_size].
+ * pa_forward, f32 included, and max_seq_len at most 2^30; query contiguous [num_rows][num_heads][head_size].
  * The workspace holds pa_sparse_workspace_bytes(...) bytes, initialised once by
  * pa_workspace_init (one sized for the largest call serves smaller ones too);
  * partition_size is the one it was sized with, and the largest partition of
@@ -497,8 +497,9 @@ size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
  *                  are group g; a group may be empty
  * block_tables and seq_lens hold the own tokens only, with max_seq_len their
  * bound (0 if no sequence has any).  Sequences with no tokens at all get
- * zeros.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); the other arguments and
- * limits as pa_v2_forward.  The workspace holds pa_prefix_workspace_bytes(...)
+ * zeros.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); max_seq_len and
+ * max_prefix_len at most 2^30; the other arguments and limits as
+ * pa_v2_forward.  The workspace holds pa_prefix_workspace_bytes(...)
  * bytes, initialised once by pa_workspace_init (any workspace that is large
  * enough serves calls of any shape, one after another).  The prefix is split as
  * these sizes and the workspace's suggest, and the splits' sums are rounded

@@ -1151,6 +1151,7 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, 
                                  int partition_size) {
   if (num_seqs < 0 || num_prefixes < 1 || num_heads < 1 || num_kv_heads < 1 ||
       num_heads % num_kv_heads || max_seq_len < 0 || max_prefix_len < 0 || partition_size < 1 ||
+      max_seq_len > kMaxTokens || max_prefix_len > kMaxTokens || partition_size > kMaxTokens ||
       (head_size != 64 && head_size != 128 && head_size != 256))
     return 0;
   int split = 0, splits = 0;
@@ -1160,7 +1161,7 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, 
                                           max_prefix_len, partition_size);
   const size_t best = prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size,
                                    (long long)num_seqs * num_heads * splits);
-  return best > least ? best : least;
+  return least == 0 || best < least ? least : best;
 }
 
 pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cache,
@@ -1187,6 +1188,7 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
     return PA_ERR_INVALID_ARG;
   if (block_size > 0 && (long long)max_prefix_len > (long long)max_prefix_blocks * block_size)
     return PA_ERR_INVALID_ARG;
+  if (max_seq_len > kMaxTokens || max_prefix_len > kMaxTokens) return PA_ERR_UNSUPPORTED;
   Call c = make_call(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_heads, num_kv_heads, head_size, num_blocks, block_size,
                      max_blocks_per_seq, max_seq_len, scale, partition_size, dtype, workspace,

@@ -34,6 +34,11 @@ __host__ __device__ __forceinline__ int view_block(int blk, int kv_head, int num
   return (unsigned)blk < (unsigned)num_blocks ? blk * num_kv_heads + kv_head : -1;
 }
 
+// The longest prefix, and the longest sequence beside one or with selected
+// blocks: lengths stay 31-bit numbers with a split or a page added (and no
+// cache that fits the GPU holds more).
+constexpr int kMaxTokens = 1 << 30;
+
 constexpr int kMaxPrefixSplits = 64;
 constexpr int kPrefixSms = 152;  // what the splits are planned for
 constexpr int kPrefixDebugStall = 1;  // PA_DEBUG_STALL_CONSUMERS

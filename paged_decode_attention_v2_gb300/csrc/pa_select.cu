@@ -887,7 +887,7 @@ bool sparse_layout(int num_rows, int num_heads, int num_kv_heads, int head_size,
     return false;
   const long long items = (long long)num_rows * num_kv_heads;
   const long long cap = (long long)num_selected * block_size;
-  if (items > 0x7fffffffll || cap > 0x7fffffffll) return false;
+  if (items > 0x7fffffffll || cap > 0x7fffffffll || max_seq_len > kMaxTokens) return false;
   o->max_pages = (int)(((long long)max_seq_len + block_size - 1) / block_size);
   o->view_len = (int)(cap < max_seq_len ? cap : max_seq_len);
   o->partition = view_partition(items, o->view_len, partition_size, block_size);

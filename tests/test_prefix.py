@@ -104,6 +104,21 @@ def test_a_workspace_serves_every_smaller_call(lib):
             (B, G, own, prefix, b, g, o, p, K, heads, D, P)
 
 
+@pytest.mark.parametrize("n", [2 ** 30 + 1, 2 ** 31 - 129, 2 ** 31 - 1])
+def test_lengths_beyond_31_bit_arithmetic_are_refused(lib, n):
+    """They have no size and are no call, whatever the table could hold: with a
+    split added they would pass 2^31."""
+    f = pa.pa_prefix_workspace_bytes
+    for D in (64, 128, 256):
+        for P in (64, 512, 8192):
+            assert f(3, 1, 8, 2, D, 128, n, P) == f(3, 1, 8, 2, D, n, 128, P) == f(3, 1, 8, 2, D, n, n, P) == 0
+    for over in (dict(max_prefix_len=n), dict(max_seq_len=n)):
+        a = dict(BASE, max_prefix_blocks=2 ** 31 - 1, max_blocks_per_seq=2 ** 31 - 1,
+                 workspace_bytes=1 << 40, **over)
+        assert lib.pa_prefix_forward(*a.values()) == pa.PA_ERR_UNSUPPORTED
+    assert 0 < f(3, 1, 8, 2, 128, 128, 2 ** 30, 512) < 1 << 24
+
+
 # ---------------------------------------------------------------------------
 
 class Case:

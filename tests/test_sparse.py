@@ -63,6 +63,17 @@ def test_sparse_refusals(lib, over, status):
     assert lib.pa_sparse_forward(*dict(BASE, **over).values()) == status
 
 
+@pytest.mark.parametrize("n", [2 ** 30 + 1, 2 ** 31 - 16, 2 ** 31 - 1])
+def test_lengths_beyond_31_bit_arithmetic_are_refused(lib, n):
+    """With a page added they could pass 2^31."""
+    assert pa.pa_sparse_workspace_bytes(2, 8, 2, 128, 16, n, 4, 512) == 0
+    a = dict(BASE, max_seq_len=n, max_blocks_per_seq=2 ** 31 - 1, workspace_bytes=1 << 50)
+    assert lib.pa_sparse_forward(*a.values()) == pa.PA_ERR_UNSUPPORTED
+    for name in ("out", "key_cache", "value_cache", "scale"):
+        del a[name]
+    assert lib.pa_select_blocks(*a.values()) == pa.PA_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("over,status", REFUSALS + [
     (dict(selected=0), pa.PA_ERR_INVALID_ARG),
     (dict(key_bounds=0), pa.PA_ERR_INVALID_ARG),
