@@ -522,6 +522,26 @@ pa_status_t launch_phase2(const Phase2Plan &plan, cudaStream_t stream) {
   return PA_OK;
 }
 
+// Items of at most 16 rows on tcgen05 with the keys on the MMA's M, when
+// asked for (PA_DEBUG_TCGEN05_KEYS), unless the combine is to be fused
+// into Phase 1, which only the mma.sync kernels do.  Not the default:
+// measured on GB300 (16 heads a group on the 256-sequence cache) it takes
+// 0.123-0.146 ms (V2) / 0.116-0.126 ms (V1) a step, on two boxes, against
+// the two-n-tile mma.sync kernel's 0.098 ms: one CTA an SM does not cover
+// its item boundaries.  (On the tensor path.)
+bool keys_kernel(const Call &c, bool v2, const pa_options_t &opt) {
+  const int group = c.num_heads / c.num_kv_heads;
+  const long long item_rows = c.q_start ? (long long)c.max_chunk * group : group;
+  return (opt.debug_flags & PA_DEBUG_TCGEN05_KEYS) && !(opt.debug_flags & PA_DEBUG_NO_TCGEN05) &&
+         umma_keys_ok(c.head_size, item_rows) && aligned(c.query, 16) &&
+         !(v2 && !c.q_start && opt.fuse_partitions > 0);
+}
+
+// Phase 1 runs beside the prefix kernel before it (AttnParams::late_wait).
+bool late_wait(const Call &c, const pa_options_t &opt) {
+  return c.extra_parts > 0 && !keys_kernel(c, true, opt);
+}
+
 pa_status_t launch(const Call &c, bool v2, const pa_options_t &opt) {
   DeviceFacts *dev = nullptr;
   pa_status_t st = device_facts(&dev);
@@ -535,17 +555,8 @@ pa_status_t launch(const Call &c, bool v2, const pa_options_t &opt) {
   const bool chunk = c.q_start != nullptr;
   if (chunk && math != kMathTensor) return PA_ERR_UNSUPPORTED;
   const bool tc = math == kMathTensor && !(opt.debug_flags & PA_DEBUG_NO_TCGEN05);
-  // Items of at most 16 rows on tcgen05 with the keys on the MMA's M, when
-  // asked for (PA_DEBUG_TCGEN05_KEYS), unless the combine is to be fused
-  // into Phase 1, which only the mma.sync kernels do.  Not the default:
-  // measured on GB300 (16 heads a group on the 256-sequence cache) it takes
-  // 0.123-0.146 ms (V2) / 0.116-0.126 ms (V1) a step, on two boxes, against
-  // the two-n-tile mma.sync kernel's 0.098 ms: one CTA an SM does not cover
-  // its item boundaries.
   const long long item_rows = chunk ? (long long)c.max_chunk * group : group;
-  const bool keys = tc && (opt.debug_flags & PA_DEBUG_TCGEN05_KEYS) &&
-                    umma_keys_ok(c.head_size, item_rows) && aligned(c.query, 16) &&
-                    !(v2 && !chunk && opt.fuse_partitions > 0);
+  const bool keys = tc && keys_kernel(c, v2, opt);
   const bool umma = chunk && tc && umma_chunk_ok(c.head_size, group, item_rows);
   // tcgen05 chunks of several 128-row groups per KV head, when asked
   // (share_kv): a cluster of 2 or 4 CTAs takes them together, sharing each
@@ -689,7 +700,7 @@ pa_status_t launch(const Call &c, bool v2, const pa_options_t &opt) {
   }
   p.num_stages = stages;
   p.debug_flags = opt.debug_flags;
-  p.late_wait = c.extra_parts > 0 && !k.umma;  // behind the prefix kernel
+  p.late_wait = late_wait(c, opt);
   p.scale_log2 = (float)((double)c.scale * 1.4426950408889634);
   p.wait_limit_ns = opt.wait_limit_ns ? opt.wait_limit_ns : kDefaultWaitLimitNs;
 
@@ -1200,6 +1211,8 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   if (st != PA_OK) return st;
   if (dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;  // tensor path only
   if ((long long)num_seqs * (num_heads / num_kv_heads) >= (1ll << 28)) return PA_ERR_UNSUPPORTED;
+  if ((long long)num_seqs * num_kv_heads * max_parts_of(max_seq_len, partition_size) >= kReadyBit / 2)
+    return PA_ERR_UNSUPPORTED;  // own items, counted below the bit
   if (opt.math == PA_MATH_SIMT) return PA_ERR_UNSUPPORTED;
   if (opt.math != PA_MATH_AUTO && opt.math != PA_MATH_TENSOR) return PA_ERR_INVALID_ARG;
   if (opt.num_stages > 0 && (opt.num_stages < 2 || opt.num_stages > 16)) return PA_ERR_INVALID_ARG;
@@ -1256,6 +1269,7 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   p.tmp_out = reinterpret_cast<float *>(ws + off[3]);
   p.row_limit = reinterpret_cast<int *>(ws + limits);
   p.status = reinterpret_cast<int *>(ws);
+  if (late_wait(c, opt)) p.sched = reinterpret_cast<int *>(ws) + 1;
   p.num_seqs = num_seqs;
   p.num_prefixes = num_prefixes;
   p.num_heads = num_heads;
@@ -1290,7 +1304,10 @@ pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cach
   st = host_launch(k.fn, (unsigned)grid, 1, k.threads, k.smem, stream, args,
                    "launch prefix kernel");
   if (st != PA_OK) return st;
-  return launch(c, true, opt);
+  st = launch(c, true, opt);
+  if (st != PA_OK && p.sched)  // no Phase 2 to reset it
+    cudaMemsetAsync(p.sched, 0, 2 * sizeof(int), static_cast<cudaStream_t>(stream));
+  return st;
 }
 
 size_t pa_host_staging_bytes(int num_seqs, int num_heads, int head_size,

@@ -921,12 +921,18 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1) __maxnreg__((attn_max_regs<M
     // for the whole round trip of atomics queued on one address.
     auto grab_issue = [&]() -> int { return atomic_add_lane0(p.sched, lane); };
     auto grab_value = [&](int raw) -> int {
+      if (p.late_wait) raw &= kReadyBit - 1;
       return takers + __shfl_sync(0xffffffffu, raw, 0);
     };
-    if (p.late_wait) item = grab_value(grab_issue());
     int i = 0;  // stages issued by this CTA
     bool ok = true;
-    while (true) {
+    if (p.late_wait) {
+      // (nothing of the inputs or the workspace is touched before this; the
+      // consumers come behind it through their barriers)
+      item = take_over(p.sched, kReadyBit, limit);
+      ok = item >= 0;
+    }
+    while (ok) {
       // ---- locate the item: (s, kvh, part, L)
       int s = 0, kvh = 0, part = 0, L = 0, np_s = 1;
       int nrg = 0, qs = 0, n_s = 0, rg = 0;  // chunk mode

@@ -223,6 +223,39 @@ __device__ __forceinline__ int atomic_add_acq_rel_gpu(int *addr, int v) {
   return old;
 }
 
+// Hands over, between kernels that run at once, all that the caller has seen
+// written, with `bit` of a counter that the other kernel's CTAs take numbers
+// from: what was written before the set is visible behind a take that found it
+// (its number comes from the set or from a take behind it).  The proxy fence
+// lies on that way, so that it holds for copies of the async proxy too.  (One
+// here; at every taker it cost 256 sequences behind a prefix 0.7 us.)
+__device__ __forceinline__ void hand_over(int *counter, int bit) {
+  asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(counter), "r"(bit) : "memory");
+}
+// A number, by a whole warp; -1 if the bit was not set within limit_ns.
+__device__ __forceinline__ int take_over(int *counter, int bit, uint64_t limit_ns) {
+  int n = 0;
+  if ((threadIdx.x & 31) == 0) {
+    int v;
+    asm volatile("atom.acquire.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(counter) : "memory");
+    n = v & (bit - 1);
+    uint64_t t0 = 0;
+    while (!(v & bit)) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) {
+        n = -1;
+        break;
+      }
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    }
+  }
+  n = __shfl_sync(0xffffffffu, n, 0);
+  __syncwarp();  // the other lanes' accesses come behind lane 0's
+  return n;
+}
+
 // Lane 0 adds 1 to *addr and gets the old value; the other lanes get 0.  The
 // add is predicated, so the result register is read only where the caller
 // uses it, not at a select right after the issue.

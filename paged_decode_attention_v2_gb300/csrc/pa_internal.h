@@ -14,6 +14,10 @@ constexpr uint64_t kDefaultWaitLimitNs = 1000000000ull;  // 1 s
 constexpr uint64_t kDrainLimitNs = 1000000000ull;        // drain of own copies
 constexpr int kFuseLimitMax = 16;  // most partitions a fused combine handles
 
+// Set in the count of work items by the prefix kernel once it has waited for
+// all that came before it (pa_prefix_forward has fewer items).
+constexpr int kReadyBit = 1 << 30;
+
 // Parameters of the attention kernel (Phase 1 of V2, or V1).
 struct AttnParams {
   const void *query;           // [B][H][D]
@@ -51,9 +55,11 @@ struct AttnParams {
   int cluster;        // tcgen05 chunk kernel: CTAs of a thread-block cluster (1: none)
   int debug_flags;
   // 1: the kernel before this one in the stream (the prefix kernel of the same
-  // call) writes nothing that this one reads, and started only after all that
-  // came before it was complete: wait for it at the end instead of the start,
-  // so that both run at once and Phase 2 still finds both complete.
+  // call) writes nothing that this one reads, and is itself behind all that
+  // came before: wait for it at the end instead of the start, so that both run
+  // at once and Phase 2 still finds both complete.  What came before is visible
+  // to the prefix kernel by its own wait; it passes that on by kReadyBit of
+  // sched[0], which every CTA here finds with its first item.
   int late_wait;
   float scale_log2;   // scale * log2(e)
   uint64_t wait_limit_ns;

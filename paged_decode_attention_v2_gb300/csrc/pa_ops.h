@@ -52,6 +52,7 @@ struct PrefixParams {
   float *max_logits, *exp_sums, *tmp_out;  // [B][H][max_parts](, [D])
   int *row_limit;                      // [B]: partitions x partition_size, for Phase 2
   int *status;
+  int *sched;  // the own tokens' count of items, if they run beside (else null)
   int num_seqs, num_prefixes, num_heads, num_kv_heads, group, num_blocks;
   int block_size, log2_block_size, max_prefix_blocks, max_prefix_len;
   int max_seq_len, partition_size, max_parts;

@@ -51,6 +51,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_internal.h"
 #include "pa_ops.h"
 #include "pa_tcgen05.cuh"
 
@@ -259,10 +260,6 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
   // 1024-byte aligned as the swizzle needs it: dynamic shared memory starts
   // right after the 1 KB that the system reserves (checked)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if ((smem_u32(smem_raw) & 1023u) != 0) {
-    if (threadIdx.x == 0) report(p.status, kStatusBadInput);
-    return;
-  }
   uint8_t *qbuf = smem_raw;                       // NT x [panel][128 rows][128 B]
   uint8_t *ring = qbuf + NT * Z::QTILE;           // NS x [8-key group][panel][8 keys][128 B]
   uint64_t *bars = reinterpret_cast<uint64_t *>(ring + NS * Z::SLOT);
@@ -308,9 +305,16 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
     fetch(p.query, (long long)p.num_seqs * p.num_heads * D * 2);
   }
   // wait for the kernel before in the stream, also before taking tensor
-  // memory that a CTA of it may still hold
+  // memory that a CTA of it may still hold; every CTA does before it lets the
+  // own tokens' Phase 1 start, which then waits for the hand-over alone (by the
+  // last warp, ahead of the copies, which its fence would wait for)
   pdl_wait_primary();
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == Z::THREADS - 32 && p.sched) hand_over(p.sched, kReadyBit);
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) report(p.status, kStatusBadInput);
+    return;
+  }
   if (warp == Z::SOFTMAX_WARPS + 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();

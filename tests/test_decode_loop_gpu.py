@@ -213,3 +213,45 @@ def test_a_captured_step_replayed():
         a.sl.copy_(torch.tensor(a.lens))
         graphs[i % 2].replay()
         a.check(out_p, out_s, sel, rq.double().cpu())
+
+
+def test_inputs_written_right_before_the_call():
+    """The lengths, the tables (with -1 for pages that a step does not have yet)
+    and the cache's last row are written by the launches right before
+    pa_prefix_forward, whose own tokens run beside its prefix: the bits are those
+    of a run that synchronises between all of them."""
+    steps = 60
+    rows, outs = None, []
+    for wait in (False, True):
+        a = Loop(torch.bfloat16, seed=5)
+        a.prompts()
+        if rows is None:
+            rows = [a.rows(B).cuda() for _ in range(STEPS)]
+        lens = torch.tensor(PROMPTS, dtype=torch.int32, device="cuda")
+        pos = [lens + PREFIX + i for i in range(STEPS)]
+        page = torch.arange(a.width, device="cuda")[None]
+        full = a.bt.clone()
+        tables = [torch.where(page <= ((lens + i) // BS)[:, None], full, -1).to(torch.int32) for i in range(STEPS)]
+        rq, out = (torch.empty(B, H, D, dtype=a.dtype, device="cuda") for _ in range(2))
+        got = torch.empty(steps * STEPS, B, H, D, dtype=a.dtype, device="cuda")
+        sync = torch.cuda.synchronize if wait else lambda: None
+        torch.cuda.synchronize()
+        for j in range(steps):  # the same tokens over and over
+            for i in range(STEPS):
+                q, k, v = a.split(rows[i])
+                a.bt.copy_(tables[i])
+                torch.add(lens, i + 1, out=a.sl)
+                sync()
+                pa.pa_append_kv(a.kc, a.vc, k, v, a.bt, a.sl, a.status, query=q, query_out=rq, key_bounds=a.kb,
+                                cos_sin=a.cs, positions=pos[i])
+                sync()
+                pa.pa_prefix_forward(out, rq, a.kc, a.vc, a.bt, a.sl, a.pt, a.pl, a.ps, SCALE, 128, a.ws_p,
+                                     max_seq_len=a.max_len, max_prefix_len=PREFIX)
+                sync()
+                got[j * STEPS + i].copy_(out)
+            for i in range(STEPS):  # no later round finds this one's rows
+                at = (lens + i).long()
+                a.kc[full.long()[torch.arange(B, device="cuda"), at // BS], :, at % BS] = math.nan
+        assert pa.pa_read_device_status(a.ws_p) == pa.PA_OK and pa.pa_read_device_status(a.status) == pa.PA_OK
+        outs.append(got)
+    assert outs[0].isfinite().all() and torch.equal(outs[0], outs[1])

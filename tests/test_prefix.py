@@ -64,6 +64,13 @@ def test_refused_variants(lib):
     assert lib.pa_prefix_forward(*dict(BASE, opts=o).values()) == pa.PA_ERR_UNSUPPORTED
 
 
+def test_more_own_partitions_than_the_count_holds(lib):
+    """Items are counted below bit 30, which the prefix kernel sets."""
+    for n, status in ((1 << 21, pa.PA_ERR_UNSUPPORTED), (1 << 20, pa.PA_ERR_WORKSPACE_TOO_SMALL)):
+        a = dict(BASE, num_seqs=n, num_heads=8, num_kv_heads=8, max_blocks_per_seq=1 << 10, max_seq_len=1 << 14)
+        assert lib.pa_prefix_forward(*a.values()) == status
+
+
 def test_workspace_bytes(lib):
     f = pa.pa_prefix_workspace_bytes
     n = f(3, 2, 8, 2, 128, 128, 512, 512)
