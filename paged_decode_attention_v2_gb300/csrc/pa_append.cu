@@ -20,7 +20,7 @@
 // prompt rows (32/4 heads, D 128, bf16, with bounds), 189 MB, take 34.9 us,
 // 5.4 TB/s, 0.80 of the copy peak.  A decode step's bytes are a few MB or
 // less; there the launch and one dependent chain of loads (lengths, table,
-// key) are all there is: 3.2 us for one row, 3.9 us for 256, one launch after
+// angles) are all there is: 3.2 us for one row, 3.9 us for 256, one launch after
 // another.  So what can be is read before a row is located: its queries, and
 // its keys and values as far as L2.  A row is found in q_start by a warp, 32
 // entries at a time.
@@ -149,11 +149,12 @@ __device__ __forceinline__ uint32_t word_low() {
   return sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
 }
 
-// A row's sequence, token and chunk end; false: nothing to do for it (a
+// A row's sequence, token, chunk end and page; false: nothing to do for it (a
 // padding row, an empty slot) or bad input (reported).
 struct RowInfo {
-  int seq, tok, tok_end;  // tok_end: the chunk's end, L
-  bool starts;            // its chunk's first row
+  int tok, tok_end;  // tok_end: the chunk's end, L
+  int blk;           // the token's page (not yet checked)
+  bool starts;       // its chunk's first row
 };
 // (by a warp, for one row)
 __device__ __forceinline__ bool locate_row(const AppendParams &p, int row, RowInfo &o) {
@@ -182,10 +183,10 @@ __device__ __forceinline__ bool locate_row(const AppendParams &p, int row, RowIn
     if (lane == 0) report(p.status, kStatusBadInput);
     return false;
   }
-  o.seq = s;
   o.tok = L - n + i;
   o.tok_end = L;
   o.starts = i == 0;
+  o.blk = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + (o.tok >> p.log2_block_size));
   return true;
 }
 
@@ -255,8 +256,13 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
     bool first = false;
     if (locate_row(p, row0 + warp, o)) {
       pos = row_position(p, row0 + warp, o.tok);
-      first = o.starts || o.tok % p.block_size == 0;  // the first token of its page here
-      if (lane == 0) s_row[warp] = o;
+      if ((unsigned)o.blk < (unsigned)p.num_blocks) {
+        first = o.starts || o.tok % p.block_size == 0;  // the first token of its page here
+        if (lane == 0) s_row[warp] = o;
+      } else {  // nothing of the row is written, its queries neither
+        pos = -1;
+        if (lane == 0) report(p.status, kStatusBadInput);
+      }
     }
     if (lane == 0) {
       s_pos[warp] = pos;
@@ -294,12 +300,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
     const int lr = task / p.num_kv_heads, h = task - lr * p.num_kv_heads;
     if (!s_first[lr]) continue;
     const RowInfo o = s_row[lr];
-    const int page = o.tok >> p.log2_block_size;
-    const int blk = __ldg(p.block_tables + (size_t)o.seq * p.max_blocks_per_seq + page);
-    if ((unsigned)blk >= (unsigned)p.num_blocks) {
-      if (lane == 0) report(p.status, kStatusBadInput);
-      continue;
-    }
+    const int blk = o.blk;
     const int off0 = o.tok & (p.block_size - 1);
     const int n = min(o.tok_end - o.tok, p.block_size - off0);
     const size_t slot0 = ((size_t)blk * p.num_kv_heads + h) * p.block_size + off0;

@@ -414,3 +414,36 @@ def test_cache_beyond_32_bits():
     for j, page in enumerate(far.tolist()):
         held = kc[page, :, :min(16, 49 - 16 * j)]
         assert torch.equal(kb[page, :, 0], held.amax(1)) and torch.equal(kb[page, :, 1], held.amin(1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inplace", [False, True], ids=["apart", "inplace"])
+@pytest.mark.parametrize("decode", [False, True], ids=["chunks", "decode"])
+def test_rows_of_a_bad_page_keep_their_queries(inplace, decode):
+    """Nothing of a row whose table entry is bad is written: its query too stays
+    as it was, where the rotation would replace it; the other rows are as usual."""
+    new, ctx = ([1] * 6, [3, 20, 40, 15, 16, 0]) if decode else ([4, 20], [3, 20])
+    c = Case(15, torch.bfloat16, 6, 2, 64, 16, new, ctx, 64, decode=decode)
+    dev = "cuda"
+    bt = c.bt.clone()
+    bt[0, 0] = c.kc.shape[0]  # of all rows of the first sequence
+    bt[1, (32 if not decode else 20) // 16] = -5  # of the second's rows from token 32 on (its only one)
+    kc, vc, kb = c.kc.to(dev), c.vc.to(dev), c.kb.to(dev)
+    q, k, v = c.split(c.qkv.to(dev))
+    q = q.contiguous()
+    qo = q if inplace else torch.full_like(q, 7.0)
+    was = qo.clone()
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    qs = None if decode else torch.tensor(c.qs, dtype=torch.int32, device=dev)
+    pa.pa_append_kv(kc, vc, k, v, bt.to(dev), torch.tensor(c.lens, dtype=torch.int32, device=dev), ws,
+                    query=q, query_out=qo, key_bounds=kb, cos_sin=c.cs.to(dev), q_start=qs)
+    assert pa.pa_read_device_status(ws) == pa.PA_ERR_DEVICE_BAD_INPUT
+    lost = [r for r, (s, t, _) in enumerate(c.place) if s == 0 or (s == 1 and (decode or t >= 32))]
+    kept = [r for r in range(len(c.place)) if r not in lost]
+    assert torch.equal(qo[lost], was[lost])
+    ref, size = c.rotate(c.split(c.qkv)[0])
+    c.check(qo[kept], ref[kept], size[kept], "the other rows")
+    for s, t, _ in (c.place[r] for r in lost):  # their pages neither
+        page = int(c.bt[s, t // 16])
+        assert torch.equal(kc[page].cpu(), c.kc[page]) and torch.equal(vc[page].cpu(), c.vc[page])
+        assert torch.equal(kb[page].cpu(), c.kb[page])
