@@ -324,11 +324,13 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
       hi[e + 2] = word_max<T>(hi[e + 2], x.z), lo[e + 2] = word_min<T>(lo[e + 2], y.z);
       hi[e + 3] = word_max<T>(hi[e + 3], x.w), lo[e + 3] = word_min<T>(lo[e + 3], y.w);
     };
+    bool wrote = false;
 #pragma unroll 1
     for (int i = tl; i < n; i += LANES) {
       const int row = row0 + lr + i;
       const int pos = row_position(p, row, o.tok + i);
       if (pos < 0) continue;
+      wrote = true;
       const uint4 *ks = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.key) +
                                                         row * p.key_stride + (size_t)h * D);
       const uint4 *vs = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.value) +
@@ -349,7 +351,8 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
         join(k.b, k.b, 4);
       }
     }
-    if (!bnd) continue;
+    // (positions that are all bad leave the page as it was)
+    if (!bnd || !__any_sync(0xffffffffu, wrote)) continue;
 #pragma unroll
     for (int d = UNITS; d < 32; d <<= 1)
 #pragma unroll

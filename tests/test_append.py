@@ -447,3 +447,32 @@ def test_rows_of_a_bad_page_keep_their_queries(inplace, decode):
         page = int(c.bt[s, t // 16])
         assert torch.equal(kc[page].cpu(), c.kc[page]) and torch.equal(vc[page].cpu(), c.vc[page])
         assert torch.equal(kb[page].cpu(), c.kb[page])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bs", [8, 16])
+def test_bad_positions_leave_the_bounds_of_their_pages(bs):
+    """A page whose appended rows all have bad positions keeps its bounds, a new
+    page too; with one good row among them the bounds are that row's."""
+    c = Case(17, torch.bfloat16, 2, 2, 64, bs, [9, 6, bs], [0, 20, 2 * bs], 64, offsets=[0, 0, 0])
+    dev = "cuda"
+    bad = [r for r, (s, t, _) in enumerate(c.place)
+           if (s == 0 and t // bs == 0) or s == 1 or (s == 2 and t != 2 * bs + 3)]
+    pos = c.positions.clone()
+    pos[bad] = c.cs.shape[0]
+    kc, vc, kb = c.kc.to(dev), c.vc.to(dev), c.kb.to(dev)
+    _, k, v = c.split(c.qkv.to(dev))
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    pa.pa_append_kv(kc, vc, k, v, c.bt.to(dev), torch.tensor(c.lens, dtype=torch.int32, device=dev), ws,
+                    key_bounds=kb, cos_sin=c.cs.to(dev), positions=pos.to(dev),
+                    q_start=torch.tensor(c.qs, dtype=torch.int32, device=dev))
+    assert pa.pa_read_device_status(ws) == pa.PA_ERR_DEVICE_BAD_INPUT
+    kc, kb = kc.cpu(), kb.cpu()
+    for s, j in [(0, 0)] + [(1, t // bs) for t in range(20, 26)]:
+        page = int(c.bt[s, j])
+        assert torch.equal(kb[page], c.kb[page]) and torch.equal(kc[page], c.kc[page])
+    page = int(c.bt[2, 2])
+    assert torch.equal(kb[page, :, 0], kc[page, :, 3]) and torch.equal(kb[page, :, 1], kc[page, :, 3])
+    if bs == 8:  # the ninth token's page
+        page = int(c.bt[0, 1])
+        assert torch.equal(kb[page, :, 0], kc[page, :, 0]) and torch.equal(kb[page, :, 1], kc[page, :, 0])
