@@ -562,3 +562,73 @@ def test_fewer_splits_in_the_workspace_of_a_larger_batch():
         assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
         assert_close(d["out"], ref, c.dtype, "the larger batch's workspace")
     assert (buf[n:] == 0xA5).all()
+
+
+def marked(D, counts, prefix, H=8, K=1, bs=16, seed=40, extra=0):
+    """Prefixes whose first and last tokens, those at the kernel's stage (so also
+    split) edges and `extra` others, page edges among them, carry nearly all the
+    weight: their keys lie along one direction that the queries share.  Values of
+    random sign, so that each of the M of them moves the result by about
+    0.012 a channel, more than twice the bar where the result is small, and the
+    rounding of the weights by less than the bar."""
+    rng = random.Random(seed)
+    c = Case(seed, torch.bfloat16, H, K, D, bs, counts, prefix, [rng.randint(1, 9) for _ in range(sum(counts))],
+             k_mult=0.1)
+    g = torch.Generator().manual_seed(seed)
+    u = torch.randn(D, generator=g)
+    u /= u.norm()
+    stage = 64 if D == 256 else 128
+    # logits of the marked tokens: about 9.5 above the others', alike for every row
+    along = 3.1 * D ** 0.25
+    c.q.copy_(0.25 * c.q.float() + along * u)
+    c.marks = []
+    for t, n in enumerate(prefix):
+        at = {0, n - 1} | {i for i in range(n) if i % stage in (0, stage - 1)} if n else set()
+        at |= {min(n - 1, rng.randint(0, n // bs) * bs + rng.choice([0, bs - 1])) for _ in range(extra)} if n else set()
+        at = sorted(at)
+        c.marks.append(at)
+        for i in at:
+            page, o = c.pt[t, i // bs], i % bs
+            c.kc[page, :, o] = (c.kc[page, :, o].float() + along * u).to(c.dtype)
+            c.vc[page, :, o] = (0.012 * len(at) * torch.sign(torch.randn(K, D, generator=g))).to(c.dtype)
+    return c
+
+
+MARKED = [(128, [5], [100001], {}), (64, [3, 2], [50001, 777], {}), (256, [2, 1], [20001, 300], dict(K=2)),
+          (128, [70, 50], [6001, 9000], dict(H=16, K=2, extra=100)), (64, [150], [5000], dict(H=16, K=2, bs=8)),
+          (256, [90], [4001], dict(H=16, K=2, bs=64, extra=50))]
+
+
+@pytest.mark.parametrize("D,counts,prefix,kw", MARKED, ids=ids)
+def test_a_lost_key_would_be_seen(D, counts, prefix, kw):
+    """On the oracle: without any one marked token, without the prefix's last
+    page, or with a stage counted twice, results leave the bar by half of it at
+    least.  (The two calls below compare within the bar.)"""
+    c = marked(D, counts, prefix, **kw)
+    G, stage = c.H // c.K, 64 if D == 256 else 128
+    ref = torch.from_numpy(c.reference()).view(c.B, c.K, G, D)
+    for t, at in enumerate(c.marks):
+        s = c.start[t]  # one sequence of the group, as every other has the same keys
+        kp, vp = c.rows(c.kc, c.pt[t], prefix[t]), c.rows(c.vc, c.pt[t], prefix[t])
+        k = torch.cat([kp, c.rows(c.kc, c.bt[s], c.own[s])], 1)
+        p = torch.softmax(c.q[s].double().view(c.K, G, D) @ k.transpose(1, 2) * c.scale, -1)[..., :prefix[t]]
+        out = ref[s]
+        bar = 1.5 * (4e-3 + 1e-2 * out.abs())
+        n = prefix[t]
+        lost = [[i] for i in at] + [list(range((n - 1) // c.bs * c.bs, n))]
+        for tok in lost:
+            w = p[..., tok]
+            rest = (out - w @ vp[:, tok]) / (1 - w.sum(-1, keepdim=True))
+            assert ((rest - out).abs() > bar).any(), (t, tok)
+        for a in range(0, n, stage):
+            w = p[..., a:a + stage]
+            twice = (out + w @ vp[:, a:a + stage]) / (1 + w.sum(-1, keepdim=True))
+            assert ((twice - out).abs() > bar).any(), (t, a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,counts,prefix,kw", MARKED, ids=ids)
+def test_no_key_is_lost(D, counts, prefix, kw):
+    """Every stage's and split's first and last token, the prefix's last one too,
+    is in the result."""
+    marked(D, counts, prefix, **kw).check(calls=1)
