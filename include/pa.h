@@ -504,6 +504,8 @@ size_t pa_sparse_workspace_bytes(int num_rows, int num_heads, int num_kv_heads,
  * enough serves calls of any shape, one after another).  The prefix is split as
  * these sizes and the workspace's suggest, and the splits' sums are rounded
  * apart: the same call on workspaces of other sizes may differ in last bits.
+ * A max_prefix_len far above the longest prefix makes fewer and longer items
+ * of it than the GPU has room for: give the batch's own where it is known.
  * Bad tables, lengths or groups are reported as PA_ERR_DEVICE_BAD_INPUT; the
  * rows in question (with starts out of order, any row) then hold no meaningful
  * values.  opts as in pa_forward (variant V2 or auto; no fused combine, no

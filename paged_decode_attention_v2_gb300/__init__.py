@@ -426,7 +426,8 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
     _check((_lib or load_library()).pa_append_kv(
         kc, vc, kb, qo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv, D, nb, bs,
         blocks, int(max_seq_len), int(rotary_dim or 0), int(interleaved), max_position,
-        _DTYPES[key_cache.dtype], ws, workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_append_kv")
+        _DTYPES[key_cache.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "pa_append_kv")
 
 
 def pa_prefix_workspace_bytes(num_seqs: int, num_prefixes: int, num_heads: int, num_kv_heads: int,
@@ -481,8 +482,8 @@ def pa_prefix_forward(out, query, key_cache, value_cache, block_tables, seq_lens
     _check((_lib or load_library()).pa_prefix_forward(
         o, q, kc, vc, bt, sl, pt, pl, ps, B, G, H, hkv, D, nb, bs, blocks, pblocks,
         int(max_seq_len), int(max_prefix_len), float(scale), int(partition_size),
-        _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(), _stream_handle(stream), ctypes.byref(opts)),
-        "pa_prefix_forward")
+        _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream), ctypes.byref(opts)), "pa_prefix_forward")
 
 
 def pa_sparse_workspace_bytes(num_rows: int, num_heads: int, num_kv_heads: int, head_size: int,
@@ -534,7 +535,8 @@ def pa_select_blocks(selected, query, key_bounds, block_tables, seq_lens, block_
     _check((_lib or load_library()).pa_select_blocks(
         sel, q, kb, bt, sl, qs, B, R, H, hkv, D, nb, block_size, block_tables.shape[1],
         int(max_seq_len), selected.shape[2], sink_blocks, recent_blocks, int(partition_size),
-        _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_select_blocks")
+        _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "pa_select_blocks")
 
 
 def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables, seq_lens, scale,

@@ -39,6 +39,9 @@ __host__ __device__ __forceinline__ int view_block(int blk, int kv_head, int num
 // cache that fits the GPU holds more).
 constexpr int kMaxTokens = 1 << 30;
 
+// Every split is one more partial of every row, and the plan tries each number
+// of them on the host.  (With one KV head and one tile of rows, 64 CTAs are
+// fewer than the SMs; more splits there are left to be measured.)
 constexpr int kMaxPrefixSplits = 64;
 constexpr int kPrefixSms = 152;  // what the splits are planned for
 constexpr int kPrefixDebugStall = 1;  // PA_DEBUG_STALL_CONSUMERS

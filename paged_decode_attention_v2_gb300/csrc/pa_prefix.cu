@@ -34,14 +34,14 @@
 // stage exceeds it by more than 2^8, which the final sum undoes exactly.
 //
 // Measured on GB300 (a whole call, one after another; 32/4 heads, bf16, D 128):
-//   256 sequences behind 8192 tokens, 16 to 512 of their own: 61.6 us (96
+//   256 sequences behind 8192 tokens, 16 to 512 of their own: 62.1 us (96
 //     items of 22 stages; the own tokens' Phase 1 runs beside them).  First
-//     scores at 5 us, the items' ends at 42 to 45, the own tokens' last item at
-//     55, Phase 2 from 56 to 60.  In the steady state a stage of both tiles
-//     takes 2950 clocks against 2048 of its MMAs: a tile's chain S, softmax, PV
+//     scores at 6 us, the items' ends at 40 to 48, the own tokens' last item at
+//     55, Phase 2 from 56 to 61.  In the steady state a stage of both tiles
+//     takes 2960 clocks against 2048 of its MMAs: a tile's chain S, softmax, PV
 //     is what bounds it, with the tensor pipe 0.69 busy.
-//   8 sequences behind 100,000 tokens (205 MB): 48.2 us, 4.2 TB/s; a stage takes
-//     2850 clocks against 2790 that its bytes take at the copy rate, and the
+//   8 sequences behind 100,000 tokens (205 MB): 49.1 us, 4.2 TB/s; a stage takes
+//     2830 clocks against 2790 that its bytes take at the copy rate, and the
 //     rest is start, epilogue and Phase 2.
 // Two softmax threads a row were slower (3200 clocks a stage and more: the
 // exchange of their maxima joins the chain), an epilogue in full lines through
@@ -792,10 +792,10 @@ PrefixKernelInfo prefix_kernel(int dtype_bf16, int head_size) {
   return dtype_bf16 ? pick<__nv_bfloat16>(head_size) : pick<__half>(head_size);
 }
 
-// Splits of the prefix, at most most_splits, from a model of the call's time in microseconds
-// (coefficients measured on GB300; the sizes of the groups are not known on
-// the host, so a row tile is counted as half empty a group, and own lengths as
-// half their bound):
+// Splits of the prefix, at most most_splits, from a model of the call's time in
+// microseconds (coefficients measured on GB300; the sizes of the groups are not
+// known on the host, so a row tile is counted as half empty a group, and own
+// lengths as half their bound; times of one build):
 //   - the prefix kernel: waves of items on 152 SMs, each an item's stages at
 //     the tensor cores' pace or that of the keys' bytes, plus 10 us an item
 //     (start, queries, epilogue);
