@@ -632,3 +632,45 @@ def test_no_key_is_lost(D, counts, prefix, kw):
     """Every stage's and split's first and last token, the prefix's last one too,
     is in the result."""
     marked(D, counts, prefix, **kw).check(calls=1)
+
+
+@pytest.mark.gpu
+def test_the_count_of_items_is_left_as_other_calls_need_it():
+    """One workspace in turn: the prefix call, with the own tokens beside the
+    prefix or (opt-in) behind it on the other kernel, with no prefix at all,
+    pa_v2_forward, and with wrong lengths: each starts from a count of zero."""
+    c = Case(34, torch.bfloat16, 8, 2, 128, 16, [7, 3], [900, 300], [60 * i for i in range(10)])
+    d, ref = c.device(), c.reference()
+    out = torch.empty_like(d["out"])
+    plain = Case(34, torch.bfloat16, 8, 2, 128, 16, [7, 3], [900, 300], [60 * i for i in range(10)])
+    plain.prefix = [0, 0]
+    own = plain.reference()
+
+    def prefix(**kw):
+        d["out"].fill_(math.nan)
+        c.run(d, **kw)
+        assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+        assert_close(d["out"], ref, c.dtype, str(kw))
+
+    def decode():
+        pa.pa_v2_forward(out, d["q"], d["kc"], d["vc"], d["bt"], d["sl"], c.scale, 512, d["ws"],
+                         max_seq_len=max(c.own))
+        assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+        assert_close(out, own, c.dtype, "own tokens alone")
+
+    for _ in range(2):
+        prefix()
+        decode()
+        prefix(debug_flags=pa.PA_DEBUG_TCGEN05_KEYS)
+        prefix()
+        pa.pa_prefix_forward(out, d["q"], d["kc"], d["vc"], d["bt"], d["sl"], d["pt"], torch.zeros_like(d["pl"]),
+                             d["ps"], c.scale, c.P, d["ws"], max_seq_len=max(c.own), max_prefix_len=0)
+        assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+        assert_close(out, own, c.dtype, "no prefix")
+        bad = d["sl"] + 10 ** 6
+        pa.pa_prefix_forward(out, d["q"], d["kc"], d["vc"], d["bt"], bad, d["pt"], d["pl"], d["ps"], c.scale, c.P,
+                             d["ws"], max_seq_len=max(c.own), max_prefix_len=900)
+        assert pa.pa_read_device_status(d["ws"]) == pa.PA_ERR_DEVICE_BAD_INPUT
+        prefix()
+        decode()
+    assert (d["ws"][4:12] == 0).all()
