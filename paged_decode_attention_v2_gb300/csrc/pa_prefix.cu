@@ -19,9 +19,7 @@
 // is off by 2^-8 of itself at most in bf16; in f16 by 2^-11, or 2^-32 of the
 // split's largest weight where that is more), and is the PV product's A operand
 // straight from tensor memory.  The sum adds the rounded weights, so that those
-// that V is multiplied with sum to one: with the lazy maximum below a weight
-// that outweighs all others is any number up to 2^8, and its rounding would be
-// the result's.
+// that V is multiplied with sum to one.
 //   D 64, 128: two row tiles (NT 2) share every stage of 128 keys; while the
 //     softmax of one runs, the tensor cores work on the other:
 //     PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) ...
@@ -31,18 +29,25 @@
 // MMAs of one thread execute in order, so a PV has read its P before the next
 // S of that buffer overwrites it, and a commit behind an S also covers the PV
 // before it.  The running maximum is raised lazily: O is rescaled only when a
-// stage exceeds it by more than 2^8, which the final sum undoes exactly.
+// stage's exceeds it by more than 2^8, or when the key would outweigh half of all
+// before it: the weight of the running maximum itself is 1 and exact, any other's
+// is rounded, which shows where few keys carry the result.  (Raised beyond 2^8
+// only, one of 7e5 results left the parity bar with logits of standard deviation
+// 6, the worst by 1.4; with half, the worst is at 0.74 of it, and at 0.63 if every
+// new maximum is taken.  256 behind 8192 tokens 62.0 -> 61.2 us, 8 behind 100,000
+// 49.0 -> 50.5 us.)
 //
 // Measured on GB300 (a whole call, one after another; 32/4 heads, bf16, D 128):
-//   256 sequences behind 8192 tokens, 16 to 512 of their own: 62.1 us (96
+//   256 sequences behind 8192 tokens, 16 to 512 of their own: 61.0 us (96
 //     items of 22 stages; the own tokens' Phase 1 runs beside them).  First
-//     scores at 6 us, the items' ends at 40 to 48, the own tokens' last item at
-//     55, Phase 2 from 56 to 61.  In the steady state a stage of both tiles
-//     takes 2960 clocks against 2048 of its MMAs: a tile's chain S, softmax, PV
-//     is what bounds it, with the tensor pipe 0.69 busy.
-//   8 sequences behind 100,000 tokens (205 MB): 49.1 us, 4.2 TB/s; a stage takes
-//     2830 clocks against 2790 that its bytes take at the copy rate, and the
-//     rest is start, epilogue and Phase 2.
+//     scores at 6 us, the items' ends at 41 to 48, the own tokens' last item at
+//     55, Phase 2 from 57 to 61.  In the steady state a stage of both tiles
+//     takes 3000 clocks (3400 where O is rescaled, the first stages as a rule)
+//     against 2048 of its MMAs: a tile's chain S, softmax, PV is what bounds it,
+//     with the tensor pipe 0.68 busy.
+//   8 sequences behind 100,000 tokens (205 MB): 50.5 us, 4.1 TB/s; a stage takes
+//     2740 clocks (3100 where O is rescaled), what its bytes take at the copy
+//     rate, and the rest is start, epilogue and Phase 2.
 // Two softmax threads a row were slower (3200 clocks a stage and more: the
 // exchange of their maxima joins the chain), an epilogue in full lines through
 // shared memory the same.
@@ -59,7 +64,10 @@ namespace pa {
 namespace {
 
 constexpr int kTileRows = 128;      // the MMA's M
-constexpr float kLazyMargin = 8.f;  // log2 units
+// The running maximum is raised when a stage's is above it by more than this, in
+// log2 units, or by so much that the key would weigh more than 2^-kLazyShare of
+// all keys before it together.
+constexpr float kLazyMargin = 8.f, kLazyShare = 1.f;
 // Weights are 2^(s - m + this): a weight below f16's normal range loses bits
 // and below 2^-25 becomes zero, so f16's start 2^7 higher (with the margin
 // 2^15, below its largest number).  The sum takes the factor out again.
@@ -598,6 +606,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
         if (lane == 0) mbar_arrive(q_full + 8 * t);
       }
       float m_run = -CUDART_INF_F, l = 0.f;
+      float raise_at = -CUDART_INF_F;  // a stage's maximum above it becomes the running one
       for (int j = 0; ok && j < stages; ++j) {
         const int buf = NT == 2 ? t : done & 1;
         const uint32_t par = NT == 2 ? (uint32_t)done & 1u : ((uint32_t)done >> 1) & 1u;
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
           }
           const float mt = sc * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
                                       fmaxf(m8[6], m8[7]));
-          const bool raise = mt > m_run + kLazyMargin;
+          const bool raise = mt > raise_at;
           const float alpha = raise ? exp2f(m_run - mt) : 1.f;
           if (raise) m_run = mt;
           if (j > 0 && __any_sync(0xffffffffu, raise)) {
@@ -712,6 +721,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 8 * buf);
+        raise_at = m_run + fmaxf(fminf(lg2(l) - kWeightShift<T> - kLazyShare, kLazyMargin), 0.f);
         ++done;
       }
       ops += 2 * stages;

@@ -480,9 +480,9 @@ def test_two_streams_at_once():
 
 def ramp(dtype, D, stages, v):
     """Keys whose logits step up by 4.1 to 5.4 from stage to stage of the kernel,
-    less than its lazy maximum's margin of 8 ln 2: the largest weight, of the
-    last stage, is any number up to 2^8, another one for every row.  Every value
-    is v."""
+    another number for every row, and less than the 8 ln 2 beyond which its
+    running maximum is raised in any case: weights that are no powers of two,
+    and the last stage's outweighs all others.  Every value is v."""
     step = 64 if D == 256 else 128
     c = Case(30, dtype, 4, 1, D, 16, [8], [stages * step], list(range(8)), scale=1.0)
     c.q.zero_()
@@ -674,3 +674,47 @@ def test_the_count_of_items_is_left_as_other_calls_need_it():
         prefix()
         decode()
     assert (d["ws"][4:12] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("heavy_first", [True, False], ids=["heavy_first", "light_first"])
+def test_a_key_that_outweighs_the_others_is_exact(dtype, D, heavy_first):
+    """Three stages of the last split hold a key each: one of logit 0, one 4.9 to
+    5.5 above (2^7 to 2^7.9, another number for every row: a running maximum
+    raised by nothing less than 2^8 would leave it rounded), one of 5/8 the
+    weight of that.  Against the heaviest key the weights are 1 and 5/8, exact in
+    every type, so the result is rounded once, u |ref|.  Besides, a logit is off
+    by at most 2^-17 (its last bits in the key, sums of three products below 8 in
+    fp32), which moves results by 2^-17 x 8 at most; fp32's part in the sums is
+    smaller.  2^-12 covers both."""
+    stages, step = 384, 64 if D == 256 else 128
+    c = Case(35, dtype, 4, 1, D, 16, [8], [stages * step], [0] * 8, scale=1.0)
+    c.q.zero_()
+    c.q[..., 0] = torch.linspace(4.9, 5.49, 32).view(8, 4)
+    c.q[..., 1:4] = 1.0
+    c.kc.zero_()
+    c.kc[..., 1] = -60.0
+    c.vc.zero_()
+
+    def key(stage, base, logit, v):
+        t = stage * step
+        page, o = c.pt[0, t // 16], t % 16
+        hi = torch.tensor(logit, dtype=dtype)
+        c.kc[page, :, o, 0] = base
+        c.kc[page, :, o, 1] = hi
+        c.kc[page, :, o, 2] = logit - hi.double().item()
+        c.vc[page, :, o] = v
+
+    light = math.log(5 / 8)
+    key(stages - 6, 0.0, 0.0, 1.0)
+    key(stages - 4, 1.0, 0.0 if heavy_first else light, 4.0 if heavy_first else -4.0)
+    key(stages - 2, 1.0, light if heavy_first else 0.0, -4.0 if heavy_first else 4.0)
+    ref = c.reference()
+    d = c.device()
+    c.run(d)
+    assert pa.pa_read_device_status(d["ws"]) == pa.PA_OK
+    err = abs(d["out"].double().cpu().numpy() - ref)
+    bound = torch.finfo(dtype).eps / 2 * abs(ref) + 2.0 ** -12
+    assert (err <= bound).all(), f"{(err - bound).max():.3e} over"
