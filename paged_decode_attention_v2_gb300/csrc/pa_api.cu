@@ -897,6 +897,7 @@ size_t prefix_bytes(int num_seqs, int num_heads, int head_size, int max_seq_len,
                     int partition_size, long long slots) {
   const long long own = max_parts_of(max_seq_len, partition_size);
   const long long rows = (long long)num_seqs * num_heads;
+  if (rows > 1ll << 36) return 0;  // queries of terabytes: below it nothing here wraps
   const long long parts = own + (rows > 0 ? (slots + rows - 1) / rows : 0);
   if (parts > kMaxReduceParts || parts * partition_size > INT_MAX - partition_size) return 0;
   const size_t n = (size_t)(rows * own + slots);
@@ -915,6 +916,7 @@ size_t prefix_least_bytes(int num_seqs, int num_heads, int head_size, int max_se
                           int max_prefix_len, int partition_size) {
   const PrefixKernelInfo k = prefix_kernel(1, head_size);
   const long long rows = (long long)num_seqs * num_heads;
+  if (rows > 1ll << 36) return 0;
   long long splits = (max_prefix_len + k.stage_keys - 1) / k.stage_keys;
   if (splits > kMaxPrefixSplits) splits = kMaxPrefixSplits;
   long long most = (long long)kPrefixSms * k.tile_rows;
@@ -1170,9 +1172,10 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads, 
               max_prefix_len, partition_size, kMaxPrefixSplits, &split, &splits);
   const size_t least = prefix_least_bytes(num_seqs, num_heads, head_size, max_seq_len,
                                           max_prefix_len, partition_size);
+  if (least == 0) return 0;
   const size_t best = prefix_bytes(num_seqs, num_heads, head_size, max_seq_len, partition_size,
                                    (long long)num_seqs * num_heads * splits);
-  return least == 0 || best < least ? least : best;
+  return best > least ? best : least;
 }
 
 pa_status_t pa_prefix_forward(void *out, const void *query, const void *key_cache,

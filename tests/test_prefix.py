@@ -124,6 +124,12 @@ def test_lengths_beyond_31_bit_arithmetic_are_refused(lib, n):
                  workspace_bytes=1 << 40, **over)
         assert lib.pa_prefix_forward(*a.values()) == pa.PA_ERR_UNSUPPORTED
     assert 0 < f(3, 1, 8, 2, 128, 128, 2 ** 30, 512) < 1 << 24
+    # as are rows whose bytes would wrap
+    assert f(n, 1, n, 1, 128, 128, 512, 512) == f(n, 1, n, 1, 256, 0, 512, 64) == 0
+    assert f(1 << 28, 1, 256, 256, 256, 0, 8192, 64) >> 40 > 0
+    a = dict(BASE, num_seqs=1 << 27, num_heads=1 << 20, num_kv_heads=1 << 20, num_blocks=1, max_seq_len=0,
+             workspace_bytes=1 << 62)
+    assert lib.pa_prefix_forward(*a.values()) == pa.PA_ERR_UNSUPPORTED
 
 
 # ---------------------------------------------------------------------------
