@@ -536,6 +536,78 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads,
                                  int max_seq_len, int max_prefix_len,
                                  int partition_size);
 
+/* Append new keys and values to a paged cache that holds them in 4 bits.
+ *
+ * Of every 64 elements of a head (a group) the cache holds the lowest value and
+ * a step, both f16, and for each element a code of 4 bits:
+ *   lo   = f16(min x)                 (no further from 0 than f16's largest, 65504)
+ *   step = f16((max x - lo) * (1/15)) (the same)
+ *   code = (x - lo) * (1 / step) rounded to even, 0 .. 15 (0 where step is 0)
+ * in fp32, each operation rounded by itself; a code stands for lo + code * step.
+ * NaN is coded as the group's lowest value.
+ *
+ *   key_cache, value_cache    uint8 [num_blocks][num_kv_heads][block_size]
+ *                             [head_size / 2]: element 2i of a head in the low
+ *                             half of byte i, 2i + 1 in the high half
+ *   key_scales, value_scales  f16 [num_blocks][num_kv_heads][block_size]
+ *                             [head_size / 64][2]: lo, step
+ * A token takes 9/16 (72 of 128 bytes at head_size 128) of a byte an element,
+ * scales included.  Keys are rotated and rounded to dtype as by pa_append_kv
+ * (with the three operations of each element rounded apart), then coded; query
+ * is rotated into query_out.  key_out, value_out [num_rows][num_kv_heads]
+ * [head_size] (dtype), or NULL, receive what the appended codes stand for, for
+ * attention among a prompt's own tokens that agrees with later decode steps.
+ *
+ * Rows, q_start, seq_lens, positions, strides, rotation, the workspace and bad
+ * data as in pa_append_kv; padding rows leave query_out, key_out and value_out
+ * as they were.  bf16 and f16 (PA_ERR_UNSUPPORTED for f32); caches and scales
+ * 16-byte aligned.  Two rows never share a byte, so any rows may be appended at
+ * once. */
+pa_status_t pa_q4_append(void *key_cache, void *value_cache, void *key_scales,
+                         void *value_scales, void *query_out, void *key_out,
+                         void *value_out, const void *query, const void *key,
+                         const void *value, long long query_stride,
+                         long long key_stride, long long value_stride,
+                         const float *cos_sin, const int32_t *positions,
+                         const int32_t *block_tables, const int32_t *seq_lens,
+                         const int32_t *q_start, int num_seqs, int num_rows,
+                         int num_heads, int num_kv_heads, int head_size,
+                         int num_blocks, int block_size, int max_blocks_per_seq,
+                         int max_seq_len, int rotary_dim, int interleaved,
+                         int max_position, int dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Decode attention over a cache in 4 bits: out[r][h] = softmax over the keys
+ * that row r sees of (scale q . K) @ V, with the values that the codes stand
+ * for, accumulated in fp32.  Rows: one a sequence (q_start NULL, num_rows =
+ * num_seqs, the row sees the sequence's seq_lens keys; an empty sequence gets
+ * zeros), or chunks of a sequence's last tokens as in pa_chunks_forward, of any
+ * lengths (rows behind the last chunk are left as they were).
+ *
+ * The work is cut into equal shares of keys whatever the lengths are, so there
+ * is no partition size to choose, and a workspace of pa_q4_workspace_bytes(
+ * head_size) bytes, initialised once by pa_workspace_init, serves calls of any
+ * batch, one after another.  Which keys share a partial sum follows from all the
+ * lengths and the GPU's SM count, so last bits of a sequence's output may differ
+ * between batches.  query and out contiguous [num_rows][num_heads][head_size];
+ * bf16 and f16 (PA_ERR_UNSUPPORTED for f32); max_seq_len at most 2^30; the
+ * other arguments and limits as pa_forward.  Scales must be finite.  A bad table
+ * entry, length or chunk is reported as PA_ERR_DEVICE_BAD_INPUT; the rows in
+ * question then hold no meaningful values (zeros for a bad length without
+ * q_start), or are left as they were (a bad chunk). */
+pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache,
+                          const void *value_cache, const void *key_scales,
+                          const void *value_scales, const int32_t *block_tables,
+                          const int32_t *seq_lens, const int32_t *q_start,
+                          int num_seqs, int num_rows, int num_heads,
+                          int num_kv_heads, int head_size, int num_blocks,
+                          int block_size, int max_blocks_per_seq, int max_seq_len,
+                          float scale, int dtype, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for pa_q4_forward, any batch (0 on a bad head size). */
+size_t pa_q4_workspace_bytes(int head_size);
+
 /* Host heuristic: 1 if V2 should serve this batch on a GPU with sm_count
  * SMs, 0 for V1.  The pages switch on sequence length alone: the commit note
  * for computility-run.yaml (project_6, commit a2a5dd8) lists the decode path

@@ -47,7 +47,8 @@ EXPORTS = ("pa_workspace_bytes", "pa_workspace_layout", "pa_workspace_init",
            "pa_version", "pa_v2_forward_noalloc", "pa_host_staging_bytes", "pa_forward_host",
            "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine", "pa_append_kv",
            "pa_select_blocks", "pa_sparse_forward", "pa_sparse_workspace_bytes",
-           "pa_prefix_forward", "pa_prefix_workspace_bytes")
+           "pa_prefix_forward", "pa_prefix_workspace_bytes", "pa_q4_append", "pa_q4_forward",
+           "pa_q4_workspace_bytes")
 
 
 class PAError(RuntimeError):
@@ -127,6 +128,12 @@ def load_library(path: str = LIB_PATH):
         lib.pa_sparse_forward.restype = ci
         lib.pa_sparse_forward.argtypes = ([vp] * 9 + [ci] * 12 + [ctypes.c_float, ci, ci, vp, cs,
                                                                   vp])
+        lib.pa_q4_workspace_bytes.restype = cs
+        lib.pa_q4_workspace_bytes.argtypes = [ci]
+        lib.pa_q4_append.restype = ci
+        lib.pa_q4_append.argtypes = [vp] * 10 + [ll] * 3 + [vp] * 5 + [ci] * 13 + [vp, cs, vp]
+        lib.pa_q4_forward.restype = ci
+        lib.pa_q4_forward.argtypes = [vp] * 9 + [ci] * 9 + [ctypes.c_float, ci, vp, cs, vp]
         lib.pa_choose_v2.restype = ci
         lib.pa_choose_v2.argtypes = [ci] * 5
         lib.pa_choose_v2_chunks.restype = ci
@@ -333,10 +340,10 @@ def pa_chunks_forward(out, query, key_cache, value_cache, block_tables, seq_lens
         ctypes.byref(opts)), "pa_chunks_forward")
 
 
-def _pointers(first, workspace, same, ints):
-    """Data pointers of the workspace, of `same` (tensors of first's dtype) and of
-    `ints` (int32), in this order, 0 for None; all contiguous, on the current CUDA
-    device."""
+def _pointers(first, workspace, same, ints, *more):
+    """Data pointers of the workspace, of `same` (tensors of first's dtype), of
+    `ints` (int32) and of `more` ((dtype, tensors) each), in this order, 0 for
+    None; all contiguous, on the current CUDA device."""
     dtype = first.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
@@ -344,7 +351,7 @@ def _pointers(first, workspace, same, ints):
     if index < 0 or index != _current_device():
         raise ValueError(f"tensors on {first.device}: libpa runs on the current CUDA device")
     out = []
-    for want, tensors in ((workspace.dtype, (workspace,)), (dtype, same), (torch.int32, ints)):
+    for want, tensors in ((workspace.dtype, (workspace,)), (dtype, same), (torch.int32, ints), *more):
         for t in tensors:
             if t is None:
                 out.append(0)
@@ -370,6 +377,22 @@ def _rows(t, like, heads: int, head_size: int):
     if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError("libpa takes rows of contiguous heads")
     return t.data_ptr(), step if rows > 1 else h * d, rows
+
+
+def _angles(cos_sin, like, rotary_dim):
+    """(pointer, positions, rotary_dim) of a float32 [max_position, rotary_dim] table on
+    the device of `like`; rotary_dim None is its width."""
+    if cos_sin is None:
+        return 0, 0, int(rotary_dim or 0)
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 \
+            or cos_sin.get_device() != like.get_device():
+        raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+    max_position, width = cos_sin.shape
+    if rotary_dim is None:
+        rotary_dim = width
+    elif rotary_dim != width and rotary_dim != 0:
+        raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+    return _ptr(cos_sin), max_position, int(rotary_dim)
 
 
 def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, workspace,
@@ -410,22 +433,12 @@ def pa_append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, wor
             raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
     elif query_out is not None:
         raise ValueError("query_out without a query")
-    cs, max_position = 0, 0
-    if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 \
-                or cos_sin.get_device() != key_cache.get_device():
-            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
-        max_position, width = cos_sin.shape
-        if rotary_dim is None:
-            rotary_dim = width
-        elif rotary_dim != width and rotary_dim != 0:
-            raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
-        cs = _ptr(cos_sin)
+    cs, max_position, rotary_dim = _angles(cos_sin, key_cache, rotary_dim)
     if max_seq_len is None:
         max_seq_len = blocks * bs
     _check((_lib or load_library()).pa_append_kv(
         kc, vc, kb, qo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv, D, nb, bs,
-        blocks, int(max_seq_len), int(rotary_dim or 0), int(interleaved), max_position,
+        blocks, int(max_seq_len), rotary_dim, int(interleaved), max_position,
         _DTYPES[key_cache.dtype], ws, workspace.numel() * workspace.element_size(),
         _stream_handle(stream)), "pa_append_kv")
 
@@ -568,6 +581,111 @@ def pa_sparse_forward(out, selected, query, key_cache, value_cache, block_tables
         int(max_seq_len), int(num_selected), sink_blocks, recent_blocks, float(scale),
         int(partition_size), _DTYPES[query.dtype], ws,
         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "pa_sparse_forward")
+
+
+def pa_q4_workspace_bytes(head_size: int) -> int:
+    return int(load_library().pa_q4_workspace_bytes(head_size))
+
+
+def alloc_q4_workspace(head_size: int, device=None, stream=None) -> torch.Tensor:
+    """A zeroed workspace for pa_q4_forward calls of any batch."""
+    n = pa_q4_workspace_bytes(head_size)
+    if n == 0:
+        raise ValueError("bad head size for a 4-bit workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    pa_workspace_init(ws, stream)
+    return ws
+
+
+def alloc_q4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_size: int, device=None):
+    """(codes, scales) of an empty cache in 4 bits, for keys or for values: uint8
+    [num_blocks, Hkv, block_size, D / 2] and float16 [num_blocks, Hkv, block_size,
+    D / 64, 2]."""
+    shape = (num_blocks, num_kv_heads, block_size)
+    return (torch.zeros(*shape, head_size // 2, dtype=torch.uint8, device=device or "cuda"),
+            torch.zeros(*shape, head_size // 64, 2, dtype=torch.float16, device=device or "cuda"))
+
+
+def _q4_shapes(key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, q_start, head_size):
+    nb, hkv, bs, half = key_cache.shape
+    if value_cache.shape != key_cache.shape or half * 2 != head_size:
+        raise ValueError("key_cache and value_cache must be [num_blocks, num_kv_heads, block_size, "
+                         "head_size / 2]")
+    if key_scales.shape != (nb, hkv, bs, head_size // 64, 2) or value_scales.shape != key_scales.shape:
+        raise ValueError("key_scales and value_scales must be [num_blocks, num_kv_heads, block_size, "
+                         "head_size / 64, 2]")
+    B = seq_lens.numel()
+    if q_start is not None and q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [num_seqs + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    return nb, hkv, bs, B
+
+
+def pa_q4_append(key_cache, value_cache, key_scales, value_scales, key, value, block_tables,
+                 seq_lens, workspace, query=None, query_out=None, key_out=None, value_out=None,
+                 cos_sin=None, positions=None, q_start=None, rotary_dim=None, interleaved=False,
+                 max_seq_len=None, stream=None) -> None:
+    """Append key / value [rows, Hkv, D] (rows may be strided slices) to a cache in
+    4 bits: key_cache, value_cache uint8 [num_blocks, Hkv, block_size, D / 2],
+    key_scales, value_scales float16 [num_blocks, Hkv, block_size, D / 64, 2] (see
+    include/pa.h).  Keys and query are rotated as by pa_append_kv; key_out and
+    value_out [rows, Hkv, D] receive the values that the cache then holds."""
+    if key.dim() != 3:
+        raise ValueError("key must be [rows, num_kv_heads, head_size]")
+    D = key.shape[2]
+    ws, qo, ko, vo, bt, sl, qs, pos, kc, vc, ks, vs = _pointers(
+        key, workspace, (query_out, key_out, value_out), (block_tables, seq_lens, q_start, positions),
+        (torch.uint8, (key_cache, value_cache)), (torch.float16, (key_scales, value_scales)))
+    nb, hkv, bs, B = _q4_shapes(key_cache, value_cache, key_scales, value_scales, block_tables,
+                                seq_lens, q_start, D)
+    kp, kst, R = _rows(key, key, hkv, D)
+    vp, vst, rows = _rows(value, key, hkv, D)
+    if rows != R or any(t is not None and t.shape != (R, hkv, D) for t in (key_out, value_out)):
+        raise ValueError("key and value (and key_out, value_out) differ in shape")
+    if pos and positions.numel() != R:
+        raise ValueError("positions must be int32 [rows]")
+    H, qp, qst = hkv, 0, 0
+    if query is not None:
+        if query.dim() != 3 or query_out is None or query_out.shape != query.shape:
+            raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
+        H = query.shape[1]
+        qp, qst, rows = _rows(query, key, H, D)
+        if rows != R:
+            raise ValueError("query and query_out must both be [rows, num_heads, head_size]")
+    elif query_out is not None:
+        raise ValueError("query_out without a query")
+    cs, max_position, rotary_dim = _angles(cos_sin, key, rotary_dim)
+    blocks = block_tables.shape[1]
+    if max_seq_len is None:
+        max_seq_len = blocks * bs
+    _check((_lib or load_library()).pa_q4_append(
+        kc, vc, ks, vs, qo, ko, vo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv, D,
+        nb, bs, blocks, int(max_seq_len), rotary_dim, int(interleaved), max_position,
+        _DTYPES[key.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "pa_q4_append")
+
+
+def pa_q4_forward(out, query, key_cache, value_cache, key_scales, value_scales, block_tables,
+                  seq_lens, scale, workspace, q_start=None, max_seq_len=None, stream=None) -> None:
+    """Decode attention over a cache in 4 bits (pa_q4_append's), one query row a
+    sequence or, with q_start, chunks of them as in pa_chunks_forward (see
+    include/pa.h)."""
+    R, H, D = query.shape
+    ws, o, q, bt, sl, qs, kc, vc, ks, vs = _pointers(
+        query, workspace, (out, query), (block_tables, seq_lens, q_start),
+        (torch.uint8, (key_cache, value_cache)), (torch.float16, (key_scales, value_scales)))
+    nb, hkv, bs, B = _q4_shapes(key_cache, value_cache, key_scales, value_scales, block_tables,
+                                seq_lens, q_start, D)
+    if out.shape != query.shape:
+        raise ValueError("query and out differ in shape")
+    blocks = block_tables.shape[1]
+    if max_seq_len is None:
+        max_seq_len = blocks * bs
+    _check((_lib or load_library()).pa_q4_forward(
+        o, q, kc, vc, ks, vs, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks, int(max_seq_len),
+        float(scale), _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "pa_q4_forward")
 
 
 def pa_host_staging_bytes(num_seqs: int, num_heads: int, head_size: int,
