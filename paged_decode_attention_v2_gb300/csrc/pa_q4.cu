@@ -2,31 +2,39 @@
 // whose keys and values are held in 4 bits (pa_q4.h).
 //
 // With codes c, lowest values lo and steps st, group by group of 64 elements,
-//   q . K_t      = sum_g st_tg (q_g . c_tg) + lo_tg sum(q_g)
+//   q . K_t       = sum_g st_tg (q_g . c_tg) + lo_tg sum(q_g)
 //   sum_t p_t V_t = sum_t (p_t st_t) c_t + sum_t p_t lo_t      (of each group)
 // so the codes go into the matrix products as they are, and the steps and
-// lowest values meet scores and weights instead of elements.  A code becomes
-// an element of the MMA by a shift and one logic operation for two of them:
-// its four bits are the top of the mantissa of 16, which makes 16 + c.  The
-// 16s come off again with lo: lo' = lo - 16 st.
+// lowest values meet scores and weights instead of elements.  What a code costs
+// on its way there is what bounds this kernel next to the bytes (logic and shifts
+// run at half an instruction a cycle), so both products take codes in a form
+// that masking alone makes: four bits at the bottom of an f16 are c 2^-24, the
+// next four c 2^-20, as f16's lowest numbers are evenly spaced (and exact in
+// the MMA): five operations for eight codes.  Keys' powers of two are
+// made up for in the queries: a head is scaled by a power of two so that its
+// largest element is below 2^15 (or 2^11, against the larger codes), which f16
+// holds to the last bit of a bf16 or an f16 down to 2^-17 of it.  Values' come
+// off in the end.
 //
-// Weights: w = p st is rounded to bf16 for the product, and the sums take what
-// the product took: with a = 1 / st and b = lo' / st,
-//   out = (sum_t w_t (16 + c_t) + sum_t w_t b_t) / sum_t w_t a_t,
-// so that rounding w is rounding the softmax's weight, no more (the 16s and
-// lo would else be weighed differently from the codes).
+// Weights: the product takes w = p st in f16, so it must neither overflow nor
+// vanish with st: with S the larger of a token's steps, the running maximum is
+// that of x + log2 S (x: score in log2 units), p' = 2^(x + log2 S - m), and a
+// group's w = p' st / S.  The normaliser sum(p' / S) and the part of lo,
+// sum(p' lo / S), are summed in fp32.  w is off by at most 2^-12 of itself.
 //
-// Layout: S^T[16 tokens][8 heads] = K Q^T and O^T[D][8 heads] += V^T P^T by
-// mma.sync m16n8k16, a warp 16 tokens at a time.  Which element of a head is
-// which k of the product is free, and so is which element of V is which row of
-// O^T; both are chosen so that a lane's codes are whole words of a token's
-// row: words 4 t + .. (t = lane % 4) of a key's group, word g (g = lane / 4) of
-// a value's.  Rows sit in shared memory in an order (and with their 32-byte
-// groups swapped) that keeps those reads free of bank conflicts.
+// Layout: S^T[16 tokens][8 heads] = K Q^T and O^T[D][8 heads] += V^T P^T
+// (mma.sync m16n8k16, f16), a warp 16 tokens at a time.
+// Which element of a head is which k of the first product is free, and so is
+// which element of V is which row of O^T: ldmatrix hands a lane words of eight
+// codes of a key, and (transposed) units of four codes of two tokens' values,
+// and both are used as they come.  (Measured on GB300, cycles of a quarter of an
+// SM: 8.1 an f16 MMA, 2 a logic operation or byte move, 4 a movmatrix.  8-bit
+// MMAs of this kind are made of f16 ones and conversions there: slower.)
 //
-// A CTA has four warps; of every 64 tokens each takes 16, copied by cp.async
-// into its own ring, so no warp waits for another until the end of a piece of
-// a unit, where the four merge.  Work is split in equal shares (pa_share.cuh).
+// A warp takes shares of the work (pa_share.cuh) by itself, its tokens copied by
+// cp.async into its own ring of shared memory: no warp waits for another, and
+// what a warp has of a unit leaves from its registers.  (Four warps that shared
+// a unit's tokens and merged at its end spent 4 us on each piece of a unit.)
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -43,20 +51,23 @@ namespace {
 
 constexpr int kQ4Warps = 4;
 constexpr int kQ4Threads = kQ4Warps * 32;
+constexpr int kQ4MaxCtas = 4 * 152;                       // of a grid
+constexpr int kQ4Shares = (1 + kShareSmall) * kQ4MaxCtas * kQ4Warps;  // that a workspace has places for
 constexpr float kQ4Margin = 8.f;           // log2 units
 constexpr float kQ4LeastStep = 0x1p-24f;   // f16's smallest: stands in for a step of 0
+constexpr float kQ4None = -3.402823466e38f;  // the maximum of no keys
 
-constexpr int kQ4First = 1, kQ4Last = 2, kQ4End = 4;
-enum { kQ4Whole = 0, kQ4Place0 = 1, kQ4Place1 = 2 };
+enum { kQ4Whole = 0, kQ4Place0 = 1, kQ4Place1 = 2, kQ4End = 3 };
 
-// What a warp's ring stage holds, written with its copies.
-struct alignas(16) Q4Head {
-  int flags, valid;   // tokens of the stage in range
-  int tok0;           // the first of them
-  int lim_base;       // column c sees the tokens below lim_base + c / group + 1
+// A piece of a unit, as the walk hands it from a warp's copies to its products.
+struct alignas(16) Q4Piece {
+  int tok, end;       // the warp's first token, the end of the unit's tokens
+  int steps, dest;
   int rows, row0;     // columns of the unit, its first query row
-  int kvh, dest;
+  int kvh, lim_base;  // column c sees the tokens below lim_base + c / group + 1
+  int share, pad[3];
 };
+constexpr int kQ4Pieces = 8;  // handed over and not yet taken: at most stages + 1
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -77,68 +88,90 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  return __byte_perm(a, b, sel);
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-
-// Codes i and i + 4 of a word as the pair 16 + c_i, 16 + c_(i+4) of T: the code
-// at the top of the mantissa of 16.0.
-template <typename T, int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int at = bf ? 3 : 6;  // lowest bit of the mantissa's top four
-  constexpr uint32_t mask = (0xfu << at) * 0x10001u, base = bf ? 0x41804180u : 0x4c004c00u;
-  const uint32_t x = 4 * I >= at ? w >> (4 * I - at) : w << (at - 4 * I);
-  return (x & mask) | base;
+__device__ __forceinline__ float log2f_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The scales of a token's groups.
+template <int NG>
+__device__ __forceinline__ void load_scales(const uint8_t *at, float2 (&z)[NG]) {
+  uint32_t w[NG];
+  if constexpr (NG == 1) {
+    w[0] = *reinterpret_cast<const uint32_t *>(at);
+  } else if constexpr (NG == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(at);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4 *>(at);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < NG; ++i) z[i] = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+}
 template <int D, int NT>
 struct Q4Shape {
   static constexpr int NG = D / kQ4Group;   // groups of a head
   static constexpr int RB = D / 2;          // bytes of a row's codes
-  static constexpr int CPR = RB / 16;       // 16-byte pieces of a row
+  static constexpr int CPR = RB / 16;       // 16-byte pieces (32 codes) of a row
   static constexpr int GM = 8 * NT;         // columns of a unit
-  static constexpr int KEYS = 0, VALUES = 16 * RB, KSC = 32 * RB, VSC = KSC + 64 * NG,
-                       HEAD = VSC + 64 * NG, STAGE = (HEAD + (int)sizeof(Q4Head) + 127) / 128 * 128;
+  // tiles of 16 tokens that a warp takes at once: two give the MMAs of one
+  // something to run beside, where registers allow
+  static constexpr int TT = NT == 1 && D <= 128 ? 2 : 1;
+  static constexpr int TOKENS = 16 * TT;  // of a step
+  static constexpr int QREGS = CPR * NT * 4;
+  static constexpr bool QSMEM = QREGS > 32;  // query fragments in shared memory
+  static constexpr int KEYS = 0, VALUES = TOKENS * RB, KSC = 2 * TOKENS * RB, VSC = KSC + TOKENS * 4 * NG,
+                       STAGE = VSC + TOKENS * 4 * NG;
   // CTAs an SM by registers, and the ring that their shared memory leaves
-  static constexpr int CTAS = NT == 1 ? (D == 256 ? 3 : 4) : (D == 256 ? 2 : 3);
-  static constexpr int STAGES = D == 256 ? (NT == 1 ? 3 : 4) : 4;
-  static constexpr int OROW = D + 4;        // floats between rows of the merge
-  static constexpr int OBUF = 2 * GM * OROW * 4;
-  static constexpr int SMEM = kQ4Warps * STAGES * STAGE + OBUF;
-  // place of a token's row in a stage: the even ones of eight first, so that
-  // the four tokens 2t that a warp reads at once are neighbours
-  __device__ static __forceinline__ int place(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
-  // which 32-byte group of a row stands where
-  __device__ static __forceinline__ int swap(int pl) {
-    return NG == 1 ? 0 : NG == 2 ? ((pl >> 1) ^ (pl >> 2)) & 1 : (pl & 3) ^ ((pl >> 1) & 2);
+  static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : 3) : (D == 256 ? 2 : 3);
+  static constexpr int STAGES = D == 256 || (D == 128 && NT == 1) ? 3 : 4;
+  static constexpr int CACHE = D == 256 && NT == 1 ? 64 : 384;  // sequences of the plan kept by
+  static constexpr int QBUF = QSMEM ? QREGS * 128 : 0;  // a warp's
+  static constexpr int SMEM = kQ4Warps * (STAGES * STAGE + QBUF);
+  // where piece c of row r stands: eight rows' pieces c in eight 16-byte columns
+  __device__ static __forceinline__ int at(int r, int c) {
+    return r * RB + ((c ^ (CPR == 2 ? (r >> 2) & 1 : CPR == 4 ? (r >> 1) & 3 : r & 7)) << 4);
   }
 };
 
 struct Q4Batch {
   const Q4Params &p;
-  int num_seqs;
-  bool tell;  // report what is bad
-  __device__ __forceinline__ ShareSeq seq(int s) const {
-    ShareSeq q;
-    q.len = __ldg(p.seq_lens + s);
-    q.row0 = s;
-    q.n = 1;
-    q.units = p.num_kv_heads;
-    bool bad = q.len < 0 || q.len > p.max_seq_len;
+  int num_seqs, step;  // step: tokens
+  bool tell;           // report what is bad
+  __device__ __forceinline__ int4 read(int s) const {
+    int4 r = make_int4(__ldg(p.seq_lens + s), s, 1, 0);
+    bool bad = r.x < 0 || r.x > p.max_seq_len;
     if (p.q_start) {
-      q.row0 = __ldg(p.q_start + s);
+      r.y = __ldg(p.q_start + s);
       const int e = __ldg(p.q_start + s + 1);
-      q.n = e - q.row0;
-      bad = bad || q.row0 < 0 || q.n < 0 || e > p.num_rows || q.n > q.len;
-      q.units = bad ? 0 : p.num_kv_heads * ((q.n + p.chunk_tokens - 1) / p.chunk_tokens);
+      bad = bad || r.y < 0 || e < r.y || e > p.num_rows || e - r.y > r.x;
+      r.z = e - r.y;
     }
     if (bad) {
       if (tell) report(p.status, kStatusBadInput);
-      q.len = 0;
+      r.x = r.z = 0;
     }
-    q.steps = (int)(((long long)q.len + kShareStep - 1) / kShareStep);
-    if (q.steps == 0) q.units = 0;
+    return r;
+  }
+  __device__ __forceinline__ ShareSeq seq(const int4 &r) const {
+    ShareSeq q{r.x, r.y, r.z, 0, 0};
+    q.steps = (r.x + step - 1) / step;  // (at most 2^30 keys)
+    if (q.steps > 0)
+      q.units = p.q_start ? p.num_kv_heads * ((r.z + p.chunk_tokens - 1) / p.chunk_tokens) : p.num_kv_heads;
     return q;
   }
 };
@@ -149,434 +182,453 @@ template <typename T, int D, int NT, bool CHUNK>
 __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
     pa_q4_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ ShareSpace space) {
   using Z = Q4Shape<D, NT>;
-  constexpr int NG = Z::NG, RB = Z::RB, CPR = Z::CPR, GM = Z::GM, NST = Z::STAGES, KW = 4 * NG;
+  constexpr int NG = Z::NG, RB = Z::RB, CPR = Z::CPR, GM = Z::GM, NST = Z::STAGES, TT = Z::TT;
   extern __shared__ __align__(128) uint8_t smem_q4[];
-  __shared__ ShareScan<kQ4Threads> s_scan;
-  __shared__ float s_m[kQ4Warps][GM];               // a warp's maximum in use
-  __shared__ float2 s_sum[kQ4Warps][GM][NG];        // its sums of w a, w b
-  __shared__ float s_top[GM];                       // the merged maximum
+  __shared__ ShareScan<kQ4Threads, Z::CACHE> s_scan;
+  __shared__ Q4Piece s_piece[kQ4Warps][kQ4Pieces];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t *ring = smem_q4 + warp * (NST * Z::STAGE);
   const uint32_t ring_u32 = smem_u32(ring);
-  float *obuf = reinterpret_cast<float *>(smem_q4 + kQ4Warps * NST * Z::STAGE);
+  uint4 *qbuf = reinterpret_cast<uint4 *>(smem_q4 + kQ4Warps * NST * Z::STAGE + warp * Z::QBUF);
 
   pdl_wait_primary();
-  Q4Batch batch{p, p.num_seqs, blockIdx.x == 0};
-  share_scan<kQ4Threads>(batch, s_scan);
+  Q4Batch batch{p, p.num_seqs, Z::TOKENS, blockIdx.x == 0};
+  share_scan(batch, s_scan);
   batch.tell = false;
-  const long long total = s_scan.cum[kQ4Threads];
-  const int shares = share_count(total, gridDim.x, 1), me = blockIdx.x;
-  long long line = share_begin(total, me, shares), line_end = share_begin(total, me + 1, shares);
-  if (me >= shares) line = line_end = total;
+  SharePlan plan;
+  plan.make(s_scan.cum[kQ4Threads], (int)gridDim.x * kQ4Warps);
 
-  // outputs of empty sequences
-  if (!CHUNK)
-    for (int s = me; s < p.num_seqs; s += gridDim.x)
-      if (batch.seq(s).len == 0) {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (size_t)s * p.num_heads * D);
-        for (int i = threadIdx.x; i < p.num_heads * D / 8; i += kQ4Threads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
+  // the row of the query (and output) that is column c of a unit
+  auto query_row = [&](int row0, int kvh, int c) -> size_t {
+    const int tok = CHUNK ? c / p.group : 0;
+    return (size_t)(row0 + tok) * p.num_heads + (size_t)(kvh * p.group + c - tok * p.group);
+  };
 
-  // ---- the walk over the share, one tile ahead of the copies
-  ShareWalk walk;
-  walk.begin(batch, s_scan, line, line_end);
-  bool joined = false;
-  int in_piece = 0, f_flags = 0, f_tok = 0, f_end = 0, e0 = -1, e1 = -1;
-  int u_rows = 0, u_row0 = 0, u_kvh = 0, u_lim = 0, u_dest = 0;
+  // ---- the walk over the share, a tile ahead of the copies
+  ShareWalk walk{};
+  int share = (int)blockIdx.x * kQ4Warps + warp;  // the one that is walked
+  walk.begin(batch, s_scan, plan.begin(share), share < plan.big ? plan.begin(share + 1) : 0);
+  int handed = 0;                                  // pieces
+  int f_left = 0, f_tok = 0, f_end = 0, f_at = 0;  // tiles left of the piece, their next token, its KV head's place
   const int32_t *table = p.block_tables;
-  auto fetch = [&]() {
-    if (in_piece == 0) {
-      if (walk.left <= 0) {
-        f_flags = kQ4End;
-        return;
-      }
+  const int hbs = p.num_kv_heads * p.block_size;
+  auto next_piece = [&]() {
+    if (walk.left <= 0 && plan.small > 0) {
+      int k = 0;
+      if (lane == 0) k = atomicAdd(space.counters + kShareTaken, 1) & 0x7fffffff;
+      k = __shfl_sync(0xffffffffu, k, 0);
+      share = plan.big + k;
+      if (k < plan.small) walk.begin(batch, s_scan, plan.begin(share), plan.begin(share + 1));
+    }
+    Q4Piece u{};
+    u.dest = kQ4End;
+    if (walk.left > 0) {
       const int n = walk.piece(), step = walk.step;
-      int rg = 0;
-      u_kvh = walk.unit;
-      u_rows = p.group;
-      u_row0 = walk.s;
-      u_lim = walk.q.len - 1;
-      f_end = walk.q.len;
+      u.kvh = walk.unit;
+      u.rows = p.group;
+      u.row0 = walk.s;
+      u.lim_base = walk.q.len - 1;
+      u.end = walk.q.len;
       if (CHUNK) {
         const int nrg = (walk.q.n + p.chunk_tokens - 1) / p.chunk_tokens;
-        u_kvh = walk.unit / nrg;
-        rg = walk.unit - u_kvh * nrg;
-        const int t0 = rg * p.chunk_tokens, nt = min(p.chunk_tokens, walk.q.n - t0);
-        u_rows = nt * p.group;
-        u_row0 = walk.q.row0 + t0;
-        u_lim = walk.q.len - walk.q.n + t0;
-        f_end = u_lim + nt;
+        u.kvh = walk.unit / nrg;
+        const int t0 = (walk.unit - u.kvh * nrg) * p.chunk_tokens, nt = min(p.chunk_tokens, walk.q.n - t0);
+        u.rows = nt * p.group;
+        u.row0 = walk.q.row0 + t0;
+        u.lim_base = walk.q.len - walk.q.n + t0;
+        u.end = u.lim_base + nt;
       }
-      const bool ends = step + n == walk.q.steps;
-      u_dest = step > 0 ? kQ4Place0 : ends ? kQ4Whole : kQ4Place1;
-      if (u_dest == kQ4Place1 && threadIdx.x == 0) {
+      u.dest = step > 0 ? kQ4Place0 : step + n == walk.q.steps ? kQ4Whole : kQ4Place1;
+      u.steps = n;
+      u.share = share;
+      u.tok = step * Z::TOKENS;
+      if (u.dest == kQ4Place1 && lane == 0) {
         ShareJoin j{};
-        j.parts = share_of(total, line + walk.q.steps - 1, shares) - me + 1;
-        j.rows = u_rows;
+        j.share = share;
+        j.parts = plan.of(walk.line + walk.q.steps - 1) - share + 1;
+        j.by = 1;
+        j.rows = u.rows;
         j.group = p.group;
         j.stride = p.num_heads;
-        j.out_row = (long long)u_row0 * p.num_heads + u_kvh * p.group;
-        space.join[me] = j;
+        j.out_row = (long long)u.row0 * p.num_heads + u.kvh * p.group;
+        share_join(space, j);
       }
-      joined = joined || u_dest == kQ4Place1;
-      table = p.block_tables + (size_t)walk.s * p.max_blocks_per_seq;
-      line += n;
-      in_piece = n;
-      f_tok = step * kShareStep + warp * 16;
-      f_flags = kQ4First;
-      walk.next(batch);
-    } else {
-      f_tok += kShareStep;
-      f_flags = 0;
-    }
-    if (--in_piece == 0) f_flags |= kQ4Last;
-    e0 = f_tok < f_end ? __ldg(table + (f_tok >> p.log2_block_size)) : -1;
-    e1 = f_tok + 8 < f_end ? __ldg(table + ((f_tok + 8) >> p.log2_block_size)) : -1;
-  };
-  fetch();
-
-  // ---- one stage of copies: the fetched tile's codes and scales
-  auto issue = [&](int slot) {
-    const uint32_t st = ring_u32 + (uint32_t)slot * Z::STAGE;
-    if (lane == 0) {
-      Q4Head *h = reinterpret_cast<Q4Head *>(ring + slot * Z::STAGE + Z::HEAD);
-      *reinterpret_cast<int4 *>(h) = make_int4(f_flags, max(min(f_end - f_tok, 16), 0), f_tok, u_lim);
-      *(reinterpret_cast<int4 *>(h) + 1) = make_int4(u_rows, u_row0, u_kvh, u_dest);
-    }
-    if (!(f_flags & kQ4End)) {
-      const int valid = f_end - f_tok;
-      bool ok0 = valid > 0, ok1 = valid > 8;
-      if ((ok0 && (unsigned)e0 >= (unsigned)p.num_blocks) || (ok1 && (unsigned)e1 >= (unsigned)p.num_blocks)) {
-        report(p.status, kStatusBadInput);  // those rows are taken as zeros
-        ok0 = ok0 && (unsigned)e0 < (unsigned)p.num_blocks;
-        ok1 = ok1 && (unsigned)e1 < (unsigned)p.num_blocks;
-      }
-      // the first row's place in the cache of each half of the tile
-      const size_t s0 = ok0 ? ((size_t)e0 * p.num_kv_heads + u_kvh) * p.block_size + (f_tok & (p.block_size - 1)) : 0;
-      const size_t s1 =
-          ok1 ? ((size_t)e1 * p.num_kv_heads + u_kvh) * p.block_size + ((f_tok + 8) & (p.block_size - 1)) : 0;
+      // (its queries on their way to L2)
 #pragma unroll
-      for (int j = 0; j < (16 * CPR + 31) / 32; ++j) {
-        const int i = lane + 32 * j, r = i / CPR, c = i % CPR;  // CPR 2: 32 pieces in all
-        const int pl = Z::place(r);
-        const uint32_t dst = st + (uint32_t)(pl * RB + (((c >> 1) ^ Z::swap(pl)) << 5) + ((c & 1) << 4));
-        const size_t src = (r < 8 ? s0 : s1) * RB + (size_t)((r & 7) * RB + c * 16);
-        const uint32_t n = (r < 8 ? ok0 : ok1) && r < valid ? 16u : 0u;
-        const size_t from = n ? src : 0;
-        cp_async16(dst + Z::KEYS, p.key_codes + from, n);
-        cp_async16(dst + Z::VALUES, p.value_codes + from, n);
+      for (int i = lane; i < GM * (D / 64); i += 32) {
+        const int c = i / (D / 64);
+        if (c < u.rows)
+          prefetch_l2(static_cast<const T *>(p.query) + query_row(u.row0, u.kvh, c) * D + i % (D / 64) * 64);
       }
-      {
-        const int r = lane & 15;
-        const uint32_t n = (r < 8 ? ok0 : ok1) && r < valid ? 4u * NG : 0u;
-        const size_t src = n ? ((r < 8 ? s0 : s1) + (size_t)(r & 7)) * (4 * NG) : 0;
-        const void *from = (lane < 16 ? static_cast<const uint8_t *>(p.key_scales)
-                                      : static_cast<const uint8_t *>(p.value_scales)) + src;
-        const uint32_t dst = st + (lane < 16 ? Z::KSC : Z::VSC) + r * 4 * NG;
-        cp_async_small<4 * NG>(dst, from, n);
+      table = p.block_tables + (size_t)walk.s * p.max_blocks_per_seq;
+      f_left = n;
+      f_tok = u.tok;
+      f_end = u.end;
+      f_at = u.kvh * p.block_size;
+      walk.next(batch, s_scan);
+    }
+    if (lane == 0) s_piece[warp][handed & (kQ4Pieces - 1)] = u;
+    ++handed;
+  };
+  // the table entries of the next tiles, of 16 tokens each (of pages of 8 tokens: looked
+  // up with the copies)
+  int e[TT];
+#pragma unroll
+  for (int h = 0; h < TT; ++h) e[h] = -1;
+  auto look_up = [&]() {
+#pragma unroll
+    for (int h = 0; h < TT; ++h)
+      if (f_left > 0 && f_tok + 16 * h < f_end) e[h] = __ldg(table + ((f_tok + 16 * h) >> p.log2_block_size));
+  };
+  next_piece();
+  look_up();
+
+  // ---- one stage of copies
+  const uint32_t lane_dst = ring_u32 + (uint32_t)Z::at(lane / CPR, lane % CPR);
+  const uint8_t *const keys = p.key_codes + lane * 16, *const values = p.value_codes + lane * 16;
+  const uint8_t *const key_scales = static_cast<const uint8_t *>(p.key_scales), *const value_scales = static_cast<const uint8_t *>(p.value_scales);
+  auto issue = [&](uint32_t slot) {  // (a slot is its offset in the ring)
+    if (f_left > 0) {
+      bool whole = f_end - f_tok >= Z::TOKENS && p.block_size != 8;
+#pragma unroll
+      for (int h = 0; h < TT; ++h) whole = whole && (unsigned)e[h] < (unsigned)p.num_blocks;
+      if (whole) {
+#pragma unroll
+        for (int h = 0; h < TT; ++h) {  // sixteen rows one behind the other
+          const uint32_t row = (uint32_t)e[h] * hbs + (f_at + ((f_tok + 16 * h) & (p.block_size - 1)));
+          const uint8_t *k = keys + (size_t)row * RB, *v = values + (size_t)row * RB;
+          const uint32_t dst = lane_dst + slot + 16u * RB * h;
+#pragma unroll
+          for (int j = 0; j < CPR / 2; ++j) {
+            // rows 32 j / CPR on: eight (or sixteen) rows swap pieces alike, four rows
+            // (CPR 8) on the other side
+            const uint32_t to = (CPR == 8 && (j & 1) ? dst ^ 64u : dst) + 512u * j;
+            cp_async16(to + Z::KEYS, k + 512 * j, 16);
+            cp_async16(to + Z::VALUES, v + 512 * j, 16);
+          }
+          const size_t sc = (size_t)(row + (lane & 15)) * (4 * NG);
+          cp_async_small<4 * NG>(ring_u32 + slot + (lane < 16 ? Z::KSC : Z::VSC) + (16 * h + (lane & 15)) * 4 * NG,
+                                 (lane < 16 ? key_scales : value_scales) + sc, 4 * NG);
+        }
+      } else if (f_end > f_tok) {
+        // the last tokens, pages of 8, bad entries: row by row; rows out of range are zeros
+        auto place = [&](int r, bool &on) -> size_t {
+          on = f_tok + r < f_end;
+          const int blk = on ? __ldg(table + ((f_tok + r) >> p.log2_block_size)) : 0;
+          if ((unsigned)blk >= (unsigned)p.num_blocks) {
+            report(p.status, kStatusBadInput);
+            on = false;
+          }
+          return on ? (size_t)(uint32_t)(blk * hbs + f_at + ((f_tok + r) & (p.block_size - 1))) : 0;
+        };
+#pragma unroll
+        for (int j = 0; j < TT * CPR / 2; ++j) {
+          const int i = lane + 32 * j, r = i / CPR, c = i % CPR;
+          const uint32_t to = ring_u32 + slot + (uint32_t)Z::at(r, c);
+          bool on;
+          size_t src = place(r, on) * RB;
+          src += on ? c * 16 : 0;
+          cp_async16(to + Z::KEYS, p.key_codes + src, on ? 16 : 0);
+          cp_async16(to + Z::VALUES, p.value_codes + src, on ? 16 : 0);
+        }
+#pragma unroll
+        for (int h = 0; h < TT; ++h) {
+          const int r = 16 * h + (lane & 15);
+          bool on;
+          const size_t src = place(r, on) * (4 * NG);
+          cp_async_small<4 * NG>(ring_u32 + slot + (lane < 16 ? Z::KSC : Z::VSC) + r * 4 * NG,
+                                 (lane < 16 ? key_scales : value_scales) + src, on ? 4 * NG : 0);
+        }
       }
-      fetch();
+      f_tok += Z::TOKENS;
+      if (--f_left == 0) next_piece();
+      look_up();
     }
     cp_async_commit();
   };
 
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) issue(i);
+  for (int i = 0; i < NST - 1; ++i) issue((uint32_t)(i * Z::STAGE));
 
   // ---- the tiles
-  uint32_t qf[NT][KW][2];      // Q^T fragments, in the keys' order of elements
-  float qsum[NT][NG][2];       // scale_log2 x the sum of the group's q, of this lane's columns
-  float o[NT][KW][4];          // O^T: rows 64 gr + 8 g + 2 mt (+ 1), columns 2t, 2t + 1
-  float sa[NT][NG][2], sb[NT][NG][2], m[NT][2];
+  uint4 qf[Z::QSMEM ? 1 : NT][Z::QSMEM ? 1 : CPR];  // Q^T fragments of two k-steps
+  float qsum[NT][NG][2];  // scale x the sum of the group's q, of this lane's columns
+  float qmul[NT][2];      // what the columns' products are worth
+  float o[NT][2 * CPR][4];  // O^T: row pairs (g, g + 8), columns 2t, 2t + 1
+  float sl[NT][2], sb[NT][NG][2], m[NT][2];
   int lim[CHUNK ? NT : 1][2];
+  int rows = 0, row0 = 0, kvh = 0, dest = 0, at_share = 0, left = 0, tok = 0, end = 0, taken = 0;
 
-  for (int slot = 0;; slot = slot + 1 == NST ? 0 : slot + 1) {
+  // (slots: of this tile, and of the one to copy, whose last tile is done with)
+  for (uint32_t slot = 0, copy = (NST - 1) * Z::STAGE;; copy = slot, slot = slot + Z::STAGE == NST * Z::STAGE ? 0 : slot + Z::STAGE) {
     cp_async_wait<NST - 2>();
     __syncwarp();
-    uint8_t *stage = ring + slot * Z::STAGE;
-    const Q4Head h = *reinterpret_cast<const Q4Head *>(stage + Z::HEAD);
-    if (h.flags & kQ4End) break;
-    issue(slot == 0 ? NST - 1 : slot - 1);
-
-    if (h.flags & kQ4First) {
-      // queries: lane (g, t) has elements 16 t .. 16 t + 15 of each group of column g
+    const uint8_t *stage = ring + slot;
+    const uint32_t stage_u32 = ring_u32 + slot;
+    if (left == 0) {
+      const Q4Piece u = s_piece[warp][taken++ & (kQ4Pieces - 1)];
+      if (u.dest == kQ4End) break;
+      rows = u.rows, row0 = u.row0, kvh = u.kvh, dest = u.dest, at_share = u.share;
+      left = u.steps, tok = u.tok, end = u.end;
+      // queries: lane (g, t) has elements 8 t .. 8 t + 7 of each 32 of column g
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int c = nt * 8 + g;
-        const bool live = c < h.rows;
-        const size_t row = (size_t)(h.row0 + c / p.group) * p.num_heads + (size_t)(h.kvh * p.group + c % p.group);
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) + (live ? row : 0) * D) + 2 * t;
+        const bool live = c < rows;
+        const uint4 *src =
+            reinterpret_cast<const uint4 *>(static_cast<const T *>(p.query) + (live ? query_row(row0, kvh, c) : 0) * D) + t;
+        float top = 0.f, sum[NG];
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-          if (live) {
-            a = __ldg(src + gr * 8);
-            b = __ldg(src + gr * 8 + 1);
-          }
-          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-          float sum = 0.f;
+        for (int i = 0; i < NG; ++i) sum[i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+        for (int ch = 0; ch < CPR; ++ch) {
+          const uint4 a = live ? __ldg(src + 4 * ch) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             const float2 f = MmaOp<T>::unpack(w[i]);
-            sum += f.x + f.y;
-          }
-          // k-step 4 gr + 2 wi + h2: codes 2 h2, 2 h2 + 4 | 2 h2 + 1, 2 h2 + 5 of word wi
-#pragma unroll
-          for (int wi = 0; wi < 2; ++wi)
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-              qf[nt][4 * gr + 2 * wi + h2][0] = prmt(w[4 * wi + h2], w[4 * wi + h2 + 2], 0x5410);
-              qf[nt][4 * gr + 2 * wi + h2][1] = prmt(w[4 * wi + h2], w[4 * wi + h2 + 2], 0x7632);
-            }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          qsum[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * t) * p.scale_log2;
-          qsum[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4) * p.scale_log2;
-          sa[nt][gr][0] = sa[nt][gr][1] = sb[nt][gr][0] = sb[nt][gr][1] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < KW; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-        m[nt][0] = m[nt][1] = -CUDART_INF_F;
-        if (CHUNK)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) lim[nt][e] = h.lim_base + (nt * 8 + 2 * t + e) / p.group + 1;
-      }
-    }
-
-    if (h.valid > 0) {
-      // ---- scores: x = scale_log2 q . K of tokens g, g + 8 and columns 2t, 2t + 1
-      float x[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
-      const int pa0 = Z::place(g);  // rows g and g + 8: places pa0, pa0 + 8, swapped alike
-      const uint8_t *krow = stage + Z::KEYS + pa0 * RB;
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        const int off = ((gr ^ Z::swap(pa0)) << 5) + 8 * t;
-        const uint2 wa = *reinterpret_cast<const uint2 *>(krow + off);
-        const uint2 wb = *reinterpret_cast<const uint2 *>(krow + 8 * RB + off);
-        float acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
-        for (int wi = 0; wi < 2; ++wi) {
-          const uint32_t a = wi ? wa.y : wa.x, b = wi ? wb.y : wb.x;
-          const uint32_t a0 = code_pair<T, 0>(a), a1 = code_pair<T, 1>(a), a2 = code_pair<T, 2>(a), a3 = code_pair<T, 3>(a);
-          const uint32_t b0 = code_pair<T, 0>(b), b1 = code_pair<T, 1>(b), b2 = code_pair<T, 2>(b), b3 = code_pair<T, 3>(b);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int ks = 4 * gr + 2 * wi;
-            MmaOp<T>::run(acc[nt], a0, b0, a1, b1, qf[nt][ks][0], qf[nt][ks][1]);
-            MmaOp<T>::run(acc[nt], a2, b2, a3, b3, qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            sum[ch >> 1] += f.x + f.y;
           }
         }
-        const float2 za = __half22float2(*reinterpret_cast<const __half2 *>(stage + Z::KSC + (g * NG + gr) * 4));
-        const float2 zb = __half22float2(*reinterpret_cast<const __half2 *>(stage + Z::KSC + ((g + 8) * NG + gr) * 4));
-        const float la = fmaf(-16.f, za.y, za.x), lb = fmaf(-16.f, zb.y, zb.x);
-        const float ta = za.y * p.scale_log2, tb = zb.y * p.scale_log2;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          x[nt][0] = fmaf(ta, acc[nt][0], fmaf(la, qsum[nt][gr][0], x[nt][0]));
-          x[nt][1] = fmaf(ta, acc[nt][1], fmaf(la, qsum[nt][gr][1], x[nt][1]));
-          x[nt][2] = fmaf(tb, acc[nt][2], fmaf(lb, qsum[nt][gr][0], x[nt][2]));
-          x[nt][3] = fmaf(tb, acc[nt][3], fmaf(lb, qsum[nt][gr][1], x[nt][3]));
+        for (int i = 0; i < NG; ++i) {
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
         }
-      }
-      // ---- the running maximum, raised when a score is 2^8 above it: any
-      // reference serves the sums as long as nothing overflows
-      bool up = false;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the head times 2^(14 - e), e the exponent of its largest: below 2^15
+        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        // (scores come in units of 2^(e - 14) 2^-24)
+        const float down = top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * 0x1p10f : CUDART_NAN_F;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (h.valid < 16) {
-          if (g >= h.valid) x[nt][0] = x[nt][1] = -CUDART_INF_F;
-          if (g + 8 >= h.valid) x[nt][2] = x[nt][3] = -CUDART_INF_F;
-        }
-        if (CHUNK) {
-          if (h.tok0 + g >= lim[nt][0]) x[nt][0] = -CUDART_INF_F;
-          if (h.tok0 + g >= lim[nt][1]) x[nt][1] = -CUDART_INF_F;
-          if (h.tok0 + g + 8 >= lim[nt][0]) x[nt][2] = -CUDART_INF_F;
-          if (h.tok0 + g + 8 >= lim[nt][1]) x[nt][3] = -CUDART_INF_F;
-        }
-        up = up || fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + kQ4Margin || fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + kQ4Margin;
-      }
-      if (__any_sync(0xffffffffu, up)) {
+        for (int ch = 0; ch < CPR; ++ch) {
+          const uint4 a = live ? __ldg(src + 4 * ch) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+          float f[8];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float t0 = fmaxf(x[nt][0], x[nt][2]), t1 = fmaxf(x[nt][1], x[nt][3]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = MmaOp<T>::unpack(w[i]);
+            f[2 * i] = v.x * up, f[2 * i + 1] = v.y * (up * 0.0625f);
           }
-          t0 = fmaxf(t0, m[nt][0]), t1 = fmaxf(t1, m[nt][1]);
-          const float f0 = t0 == -CUDART_INF_F ? 1.f : exp2f(m[nt][0] - t0);
-          const float f1 = t1 == -CUDART_INF_F ? 1.f : exp2f(m[nt][1] - t1);
-          m[nt][0] = t0, m[nt][1] = t1;
+          // elements 0, 4 | 2, 6 against the codes 2^-24, then 1, 5 | 3, 7 against 2^-20
+          using H = MmaOp<__half>;
+          const uint4 q = make_uint4(H::pack(f[0], f[4]), H::pack(f[2], f[6]), H::pack(f[1], f[5]), H::pack(f[3], f[7]));
+          if constexpr (Z::QSMEM)
+            qbuf[(nt * CPR + ch) * 32 + lane] = q;
+          else
+            qf[nt][ch] = q;
+        }
 #pragma unroll
-          for (int i = 0; i < KW; ++i) {
-            o[nt][i][0] *= f0, o[nt][i][1] *= f1;
-            o[nt][i][2] *= f0, o[nt][i][3] *= f1;
-          }
+        for (int i = 0; i < 2; ++i) {
+          qmul[nt][i] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * i) * p.scale_log2;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            sa[nt][gr][0] *= f0, sa[nt][gr][1] *= f1;
-            sb[nt][gr][0] *= f0, sb[nt][gr][1] *= f1;
+            qsum[nt][gr][i] = __shfl_sync(0xffffffffu, sum[gr], 8 * t + 4 * i) * p.scale_log2;
+            sb[nt][gr][i] = 0.f;
           }
+          sl[nt][i] = 0.f;
+          m[nt][i] = kQ4None;
+          if (CHUNK) lim[nt][i] = u.lim_base + (nt * 8 + 2 * t + i) / p.group + 1;
         }
+#pragma unroll
+        for (int i = 0; i < 2 * CPR; ++i)
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2) o[nt][i][e2] = 0.f;
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -CUDART_INF_F ? 0.f : m[nt][0];
-        const float m1 = m[nt][1] == -CUDART_INF_F ? 0.f : m[nt][1];
-        x[nt][0] = ex2f(x[nt][0] - m0), x[nt][1] = ex2f(x[nt][1] - m1);
-        x[nt][2] = ex2f(x[nt][2] - m0), x[nt][3] = ex2f(x[nt][3] - m1);
-      }
-      // ---- O^T += V^T P^T, group by group: a lane's word g of tokens 2t, 2t + 1
-      // (places t, t + 4) and of the eight behind
-      const uint8_t *vrow = stage + Z::VALUES + t * RB;
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        const float2 za = __half22float2(*reinterpret_cast<const __half2 *>(stage + Z::VSC + (g * NG + gr) * 4));
-        const float2 zb = __half22float2(*reinterpret_cast<const __half2 *>(stage + Z::VSC + ((g + 8) * NG + gr) * 4));
-        const float ta = fmaxf(za.y, kQ4LeastStep), tb = fmaxf(zb.y, kQ4LeastStep);
-        const float ra = __frcp_rn(ta), rb = __frcp_rn(tb);
-        const float ba = fmaf(za.x, ra, -16.f), bb = fmaf(zb.x, rb, -16.f);
-        uint32_t pf[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t lo = MmaOp<__nv_bfloat16>::pack(x[nt][0] * ta, x[nt][1] * ta);
-          const uint32_t hi = MmaOp<__nv_bfloat16>::pack(x[nt][2] * tb, x[nt][3] * tb);
-          const float2 wl = MmaOp<__nv_bfloat16>::unpack(lo), wh = MmaOp<__nv_bfloat16>::unpack(hi);
-          sa[nt][gr][0] = fmaf(wl.x, ra, fmaf(wh.x, rb, sa[nt][gr][0]));
-          sa[nt][gr][1] = fmaf(wl.y, ra, fmaf(wh.y, rb, sa[nt][gr][1]));
-          sb[nt][gr][0] = fmaf(wl.x, ba, fmaf(wh.x, bb, sb[nt][gr][0]));
-          sb[nt][gr][1] = fmaf(wl.y, ba, fmaf(wh.y, bb, sb[nt][gr][1]));
-          pf[nt][0] = movmatrix_trans(lo);
-          pf[nt][1] = movmatrix_trans(hi);
-        }
-        const int off = ((gr ^ Z::swap(t)) << 5) + 4 * g, off4 = ((gr ^ Z::swap(t + 4)) << 5) + 4 * g;
-        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vrow + off);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vrow + 4 * RB + off4);
-        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(vrow + 8 * RB + off);
-        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(vrow + 12 * RB + off4);
-        using B = __nv_bfloat16;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // codes 0 .. 3, then 4 .. 7 of the word
-          const uint32_t sel = half ? 0x7632 : 0x5410;
-          const uint32_t a = prmt(w0, w1, sel), b = prmt(w2, w3, sel);
-          // halves of a: codes 4 half .. + 3 of tokens 2t and 2t + 1, so pair I is code I of both
-          const uint32_t a0 = code_pair<B, 0>(a), a1 = code_pair<B, 1>(a), a2 = code_pair<B, 2>(a), a3 = code_pair<B, 3>(a);
-          const uint32_t b0 = code_pair<B, 0>(b), b1 = code_pair<B, 1>(b), b2 = code_pair<B, 2>(b), b3 = code_pair<B, 3>(b);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            MmaOp<B>::run(o[nt][4 * gr + 2 * half], a0, a1, b0, b1, pf[nt][0], pf[nt][1]);
-            MmaOp<B>::run(o[nt][4 * gr + 2 * half + 1], a2, a3, b2, b3, pf[nt][0], pf[nt][1]);
-          }
-        }
-      }
+      if (Z::QSMEM) __syncwarp();
     }
+    issue(copy);
 
-    if (h.flags & kQ4Last) {
-      // ---- the four warps' sums of this piece become one
+    const int valid = end - tok;
+    if (valid > 0) {
+      // ---- scores of tokens g, g + 8 (of each tile) and columns 2t, 2t + 1
+      constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+      const int r = lane & 15, c1 = lane >> 4;
+      float x[TT][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int h = 0; h < TT; ++h) {
+        const uint32_t krow = stage_u32 + Z::KEYS + 16 * RB * h;
+        float y[NT][4];
+        float2 ka[NG], kb[NG];  // scales of tokens g and g + 8
+        load_scales<NG>(stage + Z::KSC + (16 * h + g) * NG * 4, ka);
+        load_scales<NG>(stage + Z::KSC + (16 * h + g + 8) * NG * 4, kb);
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
+        for (int gr = 0; gr < NG; ++gr) {
+          uint32_t w0, w1, w2, w3;  // rows g and g + 8, pieces 2 gr and 2 gr + 1
+          ldsm_x4(krow + (uint32_t)Z::at(r, 2 * gr + c1), w0, w1, w2, w3);
+          float acc[NT][4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t a = c ? w2 : w0, b = c ? w3 : w1, a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              sa[nt][gr][e] += __shfl_xor_sync(0xffffffffu, sa[nt][gr][e], d);
-              sb[nt][gr][e] += __shfl_xor_sync(0xffffffffu, sb[nt][gr][e], d);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint4 q;
+              if constexpr (Z::QSMEM)
+                q = qbuf[(nt * CPR + 2 * gr + c) * 32 + lane];
+              else
+                q = qf[nt][2 * gr + c];
+              if (c == 0)
+                mma_first(acc[nt], a & kLow, b & kLow, a8 & kLow, b8 & kLow, q.x, q.y);
+              else
+                MmaOp<__half>::run(acc[nt], a & kLow, b & kLow, a8 & kLow, b8 & kLow, q.x, q.y);
+              MmaOp<__half>::run(acc[nt], a & kHigh, b & kHigh, a8 & kHigh, b8 & kHigh, q.z, q.w);
             }
-        if (g == 0) {
-          s_m[warp][nt * 8 + 2 * t] = m[nt][0];
-          s_m[warp][nt * 8 + 2 * t + 1] = m[nt][1];
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float f[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = nt * 8 + 2 * t + e;
-          const float top = fmaxf(fmaxf(s_m[0][c], s_m[1][c]), fmaxf(s_m[2][c], s_m[3][c]));
-          f[e] = m[nt][e] == -CUDART_INF_F ? 0.f : exp2f(m[nt][e] - top);
-          if (g == 0) {
-            if (warp == 0) s_top[c] = top;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) s_sum[warp][c][gr] = make_float2(sa[nt][gr][e] * f[e], sb[nt][gr][e] * f[e]);
           }
-        }
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          o[nt][i][0] *= f[0], o[nt][i][1] *= f[1];
-          o[nt][i][2] *= f[0], o[nt][i][3] *= f[1];
-        }
-      }
-      // warps 2 and 3 put theirs down, 0 and 1 add their own on top
-      float *ob = obuf + (warp & 1) * (GM * Z::OROW);
-#pragma unroll
-      for (int turn = 0; turn < 2; ++turn) {
-        if ((warp >> 1) != turn) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                // rows 64 gr + 8 g + 0 .. 7 of column 8 nt + 2 t + e
-                float4 *dst = reinterpret_cast<float4 *>(ob + (nt * 8 + 2 * t + e) * Z::OROW + 64 * gr + 8 * g);
-                float4 a = make_float4(o[nt][4 * gr][e], o[nt][4 * gr][e + 2], o[nt][4 * gr + 1][e], o[nt][4 * gr + 1][e + 2]);
-                float4 b = make_float4(o[nt][4 * gr + 2][e], o[nt][4 * gr + 2][e + 2], o[nt][4 * gr + 3][e], o[nt][4 * gr + 3][e + 2]);
-                if (turn == 1) {
-                  const float4 c = dst[0], d = dst[1];
-                  a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-                  b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
-                }
-                dst[0] = a;
-                dst[1] = b;
-              }
+            for (int i = 0; i < 4; ++i) {
+              const float2 z = i < 2 ? ka[gr] : kb[gr];
+              y[nt][i] = gr ? fmaf(z.y, acc[nt][i], y[nt][i]) : z.y * acc[nt][i];
+              x[h][nt][i] = gr ? fmaf(z.x, qsum[nt][gr][i & 1], x[h][nt][i]) : z.x * qsum[nt][gr][i & 1];
+            }
         }
-        __syncthreads();
-      }
-      // rows out, a warp a row, a lane four columns of every 128
-      for (int c = warp; c < h.rows; c += kQ4Warps) {
-        const float top = s_top[c];
-        const float s0 = (s_sum[0][c][0].x + s_sum[1][c][0].x) + (s_sum[2][c][0].x + s_sum[3][c][0].x);
-        const size_t place = (2 * (size_t)me + (h.dest == kQ4Place1 ? 1 : 0)) * 16 + c;
-        if (h.dest != kQ4Whole && lane == 0) space.ml[place] = make_float2(top, s0);
 #pragma unroll
-        for (int d = lane * 4; d < D; d += 128) {
-          const int gr = d >> 6;
-          const float a = (s_sum[0][c][gr].x + s_sum[1][c][gr].x) + (s_sum[2][c][gr].x + s_sum[3][c][gr].x);
-          const float b = (s_sum[0][c][gr].y + s_sum[1][c][gr].y) + (s_sum[2][c][gr].y + s_sum[3][c][gr].y);
-          const float4 u = *reinterpret_cast<const float4 *>(obuf + c * Z::OROW + d);
-          const float4 v = *reinterpret_cast<const float4 *>(obuf + (GM + c) * Z::OROW + d);
-          // (groups round their weights apart: a piece's outputs take its first
-          // group's sum as theirs)
-          const float inv = a > 0.f ? (h.dest == kQ4Whole ? 1.f / a : s0 / a) : (a == 0.f ? 0.f : a);
-          const float r0 = (u.x + v.x + b) * inv, r1 = (u.y + v.y + b) * inv;
-          const float r2 = (u.z + v.z + b) * inv, r3 = (u.w + v.w + b) * inv;
-          if (h.dest == kQ4Whole) {
-            const size_t row = (size_t)(h.row0 + c / p.group) * p.num_heads + (size_t)(h.kvh * p.group + c % p.group);
-            store4(static_cast<T *>(p.out) + row * D + d, r0, r1, r2, r3);
-          } else {
-            *reinterpret_cast<float4 *>(space.o + place * D + d) = make_float4(r0, r1, r2, r3);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[h][nt][i] = fmaf(qmul[nt][i & 1], y[nt][i], x[h][nt][i]);
+      }
+      // ---- values' scales of tokens g and g + 8, and the larger steps S
+      float2 va[TT][NG], vb[TT][NG];
+      float inv_a[TT], inv_b[TT];
+      bool raise = false;
+#pragma unroll
+      for (int h = 0; h < TT; ++h) {
+        load_scales<NG>(stage + Z::VSC + (16 * h + g) * NG * 4, va[h]);
+        load_scales<NG>(stage + Z::VSC + (16 * h + g + 8) * NG * 4, vb[h]);
+        float top_a = kQ4LeastStep, top_b = kQ4LeastStep;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) top_a = fmaxf(top_a, va[h][gr].y), top_b = fmaxf(top_b, vb[h][gr].y);
+        const float lg_a = log2f_fast(top_a), lg_b = log2f_fast(top_b);
+        inv_a[h] = rcp(top_a), inv_b[h] = rcp(top_b);
+        // the running maximum is raised when x + log2 S is 8 above it: any
+        // reference serves the sums as long as nothing overflows
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          x[h][nt][0] += lg_a, x[h][nt][1] += lg_a, x[h][nt][2] += lg_b, x[h][nt][3] += lg_b;
+          if (valid < Z::TOKENS) {
+            if (16 * h + g >= valid) x[h][nt][0] = x[h][nt][1] = -CUDART_INF_F;
+            if (16 * h + g + 8 >= valid) x[h][nt][2] = x[h][nt][3] = -CUDART_INF_F;
+          }
+          if (CHUNK) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (tok + 16 * h + g + 4 * (i & 2) >= lim[nt][i & 1]) x[h][nt][i] = -CUDART_INF_F;
+          }
+          raise = raise || fmaxf(x[h][nt][0], x[h][nt][2]) > m[nt][0] + kQ4Margin ||
+                  fmaxf(x[h][nt][1], x[h][nt][3]) > m[nt][1] + kQ4Margin;
+        }
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = m[nt][i];
+#pragma unroll
+            for (int h = 0; h < TT; ++h) top = fmaxf(top, fmaxf(x[h][nt][i], x[h][nt][i + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float f = ex2f(m[nt][i] - top);
+            m[nt][i] = top;
+#pragma unroll
+            for (int c = 0; c < 2 * CPR; ++c) o[nt][c][i] *= f, o[nt][c][i + 2] *= f;
+            sl[nt][i] *= f;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) sb[nt][gr][i] *= f;
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < TT; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[h][nt][i] = ex2f(x[h][nt][i] - m[nt][i & 1]);
+          sl[nt][0] = fmaf(x[h][nt][0], inv_a[h], fmaf(x[h][nt][2], inv_b[h], sl[nt][0]));
+          sl[nt][1] = fmaf(x[h][nt][1], inv_a[h], fmaf(x[h][nt][3], inv_b[h], sl[nt][1]));
+        }
+      // ---- O^T += V^T P^T, group by group
+#pragma unroll
+      for (int h = 0; h < TT; ++h) {
+        const uint32_t vrow = stage_u32 + Z::VALUES + 16 * RB * h;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const float la = va[h][gr].x * inv_a[h], lb = vb[h][gr].x * inv_b[h];
+          const float wa = va[h][gr].y * inv_a[h], wb = vb[h][gr].y * inv_b[h];
+          uint32_t pf[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float *y = x[h][nt];
+            sb[nt][gr][0] = fmaf(y[0], la, fmaf(y[2], lb, sb[nt][gr][0]));
+            sb[nt][gr][1] = fmaf(y[1], la, fmaf(y[3], lb, sb[nt][gr][1]));
+            pf[nt][0] = movmatrix_trans(MmaOp<__half>::pack(y[0] * wa, y[1] * wa));
+            pf[nt][1] = movmatrix_trans(MmaOp<__half>::pack(y[2] * wb, y[3] * wb));
+          }
+          // units of four codes: tokens 2t, 2t + 1 | the eight behind, pieces 2 gr, 2 gr + 1
+          uint32_t w[4];
+          ldsm_x4_trans(vrow + (uint32_t)Z::at(r, 2 * gr + c1), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t a = w[2 * c], b = w[2 * c + 1], a8 = a >> 8, b8 = b >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              // codes 0 and 2 of a unit (2^-24 each), then 1 and 3 (2^-20)
+              MmaOp<__half>::run(o[nt][2 * (2 * gr + c)], a & kLow, a8 & kLow, b & kLow, b8 & kLow, pf[nt][0], pf[nt][1]);
+              MmaOp<__half>::run(o[nt][2 * (2 * gr + c) + 1], a & kHigh, a8 & kHigh, b & kHigh, b8 & kHigh, pf[nt][0],
+                                 pf[nt][1]);
+            }
           }
         }
       }
     }
+
+    tok += Z::TOKENS;
+    if (--left == 0) {
+      // ---- the piece's sums: out, or into its place
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            sl[nt][e2] += __shfl_xor_sync(0xffffffffu, sl[nt][e2], d);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) sb[nt][gr][e2] += __shfl_xor_sync(0xffffffffu, sb[nt][gr][e2], d);
+          }
+          const int c = nt * 8 + 2 * t + e2;
+          if (c < rows) {
+            const float inv = dest != kQ4Whole ? 1.f : sl[nt][e2] == 0.f ? 0.f : 1.f / sl[nt][e2];
+            const float fa = inv * 0x1p24f, fb = inv * 0x1p20f;
+            const size_t place = (2 * (size_t)at_share + (dest == kQ4Place1 ? 1 : 0)) * GM + c;
+            if (dest != kQ4Whole && g == 0) space.ml[place] = make_float2(m[nt][e2], sl[nt][e2]);
+            T *out = static_cast<T *>(p.out) + query_row(row0, kvh, c) * D + 4 * g;
+            float *part = space.o + place * D + 4 * g;
+#pragma unroll
+            for (int ch = 0; ch < CPR; ++ch) {
+              // rows 32 ch + 4 g + 0 .. 3
+              const float b = sb[nt][ch >> 1][e2] * inv;
+              const float r0 = fmaf(o[nt][2 * ch][e2], fa, b), r1 = fmaf(o[nt][2 * ch + 1][e2], fb, b);
+              const float r2 = fmaf(o[nt][2 * ch][e2 + 2], fa, b), r3 = fmaf(o[nt][2 * ch + 1][e2 + 2], fb, b);
+              if (dest == kQ4Whole)
+                store4(out + 32 * ch, r0, r1, r2, r3);
+              else
+                store4(part + 32 * ch, r0, r1, r2, r3);
+            }
+          }
+        }
+    }
   }
-  if (!joined && threadIdx.x == 0) space.join[me].parts = 0;
+  // outputs of empty sequences
+  if (!CHUNK)
+    for (int q = blockIdx.x; q < p.num_seqs; q += gridDim.x)
+      if (share_seq(batch, s_scan, q).len == 0) {
+        uint4 *z = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (size_t)q * p.num_heads * D);
+        for (int i = threadIdx.x; i < p.num_heads * D / 8; i += kQ4Threads) z[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
   pdl_launch_dependents();
 }
 
@@ -616,7 +668,7 @@ extern "C" {
 
 size_t pa_q4_workspace_bytes(int head_size) {
   if (head_size != 64 && head_size != 128 && head_size != 256) return 0;
-  return pa::share_bytes(16, head_size, nullptr, nullptr);
+  return pa::share_bytes(pa::kQ4Shares, 16, head_size, nullptr, nullptr);
 }
 
 pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache, const void *value_cache,
@@ -676,23 +728,21 @@ pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache, c
   if (st != PA_OK) return st;
   const Q4Kernel k = dtype == PA_DTYPE_BF16 ? q4_pick<__nv_bfloat16>(head_size, nt, q_start != nullptr)
                                             : q4_pick<__half>(head_size, nt, q_start != nullptr);
-  st = host_ensure_smem(k.fn, k.smem);
+  st = host_ensure_smem(k.fn, (size_t)k.smem + 16 * 1024);  // (the kernel's static part counts against the same limit)
   if (st != PA_OK) return st;
-  const int ctas = sms * k.ctas < kShareMaxCtas ? sms * k.ctas : kShareMaxCtas;
+  const int ctas = sms * k.ctas < kQ4MaxCtas ? sms * k.ctas : kQ4MaxCtas;
   ShareSpace space;
-  share_bytes(16, head_size, workspace, &space);
+  share_bytes(kQ4Shares, 16, head_size, workspace, &space);
   void *args[2] = {&p, &space};
   st = host_launch(k.fn, (unsigned)ctas, 1, kQ4Threads, k.smem, stream, args, "launch 4-bit attention kernel");
   if (st != PA_OK) return st;
   JoinParams j{};
   j.space = space;
   j.out = out;
-  j.ctas = ctas;
-  j.place_step = 1;
-  j.max_rows = 16;
+  j.max_rows = 8 * nt;
   j.width = head_size;
   void *jargs[1] = {&j};
-  return host_launch(share_join_kernel(dtype == PA_DTYPE_BF16), (unsigned)(2 * sms), 1, kJoinThreads, 0, stream,
+  return host_launch(share_join_kernel(dtype == PA_DTYPE_BF16), (unsigned)(kJoinCtas * sms), 1, kJoinThreads, 0, stream,
                      jargs, "launch join kernel");
 }
 

@@ -1,16 +1,18 @@
-// Attention split into equal shares of work: every CTA (or pair of CTAs) of a
-// grid that fits the GPU takes the same number of steps of 64 keys, one after
-// another through the batch's units, and a second kernel joins the units that
-// ended up in several shares.
+// Attention cut into shares of work: each worker (a warp, a CTA) of a grid that
+// fills the GPU once takes shares of the batch's keys, in steps, one after
+// another, and a second kernel joins the units that ended up in several shares.
 //
 // A unit is what one item of rows reads: a sequence's keys, for one KV head
 // and one group of query rows.  The steps of all units stand in one line, unit
-// behind unit; share w of W is steps [w T / W, (w + 1) T / W) of the T.  So
-// each share's work is equal to a step whatever the lengths are, a share has
-// at most two units that it does not hold whole (its first and its last), and
-// the space for partial results is two places a share, whatever the batch.
-// Every CTA works its share out of the lengths by itself: a scan over the
-// sequences, which all CTAs do at once, instead of a launch that would plan.
+// behind unit, and a share is a stretch of the line, whatever units it cuts.
+// Every worker has a large share first, all equal; the rest of the line is cut
+// into small ones that the workers take from a counter as they get done, since
+// SMs do not run alike (with equal shares alone, CTAs of the same work ended
+// between 50 and 76 us).  A share has at most two units that it does not hold
+// whole, its first and its last, so the space for partial results is two
+// places a share, whatever the batch.  Every CTA works the shares out of the
+// lengths by itself: a scan over the sequences, which all CTAs do at once,
+// instead of a launch that would plan.
 #pragma once
 
 #include <math_constants.h>
@@ -19,39 +21,85 @@
 
 namespace pa {
 
-constexpr int kShareStep = 64;         // keys of a step
-constexpr int kShareMaxCtas = 8 * 152; // places for partial results in a workspace
+// A workspace, behind its status block: the units to join, then the places'
+// (maximum, sum) a row and their unnormalised outputs; 256-byte aligned each.
+// Ints of the status block: shares taken, units to join of few and of many
+// pieces, join CTAs done.
+constexpr int kShareTaken = 16, kShareFew = 17, kShareMany = 18, kShareDone = 19;
+constexpr int kJoinFew = 32; // pieces that one warp joins by itself
 
-// What a CTA leaves for the join of the unit that its share ends inside of:
-// parts pieces (its own place 1, then place 0 of the next shares), each of
-// `rows` rows.  Row r goes to out row out_row + (r / group) * stride + r % group.
+// A unit whose keys lie in several shares: parts pieces (place 1 of `share`,
+// then place 0 of the next shares, `by` apart), each of `rows` rows.  Row r
+// goes to out row out_row + (r / group) * stride + r % group.
 struct ShareJoin {
-  int parts;  // 0: nothing to join
-  int rows;
+  int share, parts, by, rows;
   int group, stride;
   long long out_row;
-  int pad[2];
 };
 
-// Layout of a workspace: the status block, the ShareJoins, the pieces' (maximum,
-// sum) a row, their unnormalised outputs; 256-byte aligned each.
 struct ShareSpace {
-  ShareJoin *join;  // [ctas]
-  float2 *ml;       // [ctas][2][rows]: maximum (log2 units), sum of exp2(x - maximum)
-  float *o;         // [ctas][2][rows][width]: sum of exp2(x - maximum) v
+  ShareJoin *join;  // [shares]: units of few pieces from the front, of many from the back
+  float2 *ml;       // [shares][2][rows]: maximum (log2 units), sum of exp2(x - maximum)
+  float *o;         // [shares][2][rows][width]: sum of exp2(x - maximum) v
+  int *counters;    // the status block
+  int shares;
 };
-__host__ inline size_t share_bytes(int rows, int width, void *base, ShareSpace *s) {
-  const size_t joins = (size_t)kShareMaxCtas * sizeof(ShareJoin);
-  const size_t ml = (size_t)kShareMaxCtas * 2 * rows * sizeof(float2);
-  const size_t o = (size_t)kShareMaxCtas * 2 * rows * width * sizeof(float);
-  size_t at = kStatusBytes;
+// (shares: a multiple of 64)
+inline size_t share_bytes(int shares, int rows, int width, void *base, ShareSpace *s) {
+  const size_t joins = (size_t)shares * sizeof(ShareJoin);
+  const size_t ml = (size_t)shares * 2 * rows * sizeof(float2);
+  const size_t o = (size_t)shares * 2 * rows * width * sizeof(float);
   if (s) {
-    s->join = reinterpret_cast<ShareJoin *>(static_cast<char *>(base) + at);
-    s->ml = reinterpret_cast<float2 *>(static_cast<char *>(base) + at + joins);
-    s->o = reinterpret_cast<float *>(static_cast<char *>(base) + at + joins + ml);
+    char *at = static_cast<char *>(base) + kStatusBytes;
+    s->join = reinterpret_cast<ShareJoin *>(at);
+    s->ml = reinterpret_cast<float2 *>(at + joins);
+    s->o = reinterpret_cast<float *>(at + joins + ml);
+    s->counters = static_cast<int *>(base);
+    s->shares = shares;
   }
-  return at + joins + ml + o;  // (each a multiple of 256: kShareMaxCtas is one of 64)
+  return kStatusBytes + joins + ml + o;
 }
+
+// a / b of numbers >= 0, in 32 bits where they fit (a tenth of the instructions)
+__device__ __forceinline__ long long div_steps(long long a, long long b) {
+  return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The shares of a line of `total` steps: `big` equal ones over its first
+// big_total steps, `small` equal ones over the rest.
+constexpr int kShareSmall = 1;     // small shares for each large one,
+constexpr int kShareSmallPct = 25; // over this much of the line,
+constexpr int kShareTwo = 8;       // where there are this many steps a worker
+constexpr int kShareLeast = 2;     // steps of a share where there are not enough for all
+struct SharePlan {
+  long long total, big_total;
+  int big, small;
+  __device__ __forceinline__ void make(long long steps, int workers) {
+    total = big_total = steps;
+    const long long most = (steps + kShareLeast - 1) / kShareLeast;
+    big = most < workers ? (int)most : workers;
+    small = 0;
+    if (steps >= (long long)workers * kShareTwo) {
+      small = kShareSmall * workers;
+      big_total = div_steps(steps, 100) * (100 - kShareSmallPct);
+    }
+  }
+  // the first step of share i
+  __device__ __forceinline__ long long begin(int i) const {
+    if (i >= big + small) return total;
+    if (i < big) return div_steps(big_total * i, big);
+    return big_total + div_steps((total - big_total) * (i - big), small);
+  }
+  // the share that step x (< total) is in
+  __device__ __forceinline__ int of(long long x) const {
+    int i = x < big_total ? (int)div_steps(x * big, big_total)
+                          : big + (int)div_steps((x - big_total) * small, total - big_total);
+    i = min(i, big + small - 1);
+    while (i > 0 && begin(i) > x) --i;
+    while (begin(i + 1) <= x) ++i;
+    return i;
+  }
+};
 
 // A sequence as the plan sees it.
 struct ShareSeq {
@@ -62,34 +110,40 @@ struct ShareSeq {
   int steps;  // of a unit
 };
 
-// The batch's side of the plan: Batch has seq(s), a ShareSeq with units and
-// steps set, and num_seqs.
-template <int THREADS>
+// The batch's side of the plan: Batch has num_seqs; read(s), a sequence's
+// (len, row0, n), checked, n < 0 if it is bad; seq(int4), the ShareSeq of it.
+template <int THREADS_, int CACHE_>
 struct ShareScan {
+  static constexpr int THREADS = THREADS_, CACHE = CACHE_;  // CACHE: sequences kept in shared memory
   long long cum[THREADS + 1];  // steps before each thread's sequences
   long long warp_sum[THREADS / 32];
+  int4 cache[CACHE];
 };
 
-__device__ __forceinline__ long long shfl_up64(long long v, int d) {
-  return __shfl_up_sync(0xffffffffu, v, d);
+template <class Scan, class Batch>
+__device__ __forceinline__ ShareSeq share_seq(const Batch &b, const Scan &scan, int s) {
+  return b.seq(b.num_seqs <= Scan::CACHE ? scan.cache[s] : b.read(s));
 }
 
 // By THREADS threads (the first of the CTA), with all of the CTA's threads at
-// the barriers: fills scan.cum.
-template <int THREADS, class Batch>
-__device__ __forceinline__ void share_scan(const Batch &b, ShareScan<THREADS> &scan) {
+// the barriers: fills the scan.
+template <class Scan, class Batch>
+__device__ __forceinline__ void share_scan(const Batch &b, Scan &scan) {
+  constexpr int THREADS = Scan::THREADS;
   const int t = threadIdx.x, per = (b.num_seqs + THREADS - 1) / THREADS;
   long long own = 0;
   if (t < THREADS) {
     for (int s = t * per; s < min(b.num_seqs, (t + 1) * per); ++s) {
-      const ShareSeq q = b.seq(s);
+      const int4 r = b.read(s);
+      if (b.num_seqs <= Scan::CACHE) scan.cache[s] = r;
+      const ShareSeq q = b.seq(r);
       own += (long long)q.units * q.steps;
     }
   }
   long long incl = own;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = shfl_up64(incl, d);
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
     if ((t & 31) >= d) incl += o;
   }
   if (t < THREADS && (t & 31) == 31) scan.warp_sum[t >> 5] = incl;
@@ -103,36 +157,19 @@ __device__ __forceinline__ void share_scan(const Batch &b, ShareScan<THREADS> &s
   __syncthreads();
 }
 
-// Share w of W of T steps: its first step.
-__device__ __forceinline__ long long share_begin(long long T, int w, int W) { return T * w / W; }
-
-// The share that step x (< T) is in.
-__device__ __forceinline__ int share_of(long long T, long long x, int W) {
-  int w = (int)min((long long)W - 1, x * W / T);
-  while (w > 0 && share_begin(T, w, W) > x) --w;
-  while (w < W - 1 && share_begin(T, w + 1, W) <= x) ++w;
-  return w;
-}
-
-// The shares of a plan: no more than there are, and none with less than `least`
-// steps where there could be fewer.
-__device__ __forceinline__ int share_count(long long T, int most, int least) {
-  const long long w = (T + least - 1) / least;
-  return w < 1 ? 1 : w < most ? (int)w : most;
-}
-
-// A walk over the pieces of units in steps [at, end) of the line.
+// A walk over the pieces of units in a share.
 struct ShareWalk {
+  long long line;  // where the walk is
   long long left;  // steps of the share from here on
   int s;           // sequence
   ShareSeq q;
   int unit, step;  // of the sequence, of the unit
 
-  template <int THREADS, class Batch>
-  __device__ __forceinline__ void begin(const Batch &b, const ShareScan<THREADS> &scan, long long at,
-                                        long long end) {
+  template <class Scan, class Batch>
+  __device__ __forceinline__ void begin(const Batch &b, const Scan &scan, long long at, long long end) {
+    constexpr int THREADS = Scan::THREADS;
+    line = at;
     left = end - at;
-    s = b.num_seqs;
     if (left <= 0) return;
     int lo = 0, hi = THREADS - 1;  // the last thread whose sequences start at or before it
     while (lo < hi) {
@@ -146,7 +183,7 @@ struct ShareWalk {
     long long x = at - scan.cum[lo];
     s = lo * per;
     while (true) {
-      q = b.seq(s);
+      q = share_seq(b, scan, s);
       const long long n = (long long)q.units * q.steps;
       if (x < n) break;
       x -= n;
@@ -155,7 +192,7 @@ struct ShareWalk {
         return;
       }
     }
-    unit = (int)(x / q.steps);
+    unit = (int)div_steps(x, q.steps);
     step = (int)(x - (long long)unit * q.steps);
   }
   // steps of this piece
@@ -163,9 +200,10 @@ struct ShareWalk {
     return (int)min(left, (long long)(q.steps - step));
   }
   // on to the next piece
-  template <class Batch>
-  __device__ __forceinline__ void next(const Batch &b) {
+  template <class Scan, class Batch>
+  __device__ __forceinline__ void next(const Batch &b, const Scan &scan) {
     const int n = piece();
+    line += n;
     left -= n;
     step += n;
     if (left <= 0 || step < q.steps) return;
@@ -177,25 +215,28 @@ struct ShareWalk {
         left = 0;
         return;
       }
-      q = b.seq(s);
+      q = share_seq(b, scan, s);
     } while (q.units == 0);
   }
 };
 
+// Notes a unit to join (by one thread).
+__device__ __forceinline__ void share_join(const ShareSpace &space, const ShareJoin &j) {
+  if (j.parts <= kJoinFew)
+    space.join[atomicAdd(space.counters + kShareFew, 1)] = j;
+  else
+    space.join[space.shares - 1 - atomicAdd(space.counters + kShareMany, 1)] = j;
+}
+
 // Joins the units that lie in several shares:
 //   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k,  M = max_k m_k
-// over the pieces k in their order.  A unit of few pieces is a warp's work a
-// row and 128 columns; one of many pieces is a CTA's, whose warps take pieces
-// in turn.
+// over the pieces k in their order.
 struct JoinParams {
   ShareSpace space;
-  void *out;       // [..][width], rows as the ShareJoins say
-  int ctas;        // of the attention kernel
-  int place_step;  // CTAs between a unit's pieces (2: pairs take a unit each)
+  void *out;  // [..][width], rows as the ShareJoins say
   int max_rows, width;
 };
-
 const void *share_join_kernel(int dtype_bf16);
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinCtas = 3;  // CTAs: an SM's
 
 }  // namespace pa
