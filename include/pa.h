@@ -608,6 +608,73 @@ pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache,
 /* Bytes of workspace for pa_q4_forward, any batch (0 on a bad head size). */
 size_t pa_q4_workspace_bytes(int head_size);
 
+/* Append to a paged cache of shared latents.  A token's row is [latent_dim |
+ * rope_dim]: the latent vector that the keys and values of every head are
+ * projections of, and one key part that carries the position, shared by all
+ * heads.
+ *
+ *   cache        [num_blocks][block_size][latent_dim + rope_dim]
+ *   latent       [num_rows][latent_dim], rows latent_stride elements apart
+ *   rope_key     [num_rows][rope_dim], rows rope_key_stride apart (both may be
+ *                slices of one projection's output)
+ *   norm_weight  [latent_dim] or NULL (the latent is stored as it is): the
+ *                latent is x * (mean(x^2) + eps)^-1/2 * norm_weight
+ *   query_rope   [num_rows][num_heads][rope_dim] or NULL, heads
+ *                query_head_stride and rows query_stride apart: the queries'
+ *                parts that carry the position; rotated into
+ *   query        [num_rows][num_heads][latent_dim + rope_dim], contiguous: the
+ *                last rope_dim elements of every head; the first latent_dim,
+ *                the queries through the keys' up-projection, are the caller's
+ *                and are not touched
+ *
+ * All of rope_dim turns, in pairs as interleaved says; everything in fp32 with
+ * one rounding to dtype.  cos_sin, positions, rows, q_start, seq_lens and bad
+ * data as in pa_append_kv; strides in multiples of 8, pointers 16-byte aligned;
+ * latent_dim 256 or 512, rope_dim 64, num_heads at most 128, block_size 8, 16,
+ * 32 or 64; bf16 and f16 (PA_ERR_UNSUPPORTED otherwise).  eps >= 0. */
+pa_status_t pa_latent_append(void *cache, void *query, const void *query_rope,
+                             const void *latent, const void *rope_key,
+                             const void *norm_weight, float eps,
+                             long long query_stride, long long query_head_stride,
+                             long long latent_stride, long long rope_key_stride,
+                             const float *cos_sin, const int32_t *positions,
+                             const int32_t *block_tables,
+                             const int32_t *seq_lens, const int32_t *q_start,
+                             int num_seqs, int num_rows, int num_heads,
+                             int latent_dim, int rope_dim, int num_blocks,
+                             int block_size, int max_blocks_per_seq,
+                             int max_seq_len, int interleaved, int max_position,
+                             int dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Decode attention over a cache of shared latents, in the absorbed form: with
+ * c_t and r_t the two parts of a token's row and q = [q_c | q_r] a head's query
+ * (q_c having gone through the keys' up-projection),
+ *   out[r][h] = sum_t softmax_t(scale (q_c . c_t + q_r . r_t)) c_t,
+ * a vector of latent_dim that the caller's value up-projection takes on.
+ *
+ *   query  [num_rows][num_heads][latent_dim + rope_dim]
+ *   out    [num_rows][num_heads][latent_dim]
+ * Rows as in pa_q4_forward: one a sequence (an empty sequence gets zeros), or
+ * chunks of a sequence's last tokens (rows behind the last chunk are left as
+ * they were).  Shares of the work, last bits, the workspace (of
+ * pa_latent_workspace_bytes(latent_dim) bytes, for any batch) and bad data as
+ * there; limits as in pa_latent_append, max_seq_len at most 2^30.  Keys that a
+ * row does not see because they are later tokens of its chunk must be finite.
+ * opts (or NULL): debug_flags (PA_DEBUG_STALL_CONSUMERS) and wait_limit_ns. */
+pa_status_t pa_latent_forward(void *out, const void *query, const void *cache,
+                              const int32_t *block_tables,
+                              const int32_t *seq_lens, const int32_t *q_start,
+                              int num_seqs, int num_rows, int num_heads,
+                              int latent_dim, int rope_dim, int num_blocks,
+                              int block_size, int max_blocks_per_seq,
+                              int max_seq_len, float scale, int dtype,
+                              void *workspace, size_t workspace_bytes,
+                              void *stream, const pa_options_t *opts);
+
+/* Bytes of workspace for pa_latent_forward, any batch (0 on a bad latent_dim). */
+size_t pa_latent_workspace_bytes(int latent_dim);
+
 /* Host heuristic: 1 if V2 should serve this batch on a GPU with sm_count
  * SMs, 0 for V1.  The pages switch on sequence length alone: the commit note
  * for computility-run.yaml (project_6, commit a2a5dd8) lists the decode path

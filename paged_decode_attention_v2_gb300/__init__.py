@@ -48,7 +48,8 @@ EXPORTS = ("pa_workspace_bytes", "pa_workspace_layout", "pa_workspace_init",
            "pa_chunks_forward", "pa_v2_partials", "pa_v2_combine", "pa_append_kv",
            "pa_select_blocks", "pa_sparse_forward", "pa_sparse_workspace_bytes",
            "pa_prefix_forward", "pa_prefix_workspace_bytes", "pa_q4_append", "pa_q4_forward",
-           "pa_q4_workspace_bytes")
+           "pa_q4_workspace_bytes", "pa_latent_append", "pa_latent_forward",
+           "pa_latent_workspace_bytes")
 
 
 class PAError(RuntimeError):
@@ -128,6 +129,14 @@ def load_library(path: str = LIB_PATH):
         lib.pa_sparse_forward.restype = ci
         lib.pa_sparse_forward.argtypes = ([vp] * 9 + [ci] * 12 + [ctypes.c_float, ci, ci, vp, cs,
                                                                   vp])
+        lib.pa_latent_workspace_bytes.restype = cs
+        lib.pa_latent_workspace_bytes.argtypes = [ci]
+        lib.pa_latent_append.restype = ci
+        lib.pa_latent_append.argtypes = ([vp] * 6 + [ctypes.c_float] + [ll] * 4 + [vp] * 5 +
+                                         [ci] * 12 + [vp, cs, vp])
+        lib.pa_latent_forward.restype = ci
+        lib.pa_latent_forward.argtypes = ([vp] * 6 + [ci] * 9 + [ctypes.c_float, ci, vp, cs, vp,
+                                                                 ctypes.POINTER(pa_options_t)])
         lib.pa_q4_workspace_bytes.restype = cs
         lib.pa_q4_workspace_bytes.argtypes = [ci]
         lib.pa_q4_append.restype = ci
@@ -686,6 +695,111 @@ def pa_q4_forward(out, query, key_cache, value_cache, key_scales, value_scales, 
         o, q, kc, vc, ks, vs, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks, int(max_seq_len),
         float(scale), _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
         _stream_handle(stream)), "pa_q4_forward")
+
+
+def pa_latent_workspace_bytes(latent_dim: int) -> int:
+    return int(load_library().pa_latent_workspace_bytes(latent_dim))
+
+
+def alloc_latent_workspace(latent_dim: int, device=None, stream=None) -> torch.Tensor:
+    """A zeroed workspace for pa_latent_forward calls of any batch."""
+    n = pa_latent_workspace_bytes(latent_dim)
+    if n == 0:
+        raise ValueError("bad latent_dim for a latent workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    pa_workspace_init(ws, stream)
+    return ws
+
+
+def _latent_part(t, like, width: int):
+    """(pointer, elements between rows, rows) of a [rows, width] tensor whose rows are
+    contiguous, of the dtype and on the device of `like`."""
+    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1 or t.dtype is not like.dtype \
+            or t.get_device() != like.get_device():
+        raise ValueError(f"expected [rows, {width}] of the cache's dtype and device, rows contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width, t.shape[0]
+
+
+def _latent_shapes(cache, block_tables, seq_lens, q_start):
+    nb, bs, width = cache.shape
+    B = seq_lens.numel()
+    if q_start is not None and q_start.numel() != B + 1:
+        raise ValueError("q_start must be int32 [num_seqs + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    return nb, bs, width, B
+
+
+def pa_latent_append(cache, latent, rope_key, block_tables, seq_lens, workspace, cos_sin,
+                     query=None, query_rope=None, norm_weight=None, eps=0.0, positions=None,
+                     q_start=None, interleaved=False, max_seq_len=None, stream=None) -> None:
+    """Append rows to a cache of shared latents [num_blocks, block_size, latent_dim +
+    rope_dim]: latent [rows, latent_dim], normalised with norm_weight and eps, and
+    rope_key [rows, rope_dim], rotated by cos_sin [max_position, rope_dim]; query_rope
+    [rows, H, rope_dim] (rows and heads may be strided) is rotated into the last
+    rope_dim elements of query [rows, H, latent_dim + rope_dim] (see include/pa.h)."""
+    if latent.dim() != 2:
+        raise ValueError("latent must be [rows, latent_dim]")
+    nb, bs, width, B = _latent_shapes(cache, block_tables, seq_lens, q_start)
+    ws, c, q, nw, bt, sl, qs, pos = _pointers(
+        cache, workspace, (cache, query, norm_weight), (block_tables, seq_lens, q_start, positions))
+    lat = latent.shape[1]
+    rope = width - lat
+    lp, lst, R = _latent_part(latent, cache, lat)
+    kp, kst, rows = _latent_part(rope_key, cache, rope)
+    if rows != R or (nw and norm_weight.numel() != lat):
+        raise ValueError("latent and rope_key (and norm_weight) differ in shape")
+    if pos and positions.numel() != R:
+        raise ValueError("positions must be int32 [rows]")
+    H, qp, qst, qhst = 1, 0, 0, 0
+    if (query is None) != (query_rope is None):
+        raise ValueError("query and query_rope go together")
+    if query is not None:
+        if query.dim() != 3 or query.shape[0] != R or query.shape[2] != width:
+            raise ValueError("query must be [rows, num_heads, latent_dim + rope_dim]")
+        H = query.shape[1]
+        if query_rope.shape != (R, H, rope) or query_rope.stride(2) != 1 \
+                or query_rope.dtype is not cache.dtype or query_rope.get_device() != cache.get_device():
+            raise ValueError("query_rope must be [rows, num_heads, rope_dim] of the cache's dtype and "
+                             "device, heads contiguous")
+        qp = query_rope.data_ptr()
+        qhst = query_rope.stride(1) if H > 1 else rope
+        qst = query_rope.stride(0) if R > 1 else (H - 1) * qhst + rope
+    cs, max_position, rotary = _angles(cos_sin, cache, None)
+    if rotary != rope:
+        raise ValueError("cos_sin must be float32 [max_position, rope_dim]")
+    blocks = block_tables.shape[1]
+    if max_seq_len is None:
+        max_seq_len = blocks * bs
+    _check((_lib or load_library()).pa_latent_append(
+        c, q, qp, lp, kp, nw, float(eps), qst, qhst, lst, kst, cs, pos, bt, sl, qs, B, R, H, lat,
+        rope, nb, bs, blocks, int(max_seq_len), int(interleaved), max_position,
+        _DTYPES[cache.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream)), "pa_latent_append")
+
+
+def pa_latent_forward(out, query, cache, block_tables, seq_lens, scale, workspace, q_start=None,
+                      max_seq_len=None, stream=None, debug_flags=0, wait_limit_ns=0) -> None:
+    """Decode attention over a cache of shared latents in the absorbed form: query
+    [rows, H, latent_dim + rope_dim], out [rows, H, latent_dim]; one row a sequence or,
+    with q_start, chunks of them as in pa_chunks_forward (see include/pa.h)."""
+    R, H, width = query.shape
+    nb, bs, W, B = _latent_shapes(cache, block_tables, seq_lens, q_start)
+    ws, o, q, c, bt, sl, qs = _pointers(query, workspace, (out, query, cache),
+                                        (block_tables, seq_lens, q_start))
+    if W != width or out.dim() != 3 or out.shape[:2] != (R, H) or out.shape[2] > width:
+        raise ValueError("query must be [rows, num_heads, latent_dim + rope_dim], out [rows, "
+                         "num_heads, latent_dim]")
+    lat = out.shape[2]
+    blocks = block_tables.shape[1]
+    if max_seq_len is None:
+        max_seq_len = blocks * bs
+    opts = ctypes.byref(pa_options_t(0, 0, 0, debug_flags, wait_limit_ns, None, 0, 0, 0)) \
+        if debug_flags or wait_limit_ns else None
+    _check((_lib or load_library()).pa_latent_forward(
+        o, q, c, bt, sl, qs, B, R, H, lat, width - lat, nb, bs, blocks, int(max_seq_len),
+        float(scale), _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
+        _stream_handle(stream), opts), "pa_latent_forward")
 
 
 def pa_host_staging_bytes(num_seqs: int, num_heads: int, head_size: int,

@@ -970,6 +970,34 @@ pa_status_t stage_in(const void *s0, void *d0, size_t b0, const void *s1, void *
 
 namespace pa {
 
+pa_status_t host_cache_map(CUtensorMap *map, const void *base, int dtype, int width, long long rows,
+                           int unit_rows) {
+  return encode_cache_map_umma(map, base, dtype, width, rows, unit_rows);
+}
+
+pa_status_t host_rows_map(CUtensorMap *map, const void *base, int dtype, int width, long long rows,
+                          int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  pa_status_t st = get_encoder(&enc);
+  if (st != PA_OK) return st;
+  const int elt = elt_size(dtype);
+  CUtensorMapDataType dt = dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  cuuint64_t gdim[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  cuuint64_t gstride[1] = {(cuuint64_t)width * elt};
+  cuuint32_t box[2] = {(cuuint32_t)(kPanelBytes / elt), (cuuint32_t)box_rows};
+  cuuint32_t estride[2] = {1, 1};
+  CUresult r = enc(map, dt, 2, const_cast<void *>(base), gdim, gstride, box, estride,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char msg[64];
+    snprintf(msg, sizeof msg, "CUresult %d", (int)r);
+    return fail_cuda("cuTensorMapEncodeTiled", msg);
+  }
+  return PA_OK;
+}
+
 pa_status_t host_fail_cuda(const char *what, cudaError_t e) { return fail_cuda(what, e); }
 
 pa_status_t host_sm_count(int *sms) {

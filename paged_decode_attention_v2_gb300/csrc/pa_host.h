@@ -2,6 +2,7 @@
 // (defined in pa_api.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -15,6 +16,16 @@ pa_status_t host_fail_cuda(const char *what, cudaError_t e);
 pa_status_t host_sm_count(int *sms);
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device).
 pa_status_t host_ensure_smem(const void *fn, size_t bytes);
+
+// TMA's view of rows of `width` 16-bit elements, eight at a time: boxes of
+// unit_rows rows (a multiple of 8) from row 8 y at (0, 0, 0, y), landing as
+// [8 rows][panel][row][128 bytes] in the 128-byte swizzle.
+pa_status_t host_cache_map(CUtensorMap *map, const void *base, int dtype, int width, long long rows,
+                           int unit_rows);
+// The same rows one panel at a time: boxes of box_rows rows by 64 elements from
+// (x, row), landing as [row][128 bytes]; zeros behind the last row.
+pa_status_t host_rows_map(CUtensorMap *map, const void *base, int dtype, int width, long long rows,
+                          int box_rows);
 
 inline bool host_aligned(const void *p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "pa.h"
+
 namespace pa {
 
 constexpr int kAppendMaxRows = 4;  // rows of a CTA
@@ -65,6 +67,23 @@ struct PrefixParams {
   float scale_log2;  // scale * log2(e)
   uint64_t wait_limit_ns;
 };
+
+// The rules that every call on a latent cache shares (no pointers).
+inline pa_status_t latent_check_cache(int dtype, int num_heads, int latent_dim, int rope_dim,
+                                      int num_blocks, int block_size, int max_blocks_per_seq,
+                                      int max_seq_len) {
+  if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16) return PA_ERR_INVALID_ARG;
+  if (num_heads < 1 || latent_dim < 1 || rope_dim < 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      max_seq_len < 0 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if ((long long)max_seq_len > (long long)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+  if (dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;  // tensor path only
+  if ((latent_dim != 256 && latent_dim != 512) || rope_dim != 64) return PA_ERR_UNSUPPORTED;
+  if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64) return PA_ERR_UNSUPPORTED;
+  if (num_heads > 128) return PA_ERR_UNSUPPORTED;
+  if ((long long)num_blocks * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
 
 struct PrefixKernelInfo {
   const void *fn;
