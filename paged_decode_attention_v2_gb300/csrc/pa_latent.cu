@@ -19,16 +19,18 @@
 // 128.  More rows a CTA do not fit: 64 rows of queries are 72 KB, a tile of 64
 // keys 72 KB, and two tiles have to be there for copies to run beside MMAs.
 //
-// A softmax thread holds two rows (of 64) by 16 keys in registers, as the MMA
-// fragments have it; a quad of threads has a row.  The maximum in use is raised
-// only when a score passes it by kLatentMargin (weights then stay far from
-// overflow, and in fp32 and bf16 their relative precision does not depend on
-// the reference): the four warps vote on it, as all of them hold part of every
-// row's O^T.
+// A softmax thread holds two rows (of 64) by 8 keys in registers, as the MMA
+// fragments have it; a quad of threads has half a row.  The maximum in use is
+// raised only when a score passes it by 2^8 (weights then stay far from
+// overflow, and their relative precision does not depend on the reference): the
+// warps vote on it, as all of them hold part of every row's O^T.
 //
-// Warps: 0-3 softmax and output, 4 producer (the walk over the shares, TMA), 5
-// MMA issuer.  One CTA an SM; work is cut in shares (pa_share.cuh), a CTA's
-// each; every wait is bounded.
+// Warps: 0-7 softmax and output (four lanes' quarters by two halves of a tile's
+// keys), 8 producer (the walk over the shares, TMA), 9 MMA issuer.  One CTA an
+// SM; work is cut in shares (pa_share.cuh), a CTA's each; every wait is bounded.
+// Loops that issue MMAs are rolled and stand once: an SM fetches code that it
+// has not run at some 250 cycles an MMA (the first tile took 13,000 cycles with
+// three unrolled copies).
 #include <limits.h>
 #include <math.h>
 #include <math_constants.h>
@@ -46,7 +48,8 @@ namespace {
 
 constexpr int kLatentRows = 64;   // query rows of a unit
 constexpr int kLatentKeys = 64;   // keys of a step
-constexpr int kLatentThreads = 192;
+constexpr int kLatentSoftmax = 8;  // warps
+constexpr int kLatentThreads = 32 * (kLatentSoftmax + 2);
 constexpr int kLatentMaxCtas = 152;
 constexpr int kLatentShares = 320;  // shares x groups of rows that a workspace has places for
 constexpr float kLatentNone = -3.402823466e38f;  // the maximum of no keys
@@ -93,9 +96,9 @@ struct LatentShared {
   uint8_t q[Z::QBYTES];
   uint8_t ring[Z::SLOTS][Z::SLOT];
   uint8_t p[Z::PBYTES];
-  float alpha[kLatentRows], inv[kLatentRows];  // a rescale's factors; a unit's maxima or normalisers
+  float part[2][kLatentRows];  // the two halves' maxima of a row (a rescale) or sums (a unit's end)
   LatentStage info[Z::SLOTS];
-  int vote[2][4];
+  int vote[2][kLatentSoftmax];
   uint64_t bars[Z::NBARS];
   int flags[2];
   uint32_t tmem;
@@ -133,11 +136,11 @@ struct LatentBatch {
   }
 };
 
-// 16 lanes by 64 columns of tensor memory, as MMA fragments: thread t has rows
+// 16 lanes by 32 columns of tensor memory, as MMA fragments: thread t has rows
 // t / 4 and t / 4 + 8, columns 8 j + 2 (t % 4) + {0, 1}: words 4 j + {0, 1} and + {2, 3}
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(taddr));
 }
 
@@ -174,22 +177,22 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 5);  // the O^T MMAs' commit and each softmax warp's header read
+      mbar_init(empty + 8 * i, kLatentSoftmax + 1);  // the O^T MMAs' commit and each softmax warp's header read
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(s_full, 1);
     mbar_init(s_full + 8, 1);
-    mbar_init(p_full, 4);
+    mbar_init(p_full, kLatentSoftmax);
     mbar_init(pv_done, 1);
     mbar_init(o_done, 1);
-    mbar_init(grp, 4);
+    mbar_init(grp, kLatentSoftmax);
     mbar_init(drain, 1);
     mbar_init(never, 1);
     sh.flags[0] = 0;
     fence_mbar_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kLatentSoftmax && lane == 0) {
     prefetch_tmap(&tmap_c);
     prefetch_tmap(&tmap_q);
   }
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   // in the stream before the tensor memory is taken and before any global
   // access.
   pdl_wait_primary();
-  if (warp == 5) {
+  if (warp == kLatentSoftmax + 1) {
     tmem_alloc(smem_u32(&sh.tmem), Z::TMEM);
     tmem_relinquish();
   }
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   tc_fence_after();
   const uint32_t tmem_o = sh.tmem, tmem_s = sh.tmem + 64 * Z::NT;
 
-  if (warp == 4) {
+  if (warp == kLatentSoftmax) {
     // ======================= producer warp =======================
     const int U = p.unit_rows;
     SharePlan plan;
@@ -344,100 +347,87 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, kDrainLimitNs, nullptr);
     }
     __syncwarp();
-  } else if (warp == 5) {
-    // ======================= MMA warp (one thread issues) =======================
-    if (lane == 0) {
-      bool ok = true;
-      int nq = 0;  // pieces whose queries S has taken
-      auto issue_s = [&](int sl, int b, int fl) {
-        const uint32_t kst = ring_u32 + (uint32_t)sl * Z::SLOT;
-#pragma unroll
-        for (int ks = 0; ks < 4 * NP; ++ks) {
-          const uint32_t off = (uint32_t)(ks & 3) * 32u;
-          const uint64_t da = smem_desc(q_u32 + (uint32_t)(ks >> 2) * 8192u + off, 16, 1024);
-          const uint64_t db = smem_desc(kst + (uint32_t)(ks >> 2) * 1024u + off, 16, Z::GROUP);
-          tc_mma(tmem_s + 64u * (uint32_t)b, da, db, kIdescS, ks > 0 ? 1u : 0u);
+  } else if (warp == kLatentSoftmax + 1) {
+    // ======================= MMA warp =======================
+    // The whole warp runs the loop, so that descriptors and control stay in
+    // uniform registers; one elected lane issues.
+    const uint32_t leader = elect_one();
+    bool ok = true;
+    int nq = 0;  // pieces whose queries S has taken
+    const uint64_t q_desc = smem_desc(q_u32, 16, 1024), k_desc = smem_desc(ring_u32, 16, Z::GROUP);
+    const uint64_t v_desc = smem_desc(ring_u32, 1024, Z::GROUP), p_desc = smem_desc(p_u32, 16, 1024);
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+      const bool w = mbar_wait(bar, parity, limit, flags);
+      ok = __all_sync(0xffffffffu, w);
+      return ok;
+    };
+    int issued = 0, fl = 0, fl_next = 0;  // tiles whose S is issued; the flags of tile i, of the last issued
+    for (int i = 0; ok; ++i) {
+      // S of this tile if it is not yet issued; then of the next, before O^T of
+      // this one, if its keys (and queries) are here
+      bool end = false;
+#pragma unroll 1
+      for (int a = issued - i; a < 2; ++a) {
+        const int sl = issued % NS;
+        const uint32_t bar = full + 8 * sl, par = (issued / NS) & 1;
+        if (a == 0 ? !wait(bar, par) : !__all_sync(0xffffffffu, mbar_test(bar, par))) break;
+        const int f = sh.info[sl].flags;
+        if (f & kLatentEnd) {
+          end = a == 0;
+          break;
         }
-        tc_commit(s_full + 8u * (uint32_t)b);
-        if (fl & kLatentLast) tc_commit(q_empty);
-      };
-      int fl = 0;
-      ok = mbar_wait(full, 0, limit, flags);
-      if (ok) fl = sh.info[0].flags;
-      bool more = ok && !(fl & kLatentEnd);
-      if (more) {
-        ok = mbar_wait(q_full, 0, limit, flags);
-        ++nq;
-        if (ok) {
-          tc_fence_after();
-          issue_s(0, 0, fl);
+        if (f & kLatentFirst) {
+          if (a == 0 ? !wait(q_full, nq & 1) : !__all_sync(0xffffffffu, mbar_test(q_full, nq & 1))) break;
+          ++nq;
         }
-        more = ok;
-      }
-      for (int i = 0; more; ++i) {
-        // S of the next tile before O^T of this one, if its keys (and queries) are here
-        const int sl = i % NS, sl1 = (i + 1) % NS;
-        const uint32_t par1 = ((i + 1) / NS) & 1;
-        bool ahead = false;
-        int fl1 = 0;
-        if (mbar_test(full + 8 * sl1, par1)) {
-          fl1 = sh.info[sl1].flags;
-          if (!(fl1 & kLatentEnd) && (!(fl1 & kLatentFirst) || mbar_test(q_full, nq & 1))) {
-            if (fl1 & kLatentFirst) ++nq;
-            tc_fence_after();
-            issue_s(sl1, (i + 1) & 1, fl1);
-            ahead = true;
-          }
-        }
-        ok = mbar_wait(p_full, i & 1, limit, flags);
-        if (!ok) break;
         tc_fence_after();
-        const uint32_t vst = ring_u32 + (uint32_t)sl * Z::SLOT;
+        const uint32_t d = tmem_s + 64u * (uint32_t)(issued & 1);
+        const uint64_t db = k_desc + (uint32_t)sl * (uint32_t)(Z::SLOT >> 4);
+#pragma unroll 1
+        for (int pn = 0; pn < NP; ++pn)
 #pragma unroll
-        for (int kk = 0; kk < kLatentKeys / 16; ++kk) {
-          const uint64_t db = smem_desc(p_u32 + (uint32_t)kk * 32u, 16, 1024);
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma_if(leader, d, q_desc + (uint32_t)(pn * 512 + ks * 2), db + (uint32_t)(pn * 64 + ks * 2), kIdescS,
+                      pn + ks > 0 ? 1u : 0u);
+        tc_commit_if(leader, s_full + 8u * (uint32_t)(issued & 1));
+        if (f & kLatentLast) tc_commit_if(leader, q_empty);
+        fl = a == 0 ? f : fl;
+        fl_next = f;
+        ++issued;
+      }
+      if (!ok || end) break;
+      if (!wait(p_full, i & 1)) break;
+      tc_fence_after();
+      const uint64_t da = v_desc + (uint32_t)(i % NS) * (uint32_t)(Z::SLOT >> 4);
+#pragma unroll 1
+      for (int kk = 0; kk < kLatentKeys / 16; ++kk)
 #pragma unroll
-          for (int j = 0; j < Z::NT; ++j) {
-            const uint64_t da = smem_desc(vst + (uint32_t)kk * 2u * Z::GROUP + (uint32_t)j * 2048u, 1024, Z::GROUP);
-            tc_mma(tmem_o + 64u * (uint32_t)j, da, db, kIdescO, ((fl & kLatentFirst) && kk == 0) ? 0u : 1u);
-          }
-        }
-        tc_commit(pv_done);
-        tc_commit(empty + 8 * sl);
-        if (fl & kLatentLast) tc_commit(o_done);
-        if (!ahead) {
-          ok = mbar_wait(full + 8 * sl1, par1, limit, flags);
-          if (!ok) break;
-          fl1 = sh.info[sl1].flags;
-          if (fl1 & kLatentEnd) break;
-          if (fl1 & kLatentFirst) {
-            ok = mbar_wait(q_full, nq & 1, limit, flags);
-            if (!ok) break;
-            ++nq;
-          }
-          tc_fence_after();
-          issue_s(sl1, (i + 1) & 1, fl1);
-        }
-        fl = fl1;
-      }
-      // nothing of this thread's may still run when the memory is freed
-      tc_commit(drain);
-      mbar_wait(drain, 0, kDrainLimitNs, nullptr);
-      if (!ok) {
-        report(p.status, kStatusTimeout);
-        flags[0] = 1;
-      }
+        for (int j = 0; j < Z::NT; ++j)
+          tc_mma_if(leader, tmem_o + 64u * (uint32_t)j, da + (uint32_t)(kk * (2 * Z::GROUP >> 4) + j * 128),
+                    p_desc + (uint32_t)(kk * 2), kIdescO, (fl & kLatentFirst) && kk == 0 ? 0u : 1u);
+      tc_commit_if(leader, pv_done);
+      tc_commit_if(leader, empty + 8 * (i % NS));
+      if (fl & kLatentLast) tc_commit_if(leader, o_done);
+      fl = fl_next;
+    }
+    // nothing may still run when the memory is freed
+    tc_commit_if(leader, drain);
+    mbar_wait(drain, 0, kDrainLimitNs, nullptr);
+    if (!ok && lane == 0) {
+      report(p.status, kStatusTimeout);
+      flags[0] = 1;
     }
     __syncwarp();
   } else {
     // ======================= softmax warps =======================
-    // thread: rows ra = 16 warp + lane / 4 and ra + 8, keys 8 j + 2 (lane % 4) + {0, 1}
-    const int t = threadIdx.x, q4 = lane & 3, ra = 16 * warp + (lane >> 2);
-    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+    // thread: rows ra = 16 quarter + lane / 4 and ra + 8, keys 32 half + 8 j + 2 (lane % 4) + {0, 1}
+    const int quarter = warp & 3, half = warp >> 2;
+    const int t = threadIdx.x, q4 = lane & 3, ra = 16 * quarter + (lane >> 2), key0 = 32 * half + 2 * q4;
+    const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     float m[2] = {kLatentNone, kLatentNone}, l[2] = {0.f, 0.f};
     int lim[2] = {0, 0}, pieces = 0, gx = 0;
     bool ok = true;
-    // a vote (or a meeting) of the four warps, after a bounded wait: their words, or'ed
+    // a vote (or a meeting) of the warps, after a bounded wait: their words, or'ed
     auto meet = [&](int v) -> int {
       __syncwarp();  // what its lanes wrote, or read of the last meeting, is done
       if (lane == 0) {
@@ -448,7 +438,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       ok = __all_sync(0xffffffffu, w);
       const volatile int *a = sh.vote[gx & 1];
       ++gx;
-      return a[0] | a[1] | a[2] | a[3];
+      int r = 0;
+#pragma unroll
+      for (int k = 0; k < kLatentSoftmax; ++k) r |= a[k];
+      return r;
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {
       const bool w = mbar_wait(bar, parity, limit, flags);
@@ -474,58 +467,73 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       }
       if (!wait(s_full + 8 * (i & 1), (i >> 1) & 1)) break;
       tc_fence_after();
-      uint32_t sr[32];
-      tmem_ld_frag(tmem_s + 64u * (uint32_t)(i & 1) + lane_off, sr);
-      tmem_ld_wait(sr);
-      float x[32];
+      uint32_t sr[16];
+      tmem_ld_frag(tmem_s + 64u * (uint32_t)(i & 1) + 32u * (uint32_t)half + lane_off, sr);
+      tmem_ld_wait16(sr);
+      float x[16];
       float top[2] = {kLatentNone, kLatentNone};
-      const bool masked = h.valid < kLatentKeys || h.tok0 + kLatentKeys > min(lim[0], lim[1]);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        x[k] = __uint_as_float(sr[k]) * p.scale_log2;
-        const int e = (k >> 1) & 1, key = 8 * (k >> 2) + 2 * q4 + (k & 1);
-        if (masked && (key >= h.valid || h.tok0 + key >= lim[e])) x[k] = -CUDART_INF_F;
-        top[e] = fmaxf(top[e], x[k]);
+      for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(sr[k]) * p.scale_log2;
+      if (h.valid < kLatentKeys || h.tok0 + kLatentKeys > min(lim[0], lim[1])) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int key = key0 + 8 * (k >> 2) + (k & 1);
+          if (key >= h.valid || h.tok0 + key >= lim[(k >> 1) & 1]) x[k] = -CUDART_INF_F;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        top[0] = fmax3(top[0], x[k], x[k + 1]);
+        top[1] = fmax3(top[1], x[k + 2], x[k + 3]);
       }
       const bool up = top[0] > m[0] + kMargin || top[1] > m[1] + kMargin;
       if (meet(__any_sync(0xffffffffu, up)) != 0 && ok) {
-        float al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(top[e], m[e]);
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          al[e] = ex2(m[e] - v);
-          m[e] = v;
-          l[e] *= al[e];
-          if (q4 == 0) sh.alpha[ra + 8 * e] = al[e];
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+          if (q4 == 0) sh.part[half][ra + 8 * e] = fmaxf(top[e], m[e]);
         }
+        meet(0);  // the maxima of both halves are there
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float v = fmaxf(sh.part[0][ra + 8 * e], sh.part[1][ra + 8 * e]);
+          const float al = ex2(m[e] - v);
+          m[e] = v;
+          l[e] *= al;
+          top[e] = al;
+        }
+        meet(0);  // (they are read)
+        if (!ok) break;
         if (!(h.flags & kLatentFirst)) {
-          meet(0);  // the factors of all rows are there
-          // O^T's lanes of this warp, once the MMAs of the tile before are done
+          if (half == 0 && q4 == 0) sh.part[0][ra] = top[0], sh.part[0][ra + 8] = top[1];
+          meet(0);  // the rows' factors are there
+          // O^T's lanes and half of its rows, once the MMAs of the tile before are done
           if (!ok || !wait(pv_done, (i - 1) & 1)) break;
           tc_fence_after();
+          const float *al = sh.part[0] + 32 * half;
 #pragma unroll 1
-          for (int c = 0; c < 2 * Z::NT; ++c) {
+          for (int j = 0; j < Z::NT; ++j) {
+            const uint32_t at = tmem_o + 64u * (uint32_t)j + 32u * (uint32_t)half + lane_off;
             uint32_t o[32];
-            tmem_ld32(tmem_o + 32u * c + lane_off, o);
+            tmem_ld32(at, o);
             tmem_ld_wait(o);
-            const float *al0 = sh.alpha + 32 * (c & 1);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al0[k]);
-            tmem_st32(tmem_o + 32u * c + lane_off, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k]);
+            tmem_st32(at, o);
           }
           tmem_st_wait();
           tc_fence_before();
-          meet(0);  // (before anyone writes factors again)
+          meet(0);  // (before anyone writes there again)
           if (!ok) break;
         }
       }
       if (!ok) break;
       // weights, rounded to the input type; the sums take them as rounded
-      uint32_t w[16];
+      uint32_t w[8];
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
+      for (int k = 0; k < 16; k += 2) {
         const int e = (k >> 1) & 1;
         w[k / 2] = MmaOp<T>::pack(ex2(x[k] - m[e]), ex2(x[k + 1] - m[e]));
         const float2 r = MmaOp<T>::unpack(w[k / 2]);
@@ -534,15 +542,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       // into P's tile, which the MMAs of the tile before have read
       if (i >= 1 && !wait(pv_done, (i - 1) & 1)) break;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int r = ra + 8 * (k & 1), c = k >> 1;  // row, 16-byte piece of eight keys
+      for (int k = 0; k < 8; ++k) {
+        const int r = ra + 8 * (k & 1), c = 4 * half + (k >> 1);  // row, 16-byte piece of eight keys
         *reinterpret_cast<uint32_t *>(sh.p + r * 128 + ((c ^ (r & 7)) << 4) + 4 * q4) = w[k];
       }
       // rows of keys that are not the item's may hold anything (0 x NaN would reach O^T)
       if (h.valid < kLatentKeys) {
         uint8_t *v = sh.ring[sl];
         constexpr int kPieces = LAT / 8;  // 16-byte pieces of a key's latent part
-        for (int e = t; e < (kLatentKeys - h.valid) * kPieces; e += 128) {
+        for (int e = t; e < (kLatentKeys - h.valid) * kPieces; e += 32 * kLatentSoftmax) {
           const int r = h.valid + e / kPieces, c = e % kPieces;
           *reinterpret_cast<uint4 *>(v + (r >> 3) * Z::GROUP + (c >> 3) * 1024 + (r & 7) * 128 +
                                      (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -557,38 +565,47 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         for (int e = 0; e < 2; ++e) {
           l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
           l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-          const int r = ra + 8 * e;
-          if (q4 == 0) {
-            sh.inv[r] = h.place >= 0 ? 1.f : l[e] == 0.f ? 0.f : 1.f / l[e];
-            if (h.place >= 0 && r < h.rows)
-              space.ml[(size_t)h.place * kLatentRows + r] = make_float2(m[e], l[e]);
-          }
+          if (q4 == 0) sh.part[half][ra + 8 * e] = l[e];
         }
-        meet(0);  // every row's normaliser is there
-        if (!ok || !wait(o_done, pieces & 1)) break;
+        meet(0);  // every row's sums are there
+        if (!ok) break;
+        if (h.place >= 0 && half == 0 && q4 == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (ra + 8 * e < h.rows)
+              space.ml[(size_t)h.place * kLatentRows + ra + 8 * e] =
+                  make_float2(m[e], sh.part[0][ra + 8 * e] + sh.part[1][ra + 8 * e]);
+        }
+        if (!wait(o_done, pieces & 1)) break;
         ++pieces;
         tc_fence_after();
+        const int r0 = 32 * half;
+        if (r0 < h.rows) {
+          float inv = sh.part[0][r0 + lane] + sh.part[1][r0 + lane];  // (lane: a row)
+          inv = inv == 0.f ? 0.f : 1.f / inv;
 #pragma unroll 1
-        for (int c = 0; c < 2 * Z::NT; ++c) {
-          const int r0 = 32 * (c & 1), d = 128 * (c >> 1) + t;
-          if (r0 >= h.rows) continue;
-          uint32_t o[32];
-          tmem_ld32(tmem_o + 32u * c + lane_off, o);
-          tmem_ld_wait(o);
-          if (h.place >= 0) {
-            float *dst = space.o + ((size_t)h.place * kLatentRows + r0) * LAT + d;
+          for (int j = 0; j < Z::NT; ++j) {
+            const int d = 128 * j + 32 * quarter + lane;
+            uint32_t o[32];
+            tmem_ld32(tmem_o + 64u * (uint32_t)j + 32u * (uint32_t)half + lane_off, o);
+            tmem_ld_wait(o);
+            if (h.place >= 0) {
+              float *dst = space.o + ((size_t)h.place * kLatentRows + r0) * LAT + d;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (r0 + k < h.rows) dst[(size_t)k * LAT] = __uint_as_float(o[k]);
-          } else {
-            T *dst = static_cast<T *>(p.out) + ((size_t)h.row0 + r0) * LAT + d;
+              for (int k = 0; k < 32; ++k)
+                if (r0 + k < h.rows) dst[(size_t)k * LAT] = __uint_as_float(o[k]);
+            } else {
+              T *dst = static_cast<T *>(p.out) + ((size_t)h.row0 + r0) * LAT + d;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (r0 + k < h.rows) dst[(size_t)k * LAT] = from_float<T>(__uint_as_float(o[k]) * sh.inv[r0 + k]);
+              for (int k = 0; k < 32; ++k) {
+                const float f = __shfl_sync(0xffffffffu, inv, k);
+                if (r0 + k < h.rows) dst[(size_t)k * LAT] = from_float<T>(__uint_as_float(o[k]) * f);
+              }
+            }
           }
         }
         tc_fence_before();
-        meet(0);  // (before anyone writes normalisers again)
+        meet(0);  // (before anyone writes sums again)
         if (!ok) break;
       }
     }
@@ -601,14 +618,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
         if (share_seq(batch, sh.scan, s).len == 0) {
           uint4 *z = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (size_t)s * p.num_heads * LAT);
-          for (int e = t; e < p.num_heads * LAT / 8; e += 128) z[e] = make_uint4(0u, 0u, 0u, 0u);
+          for (int e = t; e < p.num_heads * LAT / 8; e += 32 * kLatentSoftmax) z[e] = make_uint4(0u, 0u, 0u, 0u);
         }
   }
 
   // every role is done with the tensor memory: free it
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kLatentSoftmax + 1) {
     tc_fence_after();
     tmem_dealloc(sh.tmem, Z::TMEM);
   }
