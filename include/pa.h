@@ -594,7 +594,8 @@ pa_status_t pa_q4_append(void *key_cache, void *value_cache, void *key_scales,
  * other arguments and limits as pa_forward.  Scales must be finite.  A bad table
  * entry, length or chunk is reported as PA_ERR_DEVICE_BAD_INPUT; the rows in
  * question then hold no meaningful values (zeros for a bad length without
- * q_start), or are left as they were (a bad chunk). */
+ * q_start), or are left as they were (a bad chunk; rows that starts out of order
+ * give to two sequences hold either's). */
 pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache,
                           const void *value_cache, const void *key_scales,
                           const void *value_scales, const int32_t *block_tables,
@@ -674,6 +675,19 @@ pa_status_t pa_latent_forward(void *out, const void *query, const void *cache,
 
 /* Bytes of workspace for pa_latent_forward, any batch (0 on a bad latent_dim). */
 size_t pa_latent_workspace_bytes(int latent_dim);
+
+/* The four calls above with their arguments in an array of 64-bit words, in
+ * order (pointers and integers as they are, floats as doubles), for bindings
+ * that pay for every argument of a foreign call: `call` is a pa_call_t.  The
+ * words are read before the call returns.  An int that does not fit 32 bits is
+ * PA_ERR_INVALID_ARG. */
+typedef enum {
+  PA_CALL_Q4_APPEND = 0,
+  PA_CALL_Q4_FORWARD = 1,
+  PA_CALL_LATENT_APPEND = 2,
+  PA_CALL_LATENT_FORWARD = 3
+} pa_call_t;
+pa_status_t pa_call(int call, const void *words);
 
 /* Host heuristic: 1 if V2 should serve this batch on a GPU with sm_count
  * SMs, 0 for V1.  The pages switch on sequence length alone: the commit note

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -49,7 +50,14 @@ EXPORTS = ("pa_workspace_bytes", "pa_workspace_layout", "pa_workspace_init",
            "pa_select_blocks", "pa_sparse_forward", "pa_sparse_workspace_bytes",
            "pa_prefix_forward", "pa_prefix_workspace_bytes", "pa_q4_append", "pa_q4_forward",
            "pa_q4_workspace_bytes", "pa_latent_append", "pa_latent_forward",
-           "pa_latent_workspace_bytes")
+           "pa_latent_workspace_bytes", "pa_call")
+
+
+# pa_call's numbers, and the words of each call (q: pointer or integer, d: float)
+_Q4_APPEND = (0, struct.Struct("34q").pack)
+_Q4_FORWARD = (1, struct.Struct("18qd4q").pack)
+_LATENT_APPEND = (2, struct.Struct("6qd24q").pack)
+_LATENT_FORWARD = (3, struct.Struct("15qd5q").pack)
 
 
 class PAError(RuntimeError):
@@ -129,6 +137,8 @@ def load_library(path: str = LIB_PATH):
         lib.pa_sparse_forward.restype = ci
         lib.pa_sparse_forward.argtypes = ([vp] * 9 + [ci] * 12 + [ctypes.c_float, ci, ci, vp, cs,
                                                                   vp])
+        lib.pa_call.restype = ci
+        lib.pa_call.argtypes = [ci, ctypes.c_char_p]
         lib.pa_latent_workspace_bytes.restype = cs
         lib.pa_latent_workspace_bytes.argtypes = [ci]
         lib.pa_latent_append.restype = ci
@@ -161,6 +171,14 @@ def load_library(path: str = LIB_PATH):
 
 def status_text(status: int) -> str:
     return load_library().pa_status_string(int(status)).decode()
+
+
+def _packed(call, what, *args) -> None:
+    """A call through pa_call: its arguments as one string of 64-bit words (a foreign
+    call of 34 arguments takes five times as long)."""
+    status = (_lib or load_library()).pa_call(call[0], call[1](*args))
+    if status:
+        _check(status, what)
 
 
 def _check(status: int, what: str) -> int:
@@ -668,11 +686,10 @@ def pa_q4_append(key_cache, value_cache, key_scales, value_scales, key, value, b
     blocks = block_tables.shape[1]
     if max_seq_len is None:
         max_seq_len = blocks * bs
-    _check((_lib or load_library()).pa_q4_append(
-        kc, vc, ks, vs, qo, ko, vo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv, D,
-        nb, bs, blocks, int(max_seq_len), rotary_dim, int(interleaved), max_position,
-        _DTYPES[key.dtype], ws, workspace.numel() * workspace.element_size(),
-        _stream_handle(stream)), "pa_q4_append")
+    _packed(_Q4_APPEND, "pa_q4_append",
+            kc, vc, ks, vs, qo, ko, vo, qp, kp, vp, qst, kst, vst, cs, pos, bt, sl, qs, B, R, H, hkv,
+            D, nb, bs, blocks, max_seq_len, rotary_dim, interleaved, max_position,
+            _DTYPES[key.dtype], ws, workspace.nbytes, _stream_handle(stream))
 
 
 def pa_q4_forward(out, query, key_cache, value_cache, key_scales, value_scales, block_tables,
@@ -691,10 +708,9 @@ def pa_q4_forward(out, query, key_cache, value_cache, key_scales, value_scales, 
     blocks = block_tables.shape[1]
     if max_seq_len is None:
         max_seq_len = blocks * bs
-    _check((_lib or load_library()).pa_q4_forward(
-        o, q, kc, vc, ks, vs, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks, int(max_seq_len),
-        float(scale), _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
-        _stream_handle(stream)), "pa_q4_forward")
+    _packed(_Q4_FORWARD, "pa_q4_forward",
+            o, q, kc, vc, ks, vs, bt, sl, qs, B, R, H, hkv, D, nb, bs, blocks, max_seq_len, scale,
+            _DTYPES[query.dtype], ws, workspace.nbytes, _stream_handle(stream))
 
 
 def pa_latent_workspace_bytes(latent_dim: int) -> int:
@@ -771,11 +787,10 @@ def pa_latent_append(cache, latent, rope_key, block_tables, seq_lens, workspace,
     blocks = block_tables.shape[1]
     if max_seq_len is None:
         max_seq_len = blocks * bs
-    _check((_lib or load_library()).pa_latent_append(
-        c, q, qp, lp, kp, nw, float(eps), qst, qhst, lst, kst, cs, pos, bt, sl, qs, B, R, H, lat,
-        rope, nb, bs, blocks, int(max_seq_len), int(interleaved), max_position,
-        _DTYPES[cache.dtype], ws, workspace.numel() * workspace.element_size(),
-        _stream_handle(stream)), "pa_latent_append")
+    _packed(_LATENT_APPEND, "pa_latent_append",
+            c, q, qp, lp, kp, nw, eps, qst, qhst, lst, kst, cs, pos, bt, sl, qs, B, R, H, lat, rope,
+            nb, bs, blocks, max_seq_len, interleaved, max_position, _DTYPES[cache.dtype], ws,
+            workspace.nbytes, _stream_handle(stream))
 
 
 def pa_latent_forward(out, query, cache, block_tables, seq_lens, scale, workspace, q_start=None,
@@ -794,12 +809,12 @@ def pa_latent_forward(out, query, cache, block_tables, seq_lens, scale, workspac
     blocks = block_tables.shape[1]
     if max_seq_len is None:
         max_seq_len = blocks * bs
-    opts = ctypes.byref(pa_options_t(0, 0, 0, debug_flags, wait_limit_ns, None, 0, 0, 0)) \
+    opts = pa_options_t(0, 0, 0, debug_flags, wait_limit_ns, None, 0, 0, 0) \
         if debug_flags or wait_limit_ns else None
-    _check((_lib or load_library()).pa_latent_forward(
-        o, q, c, bt, sl, qs, B, R, H, lat, width - lat, nb, bs, blocks, int(max_seq_len),
-        float(scale), _DTYPES[query.dtype], ws, workspace.numel() * workspace.element_size(),
-        _stream_handle(stream), opts), "pa_latent_forward")
+    _packed(_LATENT_FORWARD, "pa_latent_forward",
+            o, q, c, bt, sl, qs, B, R, H, lat, width - lat, nb, bs, blocks, max_seq_len, scale,
+            _DTYPES[query.dtype], ws, workspace.nbytes, _stream_handle(stream),
+            ctypes.addressof(opts) if opts is not None else 0)
 
 
 def pa_host_staging_bytes(num_seqs: int, num_heads: int, head_size: int,

@@ -1,0 +1,474 @@
+"""pa_latent_append and pa_latent_forward: a paged cache of shared latents against
+its definition in 64 bits, their refusals (CPU), their reports of bad data and their
+bounded waits."""
+import math
+import random
+
+import pytest
+import torch
+
+import paged_decode_attention_v2_gb300 as pa
+
+FAKE = 1 << 20  # aligned, never dereferenced by the host checks
+ROPE = 64
+
+APPEND = dict(cache=FAKE, query=FAKE, query_rope=FAKE, latent=FAKE, rope_key=FAKE, norm_weight=FAKE,
+              eps=1e-6, query_stride=8 * 192, query_head_stride=192, latent_stride=576,
+              rope_key_stride=576, cos_sin=FAKE, positions=FAKE, block_tables=FAKE, seq_lens=FAKE,
+              q_start=FAKE, num_seqs=2, num_rows=5, num_heads=8, latent_dim=512, rope_dim=64,
+              num_blocks=64, block_size=16, max_blocks_per_seq=8, max_seq_len=128, interleaved=0,
+              max_position=200, dtype=pa.PA_DTYPE_BF16, workspace=FAKE, workspace_bytes=256, stream=0)
+FORWARD = dict(out=FAKE, query=FAKE, cache=FAKE, block_tables=FAKE, seq_lens=FAKE, q_start=FAKE,
+               num_seqs=2, num_rows=5, num_heads=8, latent_dim=512, rope_dim=64, num_blocks=64,
+               block_size=16, max_blocks_per_seq=8, max_seq_len=128, scale=0.1,
+               dtype=pa.PA_DTYPE_BF16, workspace=FAKE, workspace_bytes=1 << 40, stream=0, opts=None)
+
+# The parity bar of the framework's 16-bit calls, for latents of deviation 1: a
+# weight is rounded to the type (2^-8 of it for bf16, the sums taking it as rounded, so
+# only unlike roundings of a row's weights count), the output again (2^-8 of it).
+ATOL, RTOL = 4e-3, 1e-2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    return pa.load_library()
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(cache=0), pa.PA_ERR_INVALID_ARG),
+    (dict(latent=0), pa.PA_ERR_INVALID_ARG),
+    (dict(rope_key=0), pa.PA_ERR_INVALID_ARG),
+    (dict(cos_sin=0), pa.PA_ERR_INVALID_ARG),
+    (dict(seq_lens=0), pa.PA_ERR_INVALID_ARG),
+    (dict(workspace=0), pa.PA_ERR_INVALID_ARG),
+    (dict(query=0), pa.PA_ERR_INVALID_ARG),
+    (dict(query_rope=0), pa.PA_ERR_INVALID_ARG),
+    (dict(eps=-1.0), pa.PA_ERR_INVALID_ARG),
+    (dict(eps=math.nan), pa.PA_ERR_INVALID_ARG),
+    (dict(interleaved=2), pa.PA_ERR_INVALID_ARG),
+    (dict(max_position=0), pa.PA_ERR_INVALID_ARG),
+    (dict(latent=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(norm_weight=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(positions=FAKE + 2), pa.PA_ERR_INVALID_ARG),
+    (dict(workspace=FAKE + 128), pa.PA_ERR_INVALID_ARG),
+    (dict(latent_stride=504), pa.PA_ERR_INVALID_ARG),
+    (dict(latent_stride=516), pa.PA_ERR_INVALID_ARG),
+    (dict(rope_key_stride=60), pa.PA_ERR_INVALID_ARG),
+    (dict(query_head_stride=60), pa.PA_ERR_INVALID_ARG),
+    (dict(query_stride=1400), pa.PA_ERR_INVALID_ARG),      # rows would overlap
+    (dict(q_start=0), pa.PA_ERR_INVALID_ARG),
+    (dict(num_rows=-1), pa.PA_ERR_INVALID_ARG),
+    (dict(max_seq_len=129), pa.PA_ERR_INVALID_ARG),
+    (dict(dtype=7), pa.PA_ERR_INVALID_ARG),
+    (dict(dtype=pa.PA_DTYPE_F32), pa.PA_ERR_UNSUPPORTED),
+    (dict(latent_dim=384), pa.PA_ERR_UNSUPPORTED),
+    (dict(rope_dim=32), pa.PA_ERR_UNSUPPORTED),
+    (dict(block_size=12, max_seq_len=96), pa.PA_ERR_UNSUPPORTED),
+    (dict(num_heads=129), pa.PA_ERR_UNSUPPORTED),
+    (dict(num_blocks=1 << 28), pa.PA_ERR_UNSUPPORTED),
+    (dict(workspace_bytes=255), pa.PA_ERR_WORKSPACE_TOO_SMALL),
+])
+def test_append_refusals(lib, over, status):
+    assert lib.pa_latent_append(*dict(APPEND, **over).values()) == status
+    words = pa._LATENT_APPEND[1](*dict(APPEND, **over).values())
+    assert lib.pa_call(2, words) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(out=0), pa.PA_ERR_INVALID_ARG),
+    (dict(cache=0), pa.PA_ERR_INVALID_ARG),
+    (dict(block_tables=0), pa.PA_ERR_INVALID_ARG),
+    (dict(workspace=0), pa.PA_ERR_INVALID_ARG),
+    (dict(query=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(seq_lens=FAKE + 2), pa.PA_ERR_INVALID_ARG),
+    (dict(q_start=0), pa.PA_ERR_INVALID_ARG),
+    (dict(scale=math.inf), pa.PA_ERR_INVALID_ARG),
+    (dict(num_seqs=-1), pa.PA_ERR_INVALID_ARG),
+    (dict(num_heads=0), pa.PA_ERR_INVALID_ARG),
+    (dict(max_seq_len=129), pa.PA_ERR_INVALID_ARG),
+    (dict(dtype=pa.PA_DTYPE_F32), pa.PA_ERR_UNSUPPORTED),
+    (dict(latent_dim=1024), pa.PA_ERR_UNSUPPORTED),
+    (dict(rope_dim=0), pa.PA_ERR_UNSUPPORTED),
+    (dict(max_blocks_per_seq=1 << 28, max_seq_len=(1 << 30) + 1), pa.PA_ERR_UNSUPPORTED),
+    (dict(num_rows=(1 << 31) - 1), pa.PA_ERR_UNSUPPORTED),
+    (dict(workspace_bytes=4096), pa.PA_ERR_WORKSPACE_TOO_SMALL),
+])
+def test_forward_refusals(lib, over, status):
+    assert lib.pa_latent_forward(*dict(FORWARD, **over).values()) == status
+    words = pa._LATENT_FORWARD[1](*dict(FORWARD, **dict(over, opts=0)).values())
+    assert lib.pa_call(3, words) == status
+
+
+def test_no_rows_is_no_work(lib):
+    assert lib.pa_latent_append(*dict(APPEND, num_rows=0, latent=0, rope_key=0, query=0, query_rope=0).values()) == pa.PA_OK
+    assert lib.pa_latent_forward(*dict(FORWARD, num_rows=0, query=0, out=0).values()) == pa.PA_OK
+
+
+def test_workspace_sizes(lib):
+    assert pa.pa_latent_workspace_bytes(384) == 0
+    a, b = pa.pa_latent_workspace_bytes(256), pa.pa_latent_workspace_bytes(512)
+    assert 0 < a < b and a % 256 == 0 and b % 256 == 0
+
+
+def test_binding_refuses_host_tensors():
+    cache = torch.zeros(4, 16, 320, dtype=torch.bfloat16)
+    i = torch.zeros(1, dtype=torch.int32)
+    w = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        pa.pa_latent_append(cache, cache[0, :1, :256], cache[0, :1, 256:], i.view(1, 1), i, w, torch.zeros(4, 64))
+    with pytest.raises(ValueError):
+        pa.pa_latent_forward(torch.zeros(1, 1, 256), torch.zeros(1, 1, 320), cache, i.view(1, 1), i, 1.0, w)
+
+
+# ---------------------------------------------------------------------------
+
+def tables(lens, bs, g, spare=2):
+    pages = [-(-max(L, 0) // bs) for L in lens]
+    pool = sum(pages) + spare
+    perm = torch.randperm(pool, generator=g).to(torch.int32)
+    bt = torch.full((len(lens), max(pages + [1])), -1, dtype=torch.int32)
+    at = 0
+    for s, n in enumerate(pages):
+        bt[s, :n] = perm[at:at + n]
+        at += n
+    return bt, pool
+
+
+def turn(x, cs, il):
+    """x [rows, heads, 64] in 64 bits, cs [rows, 64]."""
+    c, s = cs[:, None, :32].double(), cs[:, None, 32:].double()
+    a, b = (x[..., 0::2], x[..., 1::2]) if il else (x[..., :32], x[..., 32:])
+    u, v = a * c - b * s, b * c + a * s
+    return torch.stack([u, v], -1).flatten(-2) if il else torch.cat([u, v], -1)
+
+
+def near(got, ref, dtype):
+    """One rounding of fp32 arithmetic: half a step of the type, and 2^-20 of the largest
+    term for the fp32 operations before it."""
+    u = torch.finfo(dtype).eps / 2
+    err = (got.double().cpu() - ref).abs()
+    return (err <= 1.01 * u * ref.abs() + 2 ** -20 * ref.abs().amax().clamp_min(1e-30) + 2 ** -25).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,L,bs,il,norm,query,decode", [
+    (8, 512, 16, False, True, True, False), (1, 256, 8, True, True, True, False), (128, 512, 64, True, False, True, False),
+    (5, 256, 32, False, True, False, False), (24, 512, 16, True, True, True, True)])
+def test_append(dtype, H, L, bs, il, norm, query, decode):
+    g = torch.Generator().manual_seed(H)
+    new = [1] * 5 if decode else [5, 0, 1, 33, 700]
+    lens = [n + c for n, c in zip(new, [0, 7, 15, 3, 60])]
+    bt, pool = tables(lens, bs, g)
+    rows, pad = sum(new), 0 if decode else 3
+    down = (torch.randn(rows + pad, L + ROPE, generator=g) * 3).to(dtype)
+    qfull = torch.randn(rows + pad, H, 128 + ROPE, generator=g).to(dtype)
+    w = (1 + 0.2 * torch.randn(L, generator=g)).to(dtype) if norm else None
+    cache = torch.randn(pool, bs, L + ROPE, generator=g).to(dtype)
+    q = torch.randn(rows + pad, H, L + ROPE, generator=g).to(dtype)
+    place = [(s, t) for s, (n, m) in enumerate(zip(new, lens)) for t in range(m - n, m)]
+    ang = torch.arange(max(lens), dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    qs = [0]
+    for n in new:
+        qs.append(qs[-1] + n)
+    d = "cuda"
+    dc, dq, dd, dqf = cache.to(d), q.to(d), down.to(d), qfull.to(d)
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    pa.pa_latent_append(dc, dd[:, :L], dd[:, L:], bt.to(d), torch.tensor(lens, dtype=torch.int32, device=d), ws, cs.to(d),
+                        query=dq if query else None, query_rope=dqf[..., 128:] if query else None,
+                        norm_weight=w.to(d) if norm else None, eps=1e-5,
+                        q_start=None if decode else torch.tensor(qs, dtype=torch.int32, device=d), interleaved=il)
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    x = down[:rows].double()
+    c = x[:, :L]
+    if norm:
+        c = c / torch.sqrt((c * c).mean(-1, keepdim=True) + 1e-5) * w.double()
+    rcs = cs[[t for _, t in place]]
+    ref = torch.cat([c, turn(x[:, None, L:], rcs, il)[:, 0]], -1)
+    got = dc.cpu()
+    at = [(int(bt[s, t // bs]), t % bs) for s, t in place]
+    assert near(torch.stack([got[p, o] for p, o in at]), ref, dtype)
+    for p, o in at:
+        got[p, o] = cache[p, o]
+    assert torch.equal(got, cache)  # nothing else
+    gq = dq.cpu()
+    if query:
+        assert near(gq[:rows, :, L:], turn(qfull[:rows, :, 128:].double(), rcs, il), dtype)
+        gq[:rows, :, L:] = q[:rows, :, L:]
+    assert torch.equal(gq, q)
+
+
+@pytest.mark.gpu
+def test_append_bad_data():
+    g = torch.Generator().manual_seed(1)
+    for what in ("page", "length", "position", "chunk"):
+        lens, new = [22, 4], [2, 3]
+        bt, pool = tables(lens, 16, g)
+        cache = torch.randn(pool, 16, 320, generator=g).bfloat16().cuda()
+        before = cache.clone()
+        own = bt[0, :2].long() if what != "chunk" else bt[1, :1].long()
+        cs = torch.ones(64, 64)
+        qs = [0, 2, 5]
+        if what == "page":
+            bt[0, 1] = 999
+        elif what == "length":
+            lens[0] = 10 ** 6
+        elif what == "position":
+            cs = cs[:10]
+        else:
+            qs = [0, 4, 3]  # (a chunk of sequence 0, and one that ends before it starts)
+        x = torch.randn(5, 320, generator=g).bfloat16().cuda()
+        ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+        pa.pa_latent_append(cache, x[:, :256], x[:, 256:], bt.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                            ws, cs.cuda(), q_start=torch.tensor(qs, dtype=torch.int32, device="cuda"))
+        assert pa.pa_read_device_status(ws) == pa.PA_ERR_DEVICE_BAD_INPUT
+        assert torch.equal(cache[own], before[own]), what
+
+
+# ---------------------------------------------------------------------------
+
+class Attend:
+    def __init__(self, seed, dtype, H, L, bs, lens, new=None, pad=0, qmult=1.0, cmult=1.0, scale=None):
+        g = torch.Generator().manual_seed(seed)
+        self.__dict__.update(dtype=dtype, H=H, L=L, bs=bs, lens=lens, scale=scale or 1 / math.sqrt(L + ROPE))
+        self.new = new if new is not None else [1] * len(lens)
+        self.chunks = new is not None
+        self.bt, pool = tables(lens, bs, g)
+        self.rows = sum(self.new)
+        self.q = (torch.randn(self.rows + pad, H, L + ROPE, generator=g) * qmult).to(dtype)
+        self.q[self.rows:] = float("nan")  # padding: never looked at by a row of its own
+        self.cache = (torch.randn(pool, bs, L + ROPE, generator=g) * cmult).to(dtype)
+        held = torch.zeros(pool, bs, dtype=torch.bool)
+        for s, n in enumerate(lens):
+            for t in range(max(n, 0)):
+                held[self.bt[s, t // bs].long(), t % bs] = True
+        self.cache[~held] = float("nan")
+
+    def reference(self):
+        c = self.cache.double()
+        out = torch.full((len(self.q), self.H, self.L), 7.0, dtype=torch.float64)
+        row = 0
+        for s, (n, L) in enumerate(zip(self.new, self.lens)):
+            t = torch.arange(max(L, 0))
+            kv = c[self.bt[s, t // self.bs].long(), t % self.bs]
+            for i in range(n):
+                m = L - n + i + 1
+                out[row] = torch.softmax(self.q[row].double() @ kv[:m].T * self.scale, -1) @ kv[:m, :self.L] if m > 0 else 0.0
+                row += 1
+        return out
+
+    def device(self):
+        d = "cuda"
+        self.a = [t.to(d) for t in (self.q, self.cache, self.bt, torch.tensor(self.lens, dtype=torch.int32))]
+        qs = [0]
+        for n in self.new:
+            qs.append(qs[-1] + n)
+        self.qs = torch.tensor(qs, dtype=torch.int32, device=d) if self.chunks else None
+        self.ws = pa.alloc_latent_workspace(self.L)
+        return self
+
+    def run(self, ws=None, out=None, stream=None, **kw):
+        if out is None:
+            out = torch.full((len(self.q), self.H, self.L), 7.0, dtype=self.dtype, device="cuda")
+        pa.pa_latent_forward(out, *self.a, self.scale, self.ws if ws is None else ws, q_start=self.qs, stream=stream, **kw)
+        return out
+
+    def check(self, out, atol=ATOL, rtol=RTOL):
+        ref = self.reference()
+        err = (out.double().cpu() - ref).abs()
+        assert (err <= atol + rtol * ref.abs()).all(), float((err - rtol * ref.abs()).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,L,bs", [(1, 512, 16), (16, 512, 8), (64, 512, 64), (65, 512, 32), (128, 512, 16), (128, 256, 8),
+                                    (24, 256, 16), (63, 256, 64)])
+def test_decode(dtype, H, L, bs):
+    c = Attend(1, dtype, H, L, bs, [0, 1, 7, 8, 9, 63, 64, 65, 127, 128, 129, 0, 517]).device()
+    c.check(c.run())
+    assert pa.pa_read_device_status(c.ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,L,bs", [(5, 512, 8), (64, 512, 64), (128, 512, 16), (33, 256, 32), (100, 256, 16)])
+def test_chunks(dtype, H, L, bs):
+    c = Attend(2, dtype, H, L, bs, [5, 40, 33, 1, 130, 64], [5, 0, 3, 1, 6, 17], pad=3).device()
+    c.check(c.run())  # (rows behind the last sequence stay 7)
+    assert pa.pa_read_device_status(c.ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,L,lens", [(4, 512, [30000]), (3, 256, [11000, 3, 12000]), (2, 512, [200] * 300), (80, 256, [6000, 1, 2500])])
+def test_long_and_many(H, L, lens):
+    c = Attend(3, torch.bfloat16, H, L, 16, lens).device()
+    c.check(c.run())
+
+
+@pytest.mark.gpu
+def test_peaked_scores():
+    """Scores of +-1000, and none at all: maxima that rise late and by much."""
+    for kw in (dict(qmult=8.0), dict(qmult=60.0), dict(qmult=0.0), dict(scale=-0.2)):
+        for dtype in (torch.bfloat16, torch.float16):
+            c = Attend(4, dtype, 16, 512, 16, [900, 40, 1], **kw).device()
+            ref = c.reference()
+            out = c.run().double().cpu()
+            # scores of magnitude X are sums of 576 products in fp32: off by X 576 2^-24 at
+            # most, and the output by that times the spread of the latents
+            X = float((c.q[:c.rows].double().abs().sum(-1).amax() * 5 + 1) * abs(c.scale))
+            assert ((out - ref).abs() <= ATOL + X * 576 * 2 ** -24 * 8 + RTOL * ref.abs()).all(), kw
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rise", ["up", "down", "steps"])
+def test_maxima_that_rise(rise):
+    """Keys in an order that makes every tile's largest score the largest so far."""
+    c = Attend(5, torch.float16, 7, 256, 16, [1000])
+    t = torch.arange(1000, dtype=torch.float64)
+    lift = {"up": t / 25, "down": -t / 25, "steps": (t // 64) * 9.0}[rise]
+    c.q[:, :, 256] = 1.0
+    flat = c.cache[c.bt[0].long()].flatten(0, 1)
+    flat[:1000, 256] = (lift / c.scale / 16).half()
+    c.q[:, :, 256] = 16.0
+    c.cache[c.bt[0].long()] = flat.view(-1, 16, 320)
+    c.device()
+    c.check(c.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["page", "length", "negative", "chunk"])
+def test_bad_data(what):
+    c = Attend(6, torch.bfloat16, 20, 512, 16, [100, 40, 70], [3, 2, 4] if what == "chunk" else None).device()
+    ref = c.reference()
+    q, cache, bt, sl = c.a
+    if what == "page":
+        bt[1, 1] = 10 ** 6
+    elif what == "length":
+        sl[1] = 10 ** 6
+    elif what == "negative":
+        sl[1] = -5
+    else:
+        c.qs = torch.tensor([0, 3, 5, 99], dtype=torch.int32, device="cuda")
+    out = c.run().double().cpu()
+    assert pa.pa_read_device_status(c.ws) == pa.PA_ERR_DEVICE_BAD_INPUT
+    for r in ([0, 2] if len(out) == 3 else [0, 1, 2, 3, 4]):
+        assert ((out[r] - ref[r]).abs() <= ATOL + RTOL * ref[r].abs()).all()
+    if what in ("length", "negative"):
+        assert (out[1] == 0).all()
+    d = Attend(7, torch.bfloat16, 8, 512, 16, [50]).device()
+    d.check(d.run(ws=c.ws))
+    assert pa.pa_read_device_status(c.ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+def test_bounded_waits():
+    """Softmax warps that wait for a barrier nobody releases give up after the limit; the
+    workspace serves again once initialised."""
+    c = Attend(8, torch.bfloat16, 16, 512, 16, [300, 20]).device()
+    c.run(debug_flags=pa.PA_DEBUG_STALL_CONSUMERS, wait_limit_ns=2_000_000)
+    assert pa.pa_read_device_status(c.ws) == pa.PA_ERR_DEVICE_TIMEOUT
+    pa.pa_workspace_init(c.ws)
+    c.check(c.run())
+    assert pa.pa_read_device_status(c.ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+def test_graph_shared_workspace_and_streams():
+    a = Attend(10, torch.bfloat16, 128, 512, 16, [3000, 5, 700]).device()
+    b = Attend(11, torch.bfloat16, 12, 512, 8, [44, 900], [7, 3]).device()
+    oa = torch.zeros(3, 128, 512, dtype=torch.bfloat16, device="cuda")
+    ob = torch.zeros(10, 12, 512, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.run(out=oa)
+        b.run(ws=a.ws, out=ob)
+        side.synchronize()
+        graphs = []
+        for c, o in ((a, oa), (b, ob)):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                c.run(ws=a.ws, out=o)
+            graphs.append(g)
+        for _ in range(3):
+            for g, o in zip(graphs, (oa, ob)):
+                o.fill_(7.0)
+                g.replay()
+    side.synchronize()
+    a.check(oa)
+    b.check(ob)
+    s2 = torch.cuda.Stream()
+    s2.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        x = a.run(out=oa)
+        y = b.run(stream=s2, out=ob)
+    torch.cuda.synchronize()
+    a.check(x)
+    b.check(y)
+
+
+@pytest.mark.gpu
+def test_far_pages():
+    """Pages beyond 2^31 elements and 2^32 bytes."""
+    bs, L = 64, 512
+    nb = 70000
+    cache = torch.empty(nb, bs, L + ROPE, dtype=torch.bfloat16, device="cuda")
+    c = Attend(12, torch.bfloat16, 16, L, bs, [100, 65])
+    src = c.cache
+    far = {int(p): nb - 1 - 31 * i for i, p in enumerate(c.bt[c.bt >= 0].tolist())}
+    for p, f in far.items():
+        cache[f] = src[p].cuda()
+    c.device()
+    bt = c.bt.clone()
+    for p, f in far.items():
+        bt[c.bt == p] = f
+    c.a[1], c.a[2] = cache, bt.cuda()
+    c.check(c.run())
+    assert pa.pa_read_device_status(c.ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+def test_decode_loop():
+    """A prompt, then tokens one by one: appended, then attended to, against 64 bits over
+    the rows that the cache then holds."""
+    H, L, bs, dt = 20, 256, 16, torch.bfloat16
+    g = torch.Generator().manual_seed(3)
+    rng = random.Random(4)
+    prompt, steps = [37, 5, 90], 8
+    B, top = len(prompt), max(prompt) + steps * 3
+    width = -(-top // bs)
+    cache = torch.zeros(B * width, bs, L + ROPE, dtype=dt, device="cuda")
+    bt = torch.randperm(B * width, generator=g).to(torch.int32).view(B, width).cuda()
+    ang = torch.arange(top, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+    ws = pa.alloc_latent_workspace(L)
+    w = torch.ones(L, dtype=dt, device="cuda")
+    lens = [0] * B
+    for k in range(steps + 1):
+        new = prompt if k == 0 else [rng.randint(1, 3) for _ in range(B)]
+        lens = [a + b for a, b in zip(lens, new)]
+        rows = sum(new)
+        qs = [0]
+        for n in new:
+            qs.append(qs[-1] + n)
+        qs = torch.tensor(qs, dtype=torch.int32, device="cuda")
+        down = torch.randn(rows, L + ROPE, generator=g).to(dt).cuda()
+        query = torch.randn(rows, H, L + ROPE, generator=g).to(dt).cuda()
+        rope = torch.randn(rows, H, ROPE, generator=g).to(dt).cuda()
+        sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        pa.pa_latent_append(cache, down[:, :L], down[:, L:], bt, sl, ws, cs, query=query, query_rope=rope, norm_weight=w, eps=1e-6, q_start=qs)
+        out = torch.empty(rows, H, L, dtype=dt, device="cuda")
+        pa.pa_latent_forward(out, query, cache, bt, sl, 0.06, ws, q_start=qs)
+        assert pa.pa_read_device_status(ws) == pa.PA_OK
+        row = 0
+        for s, n in enumerate(new):
+            t = torch.arange(lens[s], device="cuda")
+            kv = cache[bt[s, t // bs].long(), t % bs].double()
+            for i in range(n):
+                m = lens[s] - n + i + 1
+                ref = torch.softmax(query[row].double() @ kv[:m].T * 0.06, -1) @ kv[:m, :L]
+                assert ((out[row].double() - ref).abs() <= ATOL + RTOL * ref.abs()).all()
+                row += 1
