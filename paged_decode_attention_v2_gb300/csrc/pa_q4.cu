@@ -65,7 +65,8 @@ struct alignas(16) Q4Piece {
   int steps, dest;
   int rows, row0;     // columns of the unit, its first query row
   int kvh, lim_base;  // column c sees the tokens below lim_base + c / group + 1
-  int share, pad[3];
+  int share, parts;   // parts: the shares that the unit lies in, with its first piece
+  int pad[2];
 };
 constexpr int kQ4Pieces = 8;  // handed over and not yet taken: at most stages + 1
 
@@ -129,15 +130,17 @@ struct Q4Shape {
   static constexpr int CPR = RB / 16;       // 16-byte pieces (32 codes) of a row
   static constexpr int GM = 8 * NT;         // columns of a unit
   // tiles of 16 tokens that a warp takes at once: two give the MMAs of one
-  // something to run beside, where registers allow
-  static constexpr int TT = NT == 1 && D <= 128 ? 2 : 1;
+  // something to run beside, where registers allow (D 64, 16 columns: 68.5 -> 57.8 us)
+  static constexpr int TT = D <= 128 ? 2 : 1;
   static constexpr int TOKENS = 16 * TT;  // of a step
   static constexpr int QREGS = CPR * NT * 4;
   static constexpr bool QSMEM = QREGS > 32;  // query fragments in shared memory
   static constexpr int KEYS = 0, VALUES = TOKENS * RB, KSC = 2 * TOKENS * RB, VSC = KSC + TOKENS * 4 * NG,
                        STAGE = VSC + TOKENS * 4 * NG;
-  // CTAs an SM by registers, and the ring that their shared memory leaves
-  static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : 3) : (D == 256 ? 2 : 3);
+  // CTAs an SM by registers (with a third that spilled a few, D 256 took 122 us
+  // instead of 79, 16 columns at D 128 178 instead of 117), and the ring that
+  // their shared memory leaves
+  static constexpr int CTAS = NT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : (D == 64 ? 3 : 2);
   static constexpr int STAGES = D == 256 || (D == 128 && NT == 1) ? 3 : 4;
   static constexpr int CACHE = D == 256 && NT == 1 ? 64 : 384;  // sequences of the plan kept by
   static constexpr int QBUF = QSMEM ? QREGS * 128 : 0;  // a warp's
@@ -210,14 +213,15 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
   int share = (int)blockIdx.x * kQ4Warps + warp;  // the one that is walked
   walk.begin(batch, s_scan, plan.begin(share), share < plan.big ? plan.begin(share + 1) : 0);
   int handed = 0;                                  // pieces
+  int ahead = -1;                                  // (lane 0) a small share taken before it is needed
   int f_left = 0, f_tok = 0, f_end = 0, f_at = 0;  // tiles left of the piece, their next token, its KV head's place
   const int32_t *table = p.block_tables;
   const int hbs = p.num_kv_heads * p.block_size;
   auto next_piece = [&]() {
     if (walk.left <= 0 && plan.small > 0) {
-      int k = 0;
-      if (lane == 0) k = atomicAdd(space.counters + kShareTaken, 1) & 0x7fffffff;
-      k = __shfl_sync(0xffffffffu, k, 0);
+      if (lane == 0 && ahead < 0) ahead = atomicAdd(space.counters + kShareTaken, 1) & 0x7fffffff;
+      const int k = __shfl_sync(0xffffffffu, ahead, 0);
+      ahead = -1;
       share = plan.big + k;
       if (k < plan.small) walk.begin(batch, s_scan, plan.begin(share), plan.begin(share + 1));
     }
@@ -243,17 +247,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
       u.steps = n;
       u.share = share;
       u.tok = step * Z::TOKENS;
-      if (u.dest == kQ4Place1 && lane == 0) {
-        ShareJoin j{};
-        j.share = share;
-        j.parts = plan.of(walk.line + walk.q.steps - 1) - share + 1;
-        j.by = 1;
-        j.rows = u.rows;
-        j.group = p.group;
-        j.stride = p.num_heads;
-        j.out_row = (long long)u.row0 * p.num_heads + u.kvh * p.group;
-        share_join(space, j);
-      }
+      if (u.dest == kQ4Place1) u.parts = plan.of(walk.line + walk.q.steps - 1) - share + 1;
       // (its queries on their way to L2)
 #pragma unroll
       for (int i = lane; i < GM * (D / 64); i += 32) {
@@ -343,6 +337,8 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
       }
       f_tok += Z::TOKENS;
       if (--f_left == 0) next_piece();
+      if (f_left == 2 && walk.left <= 0 && plan.small > 0 && lane == 0 && ahead < 0)
+        ahead = atomicAdd(space.counters + kShareTaken, 1) & 0x7fffffff;
       look_up();
     }
     cp_async_commit();
@@ -358,7 +354,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
   float o[NT][2 * CPR][4];  // O^T: row pairs (g, g + 8), columns 2t, 2t + 1
   float sl[NT][2], sb[NT][NG][2], m[NT][2];
   int lim[CHUNK ? NT : 1][2];
-  int rows = 0, row0 = 0, kvh = 0, dest = 0, at_share = 0, left = 0, tok = 0, end = 0, taken = 0;
+  int rows = 0, row0 = 0, kvh = 0, dest = 0, at_share = 0, parts = 0, left = 0, tok = 0, end = 0, taken = 0;
 
   // (slots: of this tile, and of the one to copy, whose last tile is done with)
   for (uint32_t slot = 0, copy = (NST - 1) * Z::STAGE;; copy = slot, slot = slot + Z::STAGE == NST * Z::STAGE ? 0 : slot + Z::STAGE) {
@@ -369,7 +365,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
     if (left == 0) {
       const Q4Piece u = s_piece[warp][taken++ & (kQ4Pieces - 1)];
       if (u.dest == kQ4End) break;
-      rows = u.rows, row0 = u.row0, kvh = u.kvh, dest = u.dest, at_share = u.share;
+      rows = u.rows, row0 = u.row0, kvh = u.kvh, dest = u.dest, at_share = u.share, parts = u.parts;
       left = u.steps, tok = u.tok, end = u.end;
       // queries: lane (g, t) has elements 8 t .. 8 t + 7 of each 32 of column g
 #pragma unroll
@@ -589,6 +585,17 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
     tok += Z::TOKENS;
     if (--left == 0) {
       // ---- the piece's sums: out, or into its place
+      if (dest == kQ4Place1 && lane == 0) {
+        ShareJoin j{};
+        j.share = at_share;
+        j.parts = parts;
+        j.by = 1;
+        j.rows = rows;
+        j.group = p.group;
+        j.stride = p.num_heads;
+        j.out_row = (long long)row0 * p.num_heads + kvh * p.group;
+        share_join(space, j);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

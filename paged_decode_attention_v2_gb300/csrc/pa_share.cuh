@@ -69,7 +69,7 @@ __device__ __forceinline__ long long div_steps(long long a, long long b) {
 // big_total steps, `small` equal ones over the rest.
 constexpr int kShareSmall = 1;     // small shares for each large one,
 constexpr int kShareSmallPct = 25; // over this much of the line,
-constexpr int kShareTwo = 8;       // where there are this many steps a worker
+constexpr int kShareTwo = 24;      // where there are this many steps a worker
 constexpr int kShareLeast = 2;     // steps of a share where there are not enough for all
 struct SharePlan {
   long long total, big_total;
