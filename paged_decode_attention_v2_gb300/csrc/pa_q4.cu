@@ -629,6 +629,8 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
         }
     }
   }
+  // (earlier, the join's CTAs would wait beside this grid's: 76 -> 92 us)
+  pdl_launch_dependents();
   // outputs of empty sequences
   if (!CHUNK)
     for (int q = blockIdx.x; q < p.num_seqs; q += gridDim.x)
@@ -636,7 +638,6 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
         uint4 *z = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (size_t)q * p.num_heads * D);
         for (int i = threadIdx.x; i < p.num_heads * D / 8; i += kQ4Threads) z[i] = make_uint4(0u, 0u, 0u, 0u);
       }
-  pdl_launch_dependents();
 }
 
 namespace {

@@ -12,6 +12,15 @@ namespace {
 
 constexpr int kJoinWarps = kJoinThreads / 32;
 
+__device__ __forceinline__ ShareJoin load_join(const ShareJoin *at) {
+  const int4 a = __ldcg(reinterpret_cast<const int4 *>(at)), b = __ldcg(reinterpret_cast<const int4 *>(at) + 1);
+  ShareJoin j;
+  j.share = a.x, j.parts = a.y, j.by = a.z, j.rows = a.w;
+  j.group = b.x, j.stride = b.y;
+  j.out_row = (long long)((unsigned long long)(uint32_t)b.w << 32 | (uint32_t)b.z);
+  return j;
+}
+
 // The pieces k = first, first + by, ... of four columns of a row: their maximum,
 // sum and weighted outputs.
 struct JoinSum {
@@ -78,53 +87,64 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) pa_share_join_kernel(
 
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int per = p.max_rows * chunks;
+  // (an item's unit is read with the item before it, the first with the counts: what
+  // the list holds behind its end is not used)
+  const int per = p.max_rows * chunks, shares = p.space.shares;
+  const int narrow = p.width / 32, wide = p.max_rows * narrow;
+  int i = blockIdx.x * kJoinWarps + warp;
+  ShareJoin j = load_join(p.space.join + min(i / per, shares - 1));
+  ShareJoin jm = load_join(p.space.join + max(shares - 1 - (int)blockIdx.x / wide, 0));
   const int few = __ldcg(p.space.counters + kShareFew) * per;
+  const int many = __ldcg(p.space.counters + kShareMany) * wide;
   // rows of units of few pieces: a warp's each
-  for (int i = blockIdx.x * kJoinWarps + warp; i < few; i += gridDim.x * kJoinWarps) {
+  while (i < few) {
     const int row = i / chunks % p.max_rows, col = i % chunks * 128 + lane * 4;
-    const ShareJoin j = p.space.join[i / per];
+    i += gridDim.x * kJoinWarps;
+    const ShareJoin next = load_join(p.space.join + min(i / per, shares - 1));
     if (row < j.rows && live) {
       JoinSum s;
       join_pieces(p, j, row, col, 0, 1, s);
       join_store<T>(p, j, row, col, s);
     }
+    j = next;
   }
   // of many: 32 columns a CTA; a warp takes four pieces at once, eight lanes each
-  const int narrow = p.width / 32, items = p.max_rows * narrow * __ldcg(p.space.counters + kShareMany);
-  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+  for (i = blockIdx.x; i < many;) {
     const int row = i / narrow % p.max_rows, col = i % narrow * 32 + (lane & 7) * 4;
-    const ShareJoin j = p.space.join[p.space.shares - 1 - i / (narrow * p.max_rows)];
-    if (row >= j.rows) continue;
-    JoinSum s;
-    join_pieces(p, j, row, col, warp * 4 + (lane >> 3), kJoinWarps * 4, s);
-    s_part[warp * 4 + (lane >> 3)][lane & 7] = s;
-    __syncthreads();
-    if (warp == 0) {
-      // lanes 8 q .. 8 q + 7 join every fourth of them, then the four their sums
-      JoinSum r = s_part[lane >> 3][lane & 7];
-      for (int w = 4 + (lane >> 3); w < kJoinWarps * 4; w += 4) {
-        const JoinSum &q = s_part[w][lane & 7];
-        const float m = fmaxf(r.m, q.m);
-        join_scale(r, m);
-        join_add(r, exp2f(q.m - m), q.l, q.o);
-      }
+    i += gridDim.x;
+    const ShareJoin next = load_join(p.space.join + max(shares - 1 - i / wide, 0));
+    if (row < jm.rows) {
+      JoinSum s;
+      join_pieces(p, jm, row, col, warp * 4 + (lane >> 3), kJoinWarps * 4, s);
+      s_part[warp * 4 + (lane >> 3)][lane & 7] = s;
+      __syncthreads();
+      if (warp == 0) {
+        // lanes 8 q .. 8 q + 7 join every fourth of them, then the four their sums
+        JoinSum r = s_part[lane >> 3][lane & 7];
+        for (int w = 4 + (lane >> 3); w < kJoinWarps * 4; w += 4) {
+          const JoinSum &q = s_part[w][lane & 7];
+          const float m = fmaxf(r.m, q.m);
+          join_scale(r, m);
+          join_add(r, exp2f(q.m - m), q.l, q.o);
+        }
 #pragma unroll
-      for (int d = 8; d < 32; d <<= 1) {
-        JoinSum q;
-        q.m = __shfl_xor_sync(0xffffffffu, r.m, d);
-        q.l = __shfl_xor_sync(0xffffffffu, r.l, d);
-        q.o.x = __shfl_xor_sync(0xffffffffu, r.o.x, d);
-        q.o.y = __shfl_xor_sync(0xffffffffu, r.o.y, d);
-        q.o.z = __shfl_xor_sync(0xffffffffu, r.o.z, d);
-        q.o.w = __shfl_xor_sync(0xffffffffu, r.o.w, d);
-        const float m = fmaxf(r.m, q.m);
-        join_scale(r, m);
-        join_add(r, exp2f(q.m - m), q.l, q.o);
+        for (int d = 8; d < 32; d <<= 1) {
+          JoinSum q;
+          q.m = __shfl_xor_sync(0xffffffffu, r.m, d);
+          q.l = __shfl_xor_sync(0xffffffffu, r.l, d);
+          q.o.x = __shfl_xor_sync(0xffffffffu, r.o.x, d);
+          q.o.y = __shfl_xor_sync(0xffffffffu, r.o.y, d);
+          q.o.z = __shfl_xor_sync(0xffffffffu, r.o.z, d);
+          q.o.w = __shfl_xor_sync(0xffffffffu, r.o.w, d);
+          const float m = fmaxf(r.m, q.m);
+          join_scale(r, m);
+          join_add(r, exp2f(q.m - m), q.l, q.o);
+        }
+        if (lane < 8) join_store<T>(p, jm, row, col, r);
       }
-      if (lane < 8) join_store<T>(p, j, row, col, r);
+      __syncthreads();
     }
-    __syncthreads();
+    jm = next;
   }
   // the counters as the next call needs them: no CTA has one to read any more
   __syncthreads();

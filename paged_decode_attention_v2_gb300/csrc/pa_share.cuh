@@ -31,7 +31,7 @@ constexpr int kJoinFew = 32; // pieces that one warp joins by itself
 // A unit whose keys lie in several shares: parts pieces (place 1 of `share`,
 // then place 0 of the next shares, `by` apart), each of `rows` rows.  Row r
 // goes to out row out_row + (r / group) * stride + r % group.
-struct ShareJoin {
+struct alignas(16) ShareJoin {
   int share, parts, by, rows;
   int group, stride;
   long long out_row;
@@ -68,7 +68,7 @@ __device__ __forceinline__ long long div_steps(long long a, long long b) {
 // The shares of a line of `total` steps: `big` equal ones over its first
 // big_total steps, `small` equal ones over the rest.
 constexpr int kShareSmall = 1;     // small shares for each large one,
-constexpr int kShareSmallPct = 25; // over this much of the line,
+constexpr int kShareSmallPct = 35; // over this much of the line,
 constexpr int kShareTwo = 24;      // where there are this many steps a worker
 constexpr int kShareLeast = 2;     // steps of a share where there are not enough for all
 struct SharePlan {
