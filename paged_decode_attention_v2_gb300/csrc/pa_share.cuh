@@ -74,12 +74,12 @@ constexpr int kShareLeast = 2;     // steps of a share where there are not enoug
 struct SharePlan {
   long long total, big_total;
   int big, small;
-  __device__ __forceinline__ void make(long long steps, int workers) {
+  __device__ __forceinline__ void make(long long steps, int workers, int two = kShareTwo) {
     total = big_total = steps;
     const long long most = (steps + kShareLeast - 1) / kShareLeast;
     big = most < workers ? (int)most : workers;
     small = 0;
-    if (steps >= (long long)workers * kShareTwo) {
+    if (steps >= (long long)workers * two) {
       small = kShareSmall * workers;
       big_total = div_steps(steps, 100) * (100 - kShareSmallPct);
     }
@@ -234,9 +234,9 @@ __device__ __forceinline__ void share_join(const ShareSpace &space, const ShareJ
 struct JoinParams {
   ShareSpace space;
   void *out;  // [..][width], rows as the ShareJoins say
-  int max_rows, width;
+  int max_rows, item_rows, width;  // rows of a place, of the largest unit
 };
-const void *share_join_kernel(int dtype_bf16);
+const void *share_join_kernel(int dtype_bf16, int width);
 constexpr int kJoinThreads = 256, kJoinCtas = 3;  // CTAs: an SM's
 
 }  // namespace pa
