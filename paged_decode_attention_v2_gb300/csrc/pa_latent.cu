@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // ======================= producer warp =======================
     const int U = p.unit_rows;
     SharePlan plan;
-    plan.make(sh.scan.cum[128], (int)gridDim.x / p.side);
+    // (large shares alone: a piece's rows are up to 128 KB, and more pieces took more
+    // than they evened out: 168 -> 160 us for 64 sequences with 128 heads)
+    plan.make(sh.scan.cum[128], (int)gridDim.x / p.side, INT_MAX);
     // an item: a share, for one of the row groups that stand side by side
     int item = blockIdx.x;
     ShareWalk walk{};
@@ -297,12 +299,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // would rest until then.
     LatentStage line[2];
     int line_y[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!(f.flags & kLatentEnd)) fetch();
-      line[k] = f;
-      line_y[k] = y;
-    }
+    fetch();
+    line[0] = f;
+    line_y[0] = y;
     bool ok = true;
     int i = 0, nq = 0;
     while (true) {
@@ -346,6 +345,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         __syncwarp();
         if (lane < NP) tma_load_2d(q_u32 + lane * 8192u, &tmap_q, lane * 64, row0, q_full);
         ++nq;
+      }
+      if (i == 1) {  // (the first copy did not wait for the tiles behind it)
+        if (!(f.flags & kLatentEnd)) fetch();
+        line[1] = f;
+        line_y[1] = y;
       }
       line[0] = line[1];
       line_y[0] = line_y[1];

@@ -108,26 +108,38 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) pa_share_join_kernel(
 
   pdl_wait_primary();
   pdl_launch_dependents();
-  // (an item's unit is read with the item before it, the first with the counts: what
-  // the list holds behind its end is not used)
   const int per = p.item_rows, shares = p.space.shares;
   const int narrow = p.width / 32, wide = per * narrow;
+  const int warps = gridDim.x * kJoinWarps;
   int i = blockIdx.x * kJoinWarps + warp;
-  ShareJoin j = load_join(p.space.join + min(i / per, shares - 1));
+  // (an item's unit is read with the item before it, the first with the counts: what
+  // the list holds behind its end is not used)
+  ShareJoin j = load_join(p.space.join + min(i / (per * C), shares - 1));
   ShareJoin jm = load_join(p.space.join + max(shares - 1 - (int)blockIdx.x / wide, 0));
   const int few = __ldcg(p.space.counters + kShareFew) * per;
   const int many = __ldcg(p.space.counters + kShareMany) * wide;
-  // rows of units of few pieces: a warp's each
-  while (i < few) {
-    const int row = i % per;
-    i += gridDim.x * kJoinWarps;
-    const ShareJoin next = load_join(p.space.join + min(i / per, shares - 1));
-    if (row < j.rows && live) {
-      JoinSum<C> s;
-      join_pieces(p, j, row, lane * 4, 0, 1, s);
-      join_store<T>(p, j, row, lane * 4, s);
+  // rows of units of few pieces: a warp's each, or (while there are warps for it) a
+  // warp's every 128 columns
+  if (C > 1 && few * C <= warps) {
+    const int row = i / C % per, col = i % C * 128 + lane * 4;
+    if (i < few * C && row < j.rows) {
+      JoinSum<1> s;
+      join_pieces(p, j, row, col, 0, 1, s);
+      join_store<T>(p, j, row, col, s);
     }
-    j = next;
+  } else {
+    if (C > 1) j = load_join(p.space.join + min(i / per, shares - 1));
+    while (i < few) {
+      const int row = i % per;
+      i += warps;
+      const ShareJoin next = load_join(p.space.join + min(i / per, shares - 1));
+      if (row < j.rows && live) {
+        JoinSum<C> s;
+        join_pieces(p, j, row, lane * 4, 0, 1, s);
+        join_store<T>(p, j, row, lane * 4, s);
+      }
+      j = next;
+    }
   }
   // of many: 32 columns a CTA; a warp takes four pieces at once, eight lanes each
   for (i = blockIdx.x; i < many;) {

@@ -26,7 +26,7 @@ namespace pa {
 // Ints of the status block: shares taken, units to join of few and of many
 // pieces, join CTAs done.
 constexpr int kShareTaken = 16, kShareFew = 17, kShareMany = 18, kShareDone = 19;
-constexpr int kJoinFew = 32; // pieces that one warp joins by itself
+constexpr int kJoinFew = 64; // pieces that one warp joins by itself
 
 // A unit whose keys lie in several shares: parts pieces (place 1 of `share`,
 // then place 0 of the next shares, `by` apart), each of `rows` rows.  Row r
