@@ -122,23 +122,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
-// The same for waits that stand in a chain of short steps: the barrier is looked
-// at all the time, the clock (whose read takes longer than such a step) now and
-// then.
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                          const volatile int *abort) {
-  uint64_t t0 = 0;
-  while (true) {
-#pragma unroll 1
-    for (int k = 0; k < 64; ++k)
-      if (mbar_test(bar, parity)) return true;
-    if (abort && *abort) return false;
-    const uint64_t t = globaltimer_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) return false;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // TMA: one 2-D tile of the cache (box = 128 bytes x rows) into shared memory,
 // completing on an mbarrier with a byte count.
@@ -171,13 +154,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
-}
-// The same tile from HBM into L2 only.
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
 }
 __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap *map, int x, int y,
                                                  int z, uint32_t bar, uint64_t policy) {

@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       const int share = item / p.side;
       walk.begin(batch, sh.scan, plan.begin(share), share < plan.big ? plan.begin(share + 1) : 0);
     }
-    // the last tile of the line
+    // the tile whose table entries are on their way
     LatentStage f{};
-    int f_left = 0, f_end = 0, y = -1;
+    int f_left = 0, f_end = 0, ent = -1;
     const int32_t *table = p.block_tables;
     auto fetch = [&]() {
       if (f_left == 0) {
@@ -283,61 +283,53 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       }
       if (--f_left == 0) f.flags |= kLatentLast;
       f.valid = max(min(f_end - f.tok0, kLatentKeys), 0);
-      // rows of pages: unit_rows of them a copy, each panel of 8 rows one swizzle atom
-      const int tok = f.tok0 + lane * U;
-      y = -1;
-      if (lane * U < f.valid) {
-        const int ent = __ldg(table + (tok >> p.log2_block_size));
-        if ((unsigned)ent >= (unsigned)p.num_blocks)
-          report(p.status, kStatusBadInput);
-        else
-          y = ent * p.block_size + (tok & (p.block_size - 1));
-      }
+      ent = lane * U < f.valid ? __ldg(table + ((f.tok0 + lane * U) >> p.log2_block_size)) : -1;
     };
-    // Tiles stand in line two ahead of their copies, and are on their way to L2
-    // meanwhile: the ring holds two, which stay until they are done with, and HBM
-    // would rest until then.
-    LatentStage line[2];
-    int line_y[2];
     fetch();
-    line[0] = f;
-    line_y[0] = y;
     bool ok = true;
     int i = 0, nq = 0;
     while (true) {
       const int sl = i % NS;
-      const LatentStage h = line[0];
-      const int hy = line_y[0];
       if (i >= NS) {
         bool w = true;
-        if (lane == 0) w = mbar_poll(empty + 8 * sl, ((i / NS) - 1) & 1, limit, flags);
+        if (lane == 0) w = mbar_wait(empty + 8 * sl, ((i / NS) - 1) & 1, limit, flags);
         ok = __shfl_sync(0xffffffffu, w, 0);
         if (!ok) break;
       }
-      if (h.flags & kLatentEnd) {
+      if (f.flags & kLatentEnd) {
         if (lane == 0) {
-          sh.info[sl] = h;
+          sh.info[sl] = f;
           mbar_arrive(full + 8 * sl);
         }
         ++i;
         break;
       }
-      const unsigned on = __ballot_sync(0xffffffffu, hy >= 0);
+      // rows of pages: unit_rows of them a copy, each panel of 8 rows one swizzle atom
+      const int tok = f.tok0 + lane * U;
+      int y = -1;
+      if (lane * U < f.valid) {
+        if ((unsigned)ent >= (unsigned)p.num_blocks)
+          report(p.status, kStatusBadInput);
+        else
+          y = ent * p.block_size + (tok & (p.block_size - 1));
+      }
+      const unsigned on = __ballot_sync(0xffffffffu, y >= 0);
       if (lane == 0) {
-        sh.info[sl] = h;
+        sh.info[sl] = f;
         mbar_arrive_expect_tx(full + 8 * sl, (uint32_t)__popc(on) * U * 128u * NP);
       }
       __syncwarp();
-      if (hy >= 0)
+      if (y >= 0)
         tma_load_4d(ring_u32 + (uint32_t)sl * Z::SLOT + (uint32_t)(lane * U / 8) * Z::GROUP, &tmap_c, 0, 0, 0,
-                    hy >> 3, full + 8 * sl);
-      const bool first = h.flags & kLatentFirst;
-      const int row0 = h.row0;
+                    y >> 3, full + 8 * sl);
+      const bool first = f.flags & kLatentFirst;
+      const int row0 = f.row0;
       ++i;
+      fetch();
       if (first) {  // the piece's queries, once the last one's have been read
         if (nq >= 1) {
           bool w = true;
-          if (lane == 0) w = mbar_poll(q_empty, (nq - 1) & 1, limit, flags);
+          if (lane == 0) w = mbar_wait(q_empty, (nq - 1) & 1, limit, flags);
           ok = __shfl_sync(0xffffffffu, w, 0);
           if (!ok) break;
         }
@@ -346,19 +338,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         if (lane < NP) tma_load_2d(q_u32 + lane * 8192u, &tmap_q, lane * 64, row0, q_full);
         ++nq;
       }
-      if (i == 1) {  // (the first copy did not wait for the tiles behind it)
-        if (!(f.flags & kLatentEnd)) fetch();
-        line[1] = f;
-        line_y[1] = y;
-      }
-      line[0] = line[1];
-      line_y[0] = line_y[1];
-      if (!(f.flags & kLatentEnd)) {
-        fetch();
-        if (!(f.flags & kLatentEnd) && y >= 0) tma_prefetch_4d(&tmap_c, 0, 0, 0, y >> 3);
-      }
-      line[1] = f;
-      line_y[1] = y;
     }
     if (!ok && lane == 0) {
       report(p.status, kStatusTimeout);
@@ -380,7 +359,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const uint64_t q_desc = smem_desc(q_u32, 16, 1024), k_desc = smem_desc(ring_u32, 16, Z::GROUP);
     const uint64_t v_desc = smem_desc(ring_u32, 1024, Z::GROUP), p_desc = smem_desc(p_u32, 16, 1024);
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-      const bool w = mbar_poll(bar, parity, limit, flags);
+      const bool w = mbar_wait(bar, parity, limit, flags);
       ok = __all_sync(0xffffffffu, w);
       return ok;
     };
@@ -457,7 +436,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         sh.vote[gx & 1][warp] = v;
         mbar_arrive(grp);
       }
-      const bool w = mbar_poll(grp, (uint32_t)(gx & 1), limit, flags);
+      const bool w = mbar_wait(grp, (uint32_t)(gx & 1), limit, flags);
       ok = __all_sync(0xffffffffu, w);
       const volatile int *a = sh.vote[gx & 1];
       ++gx;
@@ -467,7 +446,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       return r;
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      const bool w = mbar_poll(bar, parity, limit, flags);
+      const bool w = mbar_wait(bar, parity, limit, flags);
       ok = __all_sync(0xffffffffu, w);
       return ok;
     };
