@@ -19,14 +19,15 @@
 // 128.  More rows a CTA do not fit: 64 rows of queries are 72 KB, a tile of 64
 // keys 72 KB, and two tiles have to be there for copies to run beside MMAs.
 //
-// A softmax thread holds two rows (of 64) by 8 keys in registers, as the MMA
-// fragments have it; a quad of threads has half a row.  The maximum in use is
-// raised only when a score passes it by 2^8 (weights then stay far from
-// overflow, and their relative precision does not depend on the reference): the
-// warps vote on it, as all of them hold part of every row's O^T.
+// A softmax warp has eight rows, four threads a row (16 keys each, as the MMA
+// fragments have them), so a row's maximum and sum are its own.  The maximum in
+// use is raised only when a score passes it by 2^8 (weights then stay far from
+// overflow, and their relative precision does not depend on the reference).  A
+// warp that raises goes on with the new one and leaves word with its weights;
+// the MMA warp then holds O^T's MMAs back until all warps, each of which has
+// every row in its lanes of O^T, have brought O^T down to it.
 //
-// Warps: 0-7 softmax and output (four lanes' quarters by two halves of a tile's
-// keys), 8 producer (the walk over the shares, TMA), 9 MMA issuer.  One CTA an
+// Warps: 0-7 softmax and output (two to a quarter of the lanes), 8 producer (the walk over the shares, TMA), 9 MMA issuer.  One CTA an
 // SM; work is cut in shares (pa_share.cuh), a CTA's each; every wait is bounded.
 // Loops that issue MMAs are rolled and stand once: an SM fetches code that it
 // has not run at some 250 cycles an MMA (the first tile took 13,000 cycles with
@@ -96,9 +97,10 @@ struct LatentShared {
   uint8_t q[Z::QBYTES];
   uint8_t ring[Z::SLOTS][Z::SLOT];
   uint8_t p[Z::PBYTES];
-  float part[2][kLatentRows];  // the two halves' maxima of a row (a rescale) or sums (a unit's end)
+  float alpha[kLatentRows];   // factors of rows whose maximum was raised
+  float sum[2][kLatentRows];  // (pieces in turn) the rows' sums
   LatentStage info[Z::SLOTS];
-  int vote[2][kLatentSoftmax];
+  alignas(8) uint8_t raised[2][kLatentSoftmax];  // (tiles in turn) whether a warp raised any
   uint64_t bars[Z::NBARS];
   int flags[2];
   uint32_t tmem;
@@ -136,12 +138,29 @@ struct LatentBatch {
   }
 };
 
-// 16 lanes by 32 columns of tensor memory, as MMA fragments: thread t has rows
+// 16 lanes by 64 columns of tensor memory, as MMA fragments: thread t has rows
 // t / 4 and t / 4 + 8, columns 8 j + 2 (t % 4) + {0, 1}: words 4 j + {0, 1} and + {2, 3}
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                : "r"(taddr));
+}
+// 8 columns of this warp's 32 lanes (lane = thread), the load with its wait
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ bool any_raised(const uint8_t *r) {
+  static_assert(kLatentSoftmax == 8, "eight flags in a word");
+  return *reinterpret_cast<const volatile unsigned long long *>(r) != 0;
 }
 
 }  // namespace
@@ -170,7 +189,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   volatile int *flags = sh.flags;
   const uint32_t full = smem_u32(sh.bars), empty = full + 8 * NS, q_full = empty + 8 * NS, q_empty = q_full + 8,
                  s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 8, o_done = pv_done + 8,
-                 grp = o_done + 8, drain = grp + 8, never = drain + 8;
+                 rescaled = o_done + 8, drain = rescaled + 8, never = drain + 8;
   const uint32_t q_u32 = smem_u32(sh.q), ring_u32 = smem_u32(sh.ring), p_u32 = smem_u32(sh.p);
   const uint64_t limit = p.wait_limit_ns;
 
@@ -186,7 +205,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     mbar_init(p_full, kLatentSoftmax);
     mbar_init(pv_done, 1);
     mbar_init(o_done, 1);
-    mbar_init(grp, kLatentSoftmax);
+    mbar_init(rescaled, kLatentSoftmax);
     mbar_init(drain, 1);
     mbar_init(never, 1);
     sh.flags[0] = 0;
@@ -355,7 +374,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     // uniform registers; one elected lane issues.
     const uint32_t leader = elect_one();
     bool ok = true;
-    int nq = 0;  // pieces whose queries S has taken
+    int nq = 0, nr = 0;  // pieces whose queries S has taken, rescales
     const uint64_t q_desc = smem_desc(q_u32, 16, 1024), k_desc = smem_desc(ring_u32, 16, Z::GROUP);
     const uint64_t v_desc = smem_desc(ring_u32, 1024, Z::GROUP), p_desc = smem_desc(p_u32, 16, 1024);
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -399,6 +418,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       }
       if (!ok || end) break;
       if (!wait(p_full, i & 1)) break;
+      if (any_raised(sh.raised[i & 1]) && !wait(rescaled, nr++ & 1)) break;
       tc_fence_after();
       const uint64_t da = v_desc + (uint32_t)(i % NS) * (uint32_t)(Z::SLOT >> 4);
 #pragma unroll 1
@@ -422,29 +442,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     __syncwarp();
   } else {
     // ======================= softmax warps =======================
-    // thread: rows ra = 16 quarter + lane / 4 and ra + 8, keys 32 half + 8 j + 2 (lane % 4) + {0, 1}
+    // thread: row 16 quarter + 8 half + lane / 4, keys 8 j + 2 (lane % 4) + {0, 1}
     const int quarter = warp & 3, half = warp >> 2;
-    const int t = threadIdx.x, q4 = lane & 3, ra = 16 * quarter + (lane >> 2), key0 = 32 * half + 2 * q4;
+    const int t = threadIdx.x, q4 = lane & 3, row = 16 * quarter + 8 * half + (lane >> 2);
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    float m[2] = {kLatentNone, kLatentNone}, l[2] = {0.f, 0.f};
-    int lim[2] = {0, 0}, pieces = 0, gx = 0;
+    float m = kLatentNone, l = 0.f;
+    int lim = 0, pieces = 0;
     bool ok = true;
-    // a vote (or a meeting) of the warps, after a bounded wait: their words, or'ed
-    auto meet = [&](int v) -> int {
-      __syncwarp();  // what its lanes wrote, or read of the last meeting, is done
-      if (lane == 0) {
-        sh.vote[gx & 1][warp] = v;
-        mbar_arrive(grp);
-      }
-      const bool w = mbar_wait(grp, (uint32_t)(gx & 1), limit, flags);
-      ok = __all_sync(0xffffffffu, w);
-      const volatile int *a = sh.vote[gx & 1];
-      ++gx;
-      int r = 0;
-#pragma unroll
-      for (int k = 0; k < kLatentSoftmax; ++k) r |= a[k];
-      return r;
-    };
     auto wait = [&](uint32_t bar, uint32_t parity) {
       const bool w = mbar_wait(bar, parity, limit, flags);
       ok = __all_sync(0xffffffffu, w);
@@ -459,95 +463,51 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       if (h.flags & kLatentEnd) break;
       if (lane == 0) mbar_arrive(empty + 8 * sl);  // done with the header
       if (h.flags & kLatentFirst) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = ra + 8 * e;
-          lim[e] = r < h.rows ? h.lim_base + (h.flat0 + r) / p.num_heads + 1 : 0;
-          m[e] = kLatentNone;
-          l[e] = 0.f;
-        }
+        lim = row < h.rows ? h.lim_base + (h.flat0 + row) / p.num_heads + 1 : 0;
+        m = kLatentNone;
+        l = 0.f;
       }
       if (!wait(s_full + 8 * (i & 1), (i >> 1) & 1)) break;
       tc_fence_after();
-      uint32_t sr[16];
-      tmem_ld_frag(tmem_s + 64u * (uint32_t)(i & 1) + 32u * (uint32_t)half + lane_off, sr);
-      tmem_ld_wait16(sr);
-      float x[16];
-      float top[2] = {kLatentNone, kLatentNone};
+      uint32_t sr[32];
+      tmem_ld_frag(tmem_s + 64u * (uint32_t)(i & 1) + lane_off, sr);
+      tmem_ld_wait(sr);
+      float x[16], top = kLatentNone, al = 1.f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(sr[k]) * p.scale_log2;
-      if (h.valid < kLatentKeys || h.tok0 + kLatentKeys > min(lim[0], lim[1])) {
+      for (int k = 0; k < 16; ++k) {
+        const int j = 4 * (k >> 1) + (k & 1);
+        x[k] = __uint_as_float(half ? sr[j + 2] : sr[j]) * p.scale_log2;
+      }
+      if (h.valid < kLatentKeys || h.tok0 + kLatentKeys > lim) {
+        const int end = min(h.valid, lim - h.tok0) - 2 * q4;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int key = key0 + 8 * (k >> 2) + (k & 1);
-          if (key >= h.valid || h.tok0 + key >= lim[(k >> 1) & 1]) x[k] = -CUDART_INF_F;
-        }
+        for (int k = 0; k < 16; ++k)
+          if (8 * (k >> 1) + (k & 1) >= end) x[k] = -CUDART_INF_F;
       }
 #pragma unroll
-      for (int k = 0; k < 16; k += 4) {
-        top[0] = fmax3(top[0], x[k], x[k + 1]);
-        top[1] = fmax3(top[1], x[k + 2], x[k + 3]);
+      for (int k = 0; k < 16; k += 2) top = fmax3(top, x[k], x[k + 1]);
+      const bool raise = __any_sync(0xffffffffu, top > m + kMargin);
+      if (raise) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), m);
+        al = ex2(m - top);
+        m = top;
+        l *= al;
       }
-      const bool up = top[0] > m[0] + kMargin || top[1] > m[1] + kMargin;
-      if (meet(__any_sync(0xffffffffu, up)) != 0 && ok) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-          if (q4 == 0) sh.part[half][ra + 8 * e] = fmaxf(top[e], m[e]);
-        }
-        meet(0);  // the maxima of both halves are there
-        if (!ok) break;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float v = fmaxf(sh.part[0][ra + 8 * e], sh.part[1][ra + 8 * e]);
-          const float al = ex2(m[e] - v);
-          m[e] = v;
-          l[e] *= al;
-          top[e] = al;
-        }
-        meet(0);  // (they are read)
-        if (!ok) break;
-        if (!(h.flags & kLatentFirst)) {
-          if (half == 0 && q4 == 0) sh.part[0][ra] = top[0], sh.part[0][ra + 8] = top[1];
-          meet(0);  // the rows' factors are there
-          // O^T's lanes and half of its rows, once the MMAs of the tile before are done
-          if (!ok || !wait(pv_done, (i - 1) & 1)) break;
-          tc_fence_after();
-          const float *al = sh.part[0] + 32 * half;
-#pragma unroll 1
-          for (int j = 0; j < Z::NT; ++j) {
-            const uint32_t at = tmem_o + 64u * (uint32_t)j + 32u * (uint32_t)half + lane_off;
-            uint32_t o[32];
-            tmem_ld32(at, o);
-            tmem_ld_wait(o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k]);
-            tmem_st32(at, o);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          meet(0);  // (before anyone writes there again)
-          if (!ok) break;
-        }
-      }
-      if (!ok) break;
       // weights, rounded to the input type; the sums take them as rounded
       uint32_t w[8];
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
-        const int e = (k >> 1) & 1;
-        w[k / 2] = MmaOp<T>::pack(ex2(x[k] - m[e]), ex2(x[k + 1] - m[e]));
+        w[k / 2] = MmaOp<T>::pack(ex2(x[k] - m), ex2(x[k + 1] - m));
         const float2 r = MmaOp<T>::unpack(w[k / 2]);
-        l[e] += r.x + r.y;
+        l += r.x + r.y;
       }
       // into P's tile, which the MMAs of the tile before have read
       if (i >= 1 && !wait(pv_done, (i - 1) & 1)) break;
+      if (raise && q4 == 0) sh.alpha[row] = al;  // (those of the tile before have been used)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = ra + 8 * (k & 1), c = 4 * half + (k >> 1);  // row, 16-byte piece of eight keys
-        *reinterpret_cast<uint32_t *>(sh.p + r * 128 + ((c ^ (r & 7)) << 4) + 4 * q4) = w[k];
-      }
+      for (int k = 0; k < 8; ++k)  // 16-byte piece k: eight keys
+        *reinterpret_cast<uint32_t *>(sh.p + row * 128 + ((k ^ (row & 7)) << 4) + 4 * q4) = w[k];
       // rows of keys that are not the item's may hold anything (0 x NaN would reach O^T)
       if (h.valid < kLatentKeys) {
         uint8_t *v = sh.ring[sl];
@@ -558,33 +518,54 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                                      (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
+      if (h.flags & kLatentLast) {
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (q4 == 0) {
+          sh.sum[pieces & 1][row] = l;
+          if (h.place >= 0 && row < h.rows)
+            space.ml[(size_t)h.place * kLatentRows + row] = make_float2(m, l);
+        }
+      }
+      if (lane == 0) sh.raised[i & 1][warp] = raise && !(h.flags & kLatentFirst);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
+      // what the other warps left with their weights
+      if (!wait(p_full, i & 1)) break;
+      if (any_raised(sh.raised[i & 1])) {
+        // O^T (its MMAs of the tile before are done, those of this one wait): this
+        // warp's lanes, half of the rows, eight rows of a warp that raised at a time
+        tc_fence_after();
+#pragma unroll 1
+        for (int g = 4 * half; g < 4 * half + 4; ++g) {
+          if (!*const_cast<volatile uint8_t *>(&sh.raised[i & 1][(g >> 1) + 4 * (g & 1)])) continue;
+          const float4 a0 = *reinterpret_cast<const float4 *>(sh.alpha + 8 * g);
+          const float4 a1 = *reinterpret_cast<const float4 *>(sh.alpha + 8 * g + 4);
+          const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll 1
+          for (int j = 0; j < Z::NT; ++j) {
+            const uint32_t at = tmem_o + 64u * (uint32_t)j + 8u * (uint32_t)g + lane_off;
+            uint32_t o[8];
+            tmem_ld8(at, o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k]);
+            tmem_st8(at, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rescaled);
+      }
       if (h.flags & kLatentLast) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-          l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-          if (q4 == 0) sh.part[half][ra + 8 * e] = l[e];
-        }
-        meet(0);  // every row's sums are there
-        if (!ok) break;
-        if (h.place >= 0 && half == 0 && q4 == 0) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (ra + 8 * e < h.rows)
-              space.ml[(size_t)h.place * kLatentRows + ra + 8 * e] =
-                  make_float2(m[e], sh.part[0][ra + 8 * e] + sh.part[1][ra + 8 * e]);
-        }
         if (!wait(o_done, pieces & 1)) break;
-        ++pieces;
         tc_fence_after();
         const int r0 = 32 * half;
         if (r0 < h.rows) {
-          float inv = sh.part[0][r0 + lane] + sh.part[1][r0 + lane];  // (lane: a row)
-          inv = inv == 0.f ? 0.f : 1.f / inv;
+          const float sum = sh.sum[pieces & 1][r0 + lane];  // (lane: a row)
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
           for (int j = 0; j < Z::NT; ++j) {
             const int d = 128 * j + 32 * quarter + lane;
@@ -606,9 +587,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
           }
         }
-        tc_fence_before();
-        meet(0);  // (before anyone writes sums again)
-        if (!ok) break;
+        ++pieces;
+        tc_fence_before();  // (before this warp's next weights let O^T be written)
       }
     }
     if (!ok && lane == 0) {
