@@ -19,8 +19,14 @@
 // Weights: the product takes w = p st in f16, so it must neither overflow nor
 // vanish with st: with S the larger of a token's steps, the running maximum is
 // that of x + log2 S (x: score in log2 units), p' = 2^(x + log2 S - m), and a
-// group's w = p' st / S.  The normaliser sum(p' / S) and the part of lo,
-// sum(p' lo / S), are summed in fp32.  w is off by at most 2^-12 of itself.
+// group's w = p' st / S.  The normaliser sum(p' / S) is summed in fp32.  w is off
+// by up to 2^-12 of itself, which must not meet codes of 0 to 15 (a value is what
+// is left of lo and them, so its error would be three times that of weights
+// against values), but codes about their middle: with w' the rounded weights,
+//   sum_t p_t V_t = sum_t w'_t c_t - 7.5 sum_t w'_t + sum_t (p' / S) (lo + 7.5 st)
+// the last in fp32, sum(w') by one more MMA a group, against - 7.5 in row 0.
+// (Without it f16 outputs were off by 0.00056 of themselves, 0.00021 being their
+// own rounding's part; it costs 2 %.)
 //
 // Layout: S^T[16 tokens][8 heads] = K Q^T and O^T[D][8 heads] += V^T P^T
 // (mma.sync m16n8k16, f16), a warp 16 tokens at a time.
@@ -68,6 +74,7 @@ struct alignas(16) Q4Piece {
   int share, parts;   // parts: the shares that the unit lies in, with its first piece
   int pad[2];
 };
+constexpr float kMiddle = 7.5f;       // of the codes
 constexpr int kQ4Pieces = 8;  // handed over and not yet taken: at most stages + 1
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -347,6 +354,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) issue((uint32_t)(i * Z::STAGE));
 
+  const uint32_t middle = g == 0 ? 0xc780c780u : 0u;  // (f16) -kMiddle
   // ---- the tiles
   uint4 qf[Z::QSMEM ? 1 : NT][Z::QSMEM ? 1 : CPR];  // Q^T fragments of two k-steps
   float qsum[NT][NG][2];  // scale x the sum of the group's q, of this lane's columns
@@ -553,8 +561,9 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
         const uint32_t vrow = stage_u32 + Z::VALUES + 16 * RB * h;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          const float la = va[h][gr].x * inv_a[h], lb = vb[h][gr].x * inv_b[h];
           const float wa = va[h][gr].y * inv_a[h], wb = vb[h][gr].y * inv_b[h];
+          float la = va[h][gr].x * inv_a[h], lb = vb[h][gr].x * inv_b[h];
+          la = fmaf(kMiddle, wa, la), lb = fmaf(kMiddle, wb, lb);
           uint32_t pf[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -563,6 +572,10 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
             sb[nt][gr][1] = fmaf(y[1], la, fmaf(y[3], lb, sb[nt][gr][1]));
             pf[nt][0] = movmatrix_trans(MmaOp<__half>::pack(y[0] * wa, y[1] * wa));
             pf[nt][1] = movmatrix_trans(MmaOp<__half>::pack(y[2] * wb, y[3] * wb));
+            // - 7.5 sum(w), to the lanes of row 0
+            float d[4] = {sb[nt][gr][0], sb[nt][gr][1], 0.f, 0.f};
+            MmaOp<__half>::run(d, middle, 0u, middle, 0u, pf[nt][0], pf[nt][1]);
+            sb[nt][gr][0] = d[0], sb[nt][gr][1] = d[1];
           }
           // units of four codes: tokens 2t, 2t + 1 | the eight behind, pieces 2 gr, 2 gr + 1
           uint32_t w[4];
