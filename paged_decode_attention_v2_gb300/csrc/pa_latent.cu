@@ -49,6 +49,7 @@ namespace {
 
 constexpr int kLatentRows = 64;   // query rows of a unit
 constexpr int kLatentKeys = 64;   // keys of a step
+constexpr int kLatentHead = 2;     // tiles' time that a piece's beginning and end take
 constexpr int kLatentSoftmax = 8;  // warps
 constexpr int kLatentThreads = 32 * (kLatentSoftmax + 2);
 constexpr int kLatentMaxCtas = 152;
@@ -128,7 +129,7 @@ struct LatentBatch {
     return r;
   }
   __device__ __forceinline__ ShareSeq seq(const int4 &r) const {
-    ShareSeq q{r.x, r.y, r.z, 0, 0};
+    ShareSeq q{r.x, r.y, r.z, 0, 0, kLatentHead};
     q.steps = (r.x + kLatentKeys - 1) / kLatentKeys;
     if (q.steps > 0) {
       const int groups = (int)(((long long)r.z * p.num_heads + kLatentRows - 1) / kLatentRows);
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
           }
           // the piece's row group of this CTA; a unit's last may have none beside
           const int group = walk.unit * p.side + item % p.side;
-          const int n = walk.piece(), step = walk.step;
+          const int n = walk.steps(), step = walk.first();
           const int flat0 = group * kLatentRows, all = walk.q.n * p.num_heads;
           if (flat0 < all) {
             f.flat0 = flat0;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             if (begins && !ends && lane == 0) {
               ShareJoin j{};
               j.share = item;
-              j.parts = plan.of(walk.line + walk.q.steps - 1) - item / p.side + 1;
+              j.parts = plan.of(walk.last()) - item / p.side + 1;
               j.by = p.side;
               j.rows = f.rows;
               j.group = j.stride = 1;

@@ -74,6 +74,7 @@ struct alignas(16) Q4Piece {
   int share, parts;   // parts: the shares that the unit lies in, with its first piece
   int pad[2];
 };
+constexpr int kQ4Head = 3;         // tiles' time that a piece's beginning and end take
 constexpr float kMiddle = 7.5f;       // of the codes
 constexpr int kQ4Pieces = 8;  // handed over and not yet taken: at most stages + 1
 
@@ -178,7 +179,7 @@ struct Q4Batch {
     return r;
   }
   __device__ __forceinline__ ShareSeq seq(const int4 &r) const {
-    ShareSeq q{r.x, r.y, r.z, 0, 0};
+    ShareSeq q{r.x, r.y, r.z, 0, 0, kQ4Head};
     q.steps = (r.x + step - 1) / step;  // (at most 2^30 keys)
     if (q.steps > 0)
       q.units = p.q_start ? p.num_kv_heads * ((r.z + p.chunk_tokens - 1) / p.chunk_tokens) : p.num_kv_heads;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
     Q4Piece u{};
     u.dest = kQ4End;
     if (walk.left > 0) {
-      const int n = walk.piece(), step = walk.step;
+      const int n = walk.steps(), step = walk.first();
       u.kvh = walk.unit;
       u.rows = p.group;
       u.row0 = walk.s;
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
       u.steps = n;
       u.share = share;
       u.tok = step * Z::TOKENS;
-      if (u.dest == kQ4Place1) u.parts = plan.of(walk.line + walk.q.steps - 1) - share + 1;
+      if (u.dest == kQ4Place1) u.parts = plan.of(walk.last()) - share + 1;
       // (its queries on their way to L2)
 #pragma unroll
       for (int i = lane; i < GM * (D / 64); i += 32) {
