@@ -14,10 +14,19 @@
 //
 // Bound: a row of 576 elements is 1152 bytes and 2 (576 + 512) flops a head.
 // To 64 heads HBM bounds it.  128 heads are two groups of rows, taken by two
-// CTAs that walk the same keys at the same time (the second finds them in L2);
-// there the MMAs are next to the limit: S has M = 64, which takes the time of
-// 128.  More rows a CTA do not fit: 64 rows of queries are 72 KB, a tile of 64
-// keys 72 KB, and two tiles have to be there for copies to run beside MMAs.
+// CTAs that walk the same keys at the same time; there the MMAs are next to the
+// limit: S has M = 64, which takes the time of 128.  More rows a CTA do not fit:
+// 64 rows of queries are 72 KB, a tile of 64 keys 72 KB, and two tiles have to be
+// there for copies to run beside MMAs.
+//
+// Measured on GB300: one sequence of 100000 keys, 16 heads: 40 us (17 at the
+// bytes' rate; 10 of them the beginning and the join); 64 sequences of 1024 to
+// 8192 keys, 128 heads: 144 us, 2.5 TB/s and 580 TFLOP/s.  There a tile takes
+// 3700 cycles, 2550 of them MMAs: with two tiles in the ring its copy (2300
+// cycles; 1000 when an SM's own side of L2 has it), S, the softmax (900) and O^T
+// stand behind one another.  Slower were: tiles in parts that are copied, used
+// and given back by themselves (162), tiles sent to L2 ahead of their copies
+// (146), waits that look all the time (162).
 //
 // A softmax warp has eight rows, four threads a row (16 keys each, as the MMA
 // fragments have them), so a row's maximum and sum are its own.  The maximum in
@@ -27,12 +36,12 @@
 // the MMA warp then holds O^T's MMAs back until all warps, each of which has
 // every row in its lanes of O^T, have brought O^T down to it.
 //
-// Warps: 0-7 softmax and output (two to a quarter of the lanes), 8 producer (the walk over the shares, TMA), 9 MMA issuer.  One CTA an
-// SM; work is cut in shares (pa_share.cuh), a CTA's each; every wait is bounded.
+// Warps: 0-7 softmax and output (two to a quarter of the lanes), 8 producer (the
+// walk over the shares, TMA), 9 MMA issuer.  One CTA an SM; work is cut in shares
+// (pa_share.cuh), a CTA's each; every wait is bounded.
 // Loops that issue MMAs are rolled and stand once: an SM fetches code that it
 // has not run at some 250 cycles an MMA (the first tile took 13,000 cycles with
 // three unrolled copies).
-#include <limits.h>
 #include <math.h>
 #include <math_constants.h>
 
@@ -53,7 +62,7 @@ constexpr int kLatentHead = 2;     // tiles' time that a piece's beginning and e
 constexpr int kLatentSoftmax = 8;  // warps
 constexpr int kLatentThreads = 32 * (kLatentSoftmax + 2);
 constexpr int kLatentMaxCtas = 152;
-constexpr int kLatentShares = 320;  // shares x groups of rows that a workspace has places for
+constexpr int kLatentShares = 192;  // that a workspace has places for: a CTA's each
 constexpr float kLatentNone = -3.402823466e38f;  // the maximum of no keys
 
 constexpr int kLatentFirst = 1, kLatentLast = 2, kLatentEnd = 4;
@@ -238,14 +247,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     SharePlan plan;
     // (large shares alone: a piece's rows are up to 128 KB, and more pieces took more
     // than they evened out: 168 -> 160 us for 64 sequences with 128 heads)
-    plan.make(sh.scan.cum[128], (int)gridDim.x / p.side, INT_MAX);
+    plan.make(sh.scan.cum[128], (int)gridDim.x / p.side, true);
     // an item: a share, for one of the row groups that stand side by side
-    int item = blockIdx.x;
+    const int item = blockIdx.x, share = item / p.side;
     ShareWalk walk{};
-    {
-      const int share = item / p.side;
-      walk.begin(batch, sh.scan, plan.begin(share), share < plan.big ? plan.begin(share + 1) : 0);
-    }
+    walk.begin(batch, sh.scan, plan.begin(share), share < plan.big ? plan.begin(share + 1) : 0);
     // the tile whose table entries are on their way
     LatentStage f{};
     int f_left = 0, f_end = 0, ent = -1;
@@ -253,16 +259,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     auto fetch = [&]() {
       if (f_left == 0) {
         while (true) {
-          if (walk.left <= 0 && plan.small > 0) {
-            int k = 0;
-            if (lane == 0) k = atomicAdd(space.counters + kShareTaken, 1) & 0x3fffffff;
-            k = __shfl_sync(0xffffffffu, k, 0);
-            if (k < plan.small * p.side) {
-              item = plan.big * p.side + k;
-              const int share = item / p.side;
-              walk.begin(batch, sh.scan, plan.begin(share), plan.begin(share + 1));
-            }
-          }
           if (walk.left <= 0) {
             f.flags = kLatentEnd;
             return;
@@ -282,7 +278,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             if (begins && !ends && lane == 0) {
               ShareJoin j{};
               j.share = item;
-              j.parts = plan.of(walk.last()) - item / p.side + 1;
+              j.parts = plan.of(walk.last()) - share + 1;
               j.by = p.side;
               j.rows = f.rows;
               j.group = j.stride = 1;

@@ -42,7 +42,6 @@
 // what a warp has of a unit leaves from its registers.  (Four warps that shared
 // a unit's tokens and merged at its end spent 4 us on each piece of a unit.)
 #include <cuda_runtime.h>
-#include <limits.h>
 #include <math.h>
 #include <math_constants.h>
 

@@ -5,10 +5,10 @@
 // A unit is what one item of rows reads: a sequence's keys, for one KV head
 // and one group of query rows.  The steps of all units stand in one line, unit
 // behind unit, and a share is a stretch of the line, whatever units it cuts.
-// Every worker has a large share first, all equal; the rest of the line is cut
-// into small ones that the workers take from a counter as they get done, since
-// SMs do not run alike (with equal shares alone, CTAs of the same work ended
-// between 50 and 76 us).  A share has at most two units that it does not hold
+// Every worker has a large share first, all equal; where pieces are cheap and
+// there is work enough, the rest of the line is cut into small ones that the
+// workers take from a counter as they get done, since SMs do not run alike (with
+// equal shares alone, CTAs of the same work ended between 50 and 76 us).  A share has at most two units that it does not hold
 // whole, its first and its last, so the space for partial results is two
 // places a share, whatever the batch.  Every CTA works the shares out of the
 // lengths by itself: a scan over the sequences, which all CTAs do at once,
@@ -71,7 +71,7 @@ __device__ __forceinline__ long long div_steps(long long a, long long b) {
 }
 
 // The shares of a line of `total` steps: `big` equal ones over its first
-// big_total steps, `small` equal ones over the rest.
+// big_total steps, `small` equal ones over the rest (alone: large ones alone).
 constexpr int kShareSmall = 1;     // small shares for each large one,
 constexpr int kShareSmallPct = 35; // over this much of the line,
 constexpr int kShareTwo = 24;      // where there are this many steps a worker
@@ -79,12 +79,12 @@ constexpr int kShareLeast = 2;     // steps of a share where there are not enoug
 struct SharePlan {
   long long total, big_total;
   int big, small;
-  __device__ __forceinline__ void make(long long steps, int workers, int two = kShareTwo) {
+  __device__ __forceinline__ void make(long long steps, int workers, bool alone = false) {
     total = big_total = steps;
     const long long most = (steps + kShareLeast - 1) / kShareLeast;
     big = most < workers ? (int)most : workers;
     small = 0;
-    if (steps >= (long long)workers * two) {
+    if (!alone && steps >= (long long)workers * kShareTwo) {
       small = kShareSmall * workers;
       big_total = div_steps(steps, 100) * (100 - kShareSmallPct);
     }
