@@ -551,7 +551,7 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads,
  *                             half of byte i, 2i + 1 in the high half
  *   key_scales, value_scales  f16 [num_blocks][num_kv_heads][block_size]
  *                             [head_size / 64][2]: lo, step
- * A token takes 9/16 (72 of 128 bytes at head_size 128) of a byte an element,
+ * A token takes 9/16 of a byte an element (72 bytes at head_size 128 for a head),
  * scales included.  Keys are rotated and rounded to dtype as by pa_append_kv
  * (with the three operations of each element rounded apart), then coded; query
  * is rotated into query_out.  key_out, value_out [num_rows][num_kv_heads]

@@ -309,6 +309,17 @@ def test_long_and_many(H, L, lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,L,new", [(4, 256, False), (80, 512, False), (24, 512, True)])
+@pytest.mark.parametrize("lens", [[1] * 250 + [7000] + [2] * 40, [64] * 3, [100, 6000] + [5] * 60])
+def test_short_beside_long(H, L, new, lens):
+    """Shares that hold many whole units, parts of one, or end where a unit begins."""
+    c = Attend(8, torch.bfloat16, H, L, 16, lens, [min(n, 3) for n in lens] if new else None).device()
+    out = c.run()
+    c.check(out)
+    assert torch.equal(out, c.run())  # whoever takes which share
+
+
+@pytest.mark.gpu
 def test_peaked_scores():
     """Scores of +-1000, and none at all: maxima that rise late and by much."""
     for kw in (dict(qmult=8.0), dict(qmult=60.0), dict(qmult=0.0), dict(scale=-0.2)):

@@ -431,6 +431,31 @@ def test_long_and_many(lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,new", [(64, False), (128, False), (256, False), (128, True)])
+@pytest.mark.parametrize("lens", [[1] * 900 + [7000] + [2] * 40, [33, 6000] + [5] * 200, [16] * 3, [40, 31]])
+def test_short_beside_long(D, new, lens):
+    """Shares that hold many whole units, parts of one, or end where a unit begins."""
+    lens = lens if len(lens) < 300 or D == 64 else lens[600:]
+    c = Attend(8, torch.bfloat16, 4, 2, D, 16, lens, [min(L, 3) for L in lens] if new else None).device()
+    out = c.run()
+    c.check(out)
+    assert torch.equal(out, c.run())  # whoever takes which share
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_weights_are_rounded_against_the_middle_code(dtype):
+    """Values that are all 0, as code 7 above a lowest value of -28: weights that are off
+    by 2^-11 of themselves may give what they give half a code from the middle, not seven."""
+    c = Attend(9, dtype, 32, 2, 128, 16, [2, 3, 5, 40])
+    c.vc[:] = 0x77
+    c.vs[..., 0], c.vs[..., 1] = -28.0, 4.0
+    out = c.device().run()
+    # (and fp32's 2^-24 of terms up to 60, a few of them)
+    assert out.double().abs().max() <= 4 * 0.5 * 2 ** -11 + 60 * 2 ** -22
+
+
+@pytest.mark.gpu
 def test_peaked_and_far_scores():
     """Weights that one token has alone, scores of +-1000, keys far from zero, and no
     keys' spread at all: half the weight of the type's rounding, no overflow."""
