@@ -41,6 +41,12 @@
 // cp.async into its own ring of shared memory: no warp waits for another, and
 // what a warp has of a unit leaves from its registers.  (Four warps that shared
 // a unit's tokens and merged at its end spent 4 us on each piece of a unit.)
+//
+// Measured on GB300, bf16: 256 sequences of 512 to 3584 tokens, 32/4 heads, D 128:
+// 77 us (293 MB: 3.8 TB/s; 44 at the copy rate), one of 100,000 25 us (9), 64 of 16 to
+// 32,768, 16/2 heads, D 256, 41 us (16).  Half of the issue slots are used and hardly
+// a stall is memory's: it waits for its own steps, three warps a scheduler (two at
+// D 256) being what the registers hold.  Beginning and join are 10 us of each.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <math_constants.h>
@@ -74,6 +80,8 @@ struct alignas(16) Q4Piece {
   int pad[2];
 };
 constexpr int kQ4Head = 3;         // tiles' time that a piece's beginning and end take
+// (a small share always has steps: a warp that is given none takes no more)
+static_assert(kShareTwo * kShareSmallPct / (100 * kShareSmall) > kQ4Head, "small shares longer than a head");
 constexpr float kMiddle = 7.5f;       // of the codes
 constexpr int kQ4Pieces = 8;  // handed over and not yet taken: at most stages + 1
 
