@@ -30,8 +30,12 @@
 //
 // A softmax warp has eight rows, four threads a row (16 keys each, as the MMA
 // fragments have them), so a row's maximum and sum are its own.  The maximum in
-// use is raised only when a score passes it by 2^8 (weights then stay far from
-// overflow, and their relative precision does not depend on the reference).  A
+// use is raised only when a score passes it by 2^8.  Weights are rounded to the
+// input type (the MMA takes nothing wider): off by half a step, 2^-8 of themselves
+// at most in bf16; in f16 by 2^-11, or 2^-32 of the piece's largest where that is
+// more, as f16's start 2^7 above the maximum in use, which the sum takes out (a
+// weight below 2^-25 of it was lost, and the sum with it: 63 keys at 2^-26 with
+// values of 57344 gave 0 instead of 0.043).  The sum takes them as rounded.  A
 // warp that raises goes on with the new one and leaves word with its weights;
 // the MMA warp then holds O^T's MMAs back until all warps, each of which has
 // every row in its lanes of O^T, have brought O^T down to it.
@@ -64,6 +68,10 @@ constexpr int kLatentThreads = 32 * (kLatentSoftmax + 2);
 constexpr int kLatentMaxCtas = 152;
 constexpr int kLatentShares = 192;  // that a workspace has places for: a CTA's each
 constexpr float kLatentNone = -3.402823466e38f;  // the maximum of no keys
+constexpr float kLatentMargin = 8.f;  // log2 units
+// Weights are 2^(x - maximum in use + this): with the margin 2^15, below f16's largest
+template <typename T>
+constexpr float kLatentShift = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 constexpr int kLatentFirst = 1, kLatentLast = 2, kLatentEnd = 4;
 constexpr int kLatentDebugStall = 1;  // PA_DEBUG_STALL_CONSUMERS
@@ -184,8 +192,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
   constexpr int NP = Z::NP, NS = Z::SLOTS;
   constexpr uint32_t kIdescS = instr_desc<T>(kLatentRows, kLatentKeys, false, false);
   constexpr uint32_t kIdescO = instr_desc<T>(128, kLatentRows, false, true);
-  // f16 weights end at 65504; bf16 ones could go further, but need not
-  constexpr float kMargin = 8.f;
+  constexpr float kShift = kLatentShift<T>;
 
   // The 128-byte swizzle needs every tile 1024-byte aligned; the dynamic shared
   // memory starts so (there is no static part), which is checked.
@@ -443,7 +450,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const int quarter = warp & 3, half = warp >> 2;
     const int t = threadIdx.x, q4 = lane & 3, row = 16 * quarter + 8 * half + (lane >> 2);
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-    float m = kLatentNone, l = 0.f;
+    float m = kLatentNone, l = 0.f;  // m: 2^kShift below the maximum in use
     int lim = 0, pieces = 0;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -483,10 +490,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       }
 #pragma unroll
       for (int k = 0; k < 16; k += 2) top = fmax3(top, x[k], x[k + 1]);
-      const bool raise = __any_sync(0xffffffffu, top > m + kMargin);
+      // (rounded down, and the next reference up: no weight above 2^15 however far the scores)
+      const bool raise = __any_sync(0xffffffffu, top > __fadd_rd(m, kLatentMargin + kShift));
       if (raise) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), m);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = fmaxf(__fsub_ru(top, kShift), m);
         al = ex2(m - top);
         m = top;
         l *= al;

@@ -483,3 +483,24 @@ def test_decode_loop():
                 ref = torch.softmax(query[row].double() @ kv[:m].T * 0.06, -1) @ kv[:m, :L]
                 assert ((out[row].double() - ref).abs() <= ATOL + RTOL * ref.abs()).all()
                 row += 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,L,lens", [(5, 256, [640, 65]), (16, 512, [3000, 64]), (80, 512, [640, 1000])])
+def test_small_f16_weights(H, L, lens):
+    """Weights of 2^-26 beside one of 1, every 64 keys, whose values make up for it: f16's
+    smallest number is 2^-24.  A weight is off by 2^-32 of the largest at most."""
+    c = Attend(30, torch.float16, H, L, 16, lens, scale=1.0)
+    c.q.zero_()
+    c.q[..., L] = 1.0
+    for s, n in enumerate(lens):
+        t = torch.arange(n)
+        c.cache[c.bt[s, t // 16].long(), t % 16, :L] = 57344.0
+        c.cache[c.bt[s, t // 16].long(), t % 16, L] = -18.25
+        t = torch.arange(0, n, 64)
+        c.cache[c.bt[s, t // 16].long(), t % 16, :L] = 0.0
+        c.cache[c.bt[s, t // 16].long(), t % 16, L] = 0.0
+    ref = c.reference()
+    assert (ref > 0.02).all()
+    err = (c.device().run().double().cpu() - ref).abs()
+    assert (err <= 63 * 2 ** -32 * 57344 * 1.01 + (2 ** -11 + 2 ** -20) * ref).all(), float(err.max())
