@@ -19,10 +19,14 @@
 // Weights: the product takes w = p st in f16, so it must neither overflow nor
 // vanish with st: with S the larger of a token's steps, the running maximum is
 // that of x + log2 S (x: score in log2 units), p' = 2^(x + log2 S - m), and a
-// group's w = p' st / S.  The normaliser sum(p' / S) is summed in fp32.  w is off
-// by up to 2^-12 of itself, which must not meet codes of 0 to 15 (a value is what
-// is left of lo and them, so its error would be three times that of weights
-// against values), but codes about their middle: with w' the rounded weights,
+// group's w = p' st / S.  The normaliser sum(p' / S) is summed in fp32.  The
+// reference m is 2^7 below the maximum in use, which the sums take out: w is off
+// by up to 2^-11 of itself, or 2^-32 of the piece's largest where that is more,
+// f16 having no more numbers there.  (With weights from 1 down, those of a group
+// whose steps are 2^-23.4 of its head's largest were off by a third.)  That must
+// not meet codes of 0 to 15 (a value is what is left of lo and them, so its error
+// would be three times that of weights against values), but codes about their
+// middle: with w' the rounded weights,
 //   sum_t p_t V_t = sum_t w'_t c_t - 7.5 sum_t w'_t + sum_t (p' / S) (lo + 7.5 st)
 // the last in fp32, sum(w') by one more MMA a group, against - 7.5 in row 0.
 // (Without it f16 outputs were off by 0.00056 of themselves, 0.00021 being their
@@ -65,6 +69,7 @@ constexpr int kQ4Threads = kQ4Warps * 32;
 constexpr int kQ4MaxCtas = 4 * 152;                       // of a grid
 constexpr int kQ4Shares = (1 + kShareSmall) * kQ4MaxCtas * kQ4Warps;  // that a workspace has places for
 constexpr float kQ4Margin = 8.f;           // log2 units
+constexpr float kQ4Shift = 7.f;            // weights are 2^(x + log2 S - maximum in use + this): up to 2^15
 constexpr float kQ4LeastStep = 0x1p-24f;   // f16's smallest: stands in for a step of 0
 constexpr float kQ4None = -3.402823466e38f;  // the maximum of no keys
 
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
   float qsum[NT][NG][2];  // scale x the sum of the group's q, of this lane's columns
   float qmul[NT][2];      // what the columns' products are worth
   float o[NT][2 * CPR][4];  // O^T: row pairs (g, g + 8), columns 2t, 2t + 1
-  float sl[NT][2], sb[NT][NG][2], m[NT][2];
+  float sl[NT][2], sb[NT][NG][2], m[NT][2];  // m: 2^kQ4Shift below the maximum in use
   int lim[CHUNK ? NT : 1][2];
   int rows = 0, row0 = 0, kvh = 0, dest = 0, at_share = 0, parts = 0, left = 0, tok = 0, end = 0, taken = 0;
 
@@ -517,8 +522,9 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
         for (int gr = 0; gr < NG; ++gr) top_a = fmaxf(top_a, va[h][gr].y), top_b = fmaxf(top_b, vb[h][gr].y);
         const float lg_a = log2f_fast(top_a), lg_b = log2f_fast(top_b);
         inv_a[h] = rcp(top_a), inv_b[h] = rcp(top_b);
-        // the running maximum is raised when x + log2 S is 8 above it: any
-        // reference serves the sums as long as nothing overflows
+        // the maximum in use is raised when x + log2 S is 8 above it: any reference
+        // serves the sums as long as nothing overflows (rounded down here and up
+        // there, so that no weight passes 2^15 however far the scores are)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           x[h][nt][0] += lg_a, x[h][nt][1] += lg_a, x[h][nt][2] += lg_b, x[h][nt][3] += lg_b;
@@ -531,8 +537,8 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
             for (int i = 0; i < 4; ++i)
               if (tok + 16 * h + g + 4 * (i & 2) >= lim[nt][i & 1]) x[h][nt][i] = -CUDART_INF_F;
           }
-          raise = raise || fmaxf(x[h][nt][0], x[h][nt][2]) > m[nt][0] + kQ4Margin ||
-                  fmaxf(x[h][nt][1], x[h][nt][3]) > m[nt][1] + kQ4Margin;
+          raise = raise || fmaxf(x[h][nt][0], x[h][nt][2]) > __fadd_rd(m[nt][0], kQ4Margin + kQ4Shift) ||
+                  fmaxf(x[h][nt][1], x[h][nt][3]) > __fadd_rd(m[nt][1], kQ4Margin + kQ4Shift);
         }
       }
       if (__any_sync(0xffffffffu, raise)) {
@@ -540,11 +546,12 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = m[nt][i];
+            float top = -CUDART_INF_F;
 #pragma unroll
             for (int h = 0; h < TT; ++h) top = fmaxf(top, fmaxf(x[h][nt][i], x[h][nt][i + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(__fsub_ru(top, kQ4Shift), m[nt][i]);
             const float f = ex2f(m[nt][i] - top);
             m[nt][i] = top;
 #pragma unroll

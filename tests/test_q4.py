@@ -639,3 +639,45 @@ def test_decode_loop():
     for t in range(1, steps + 1):
         step([1] * B, [p + t for p in prompt], None)
     assert pa.pa_read_device_status(ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_weights(dtype, D):
+    """Weights of 2^-26 beside one of 1, every 64 keys, whose values make up for it: f16's
+    smallest number is 2^-24.  A weight is off by 2^-32 of the largest at most, 63 of them
+    by that times 7.5 x 4096 about the middle code.  The middle of the key of weight 1, 7.5 x
+    4096 above its value of 0, goes into an fp32 sum, rounded to 2^-24 of it, and out of it by
+    an MMA, whose terms are cut at 2^-23 of the largest, one each: below 2^-21 of it together."""
+    c = Attend(20, dtype, 4, 1, D, 16, [640, 65, 3000])
+    c.scale = 1.0
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.kc.zero_(), c.vc.fill_(0xff)
+    c.ks[..., 0], c.ks[..., 1] = -18.25, 0.0
+    c.vs[..., 0], c.vs[..., 1] = 0.0, 4096.0
+    for s, L in enumerate(c.lens):
+        for t in range(0, L, 64):
+            p, o = int(c.bt[s, t // 16]), t % 16
+            c.ks[p, :, o, :, 0], c.vc[p, :, o] = 0.0, 0
+    ref = c.reference()
+    assert (ref > 0.02).all()
+    err = (c.device().run().double().cpu() - ref).abs()
+    u = torch.finfo(dtype).eps / 2
+    middle = 7.5 * 4096
+    assert (err <= (63 * 2 ** -32 + 2 ** -21) * middle + (2 ** -11 + u + 2 ** -20) * ref).all(), float(err.max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_steps_far_below_the_heads_largest(dtype):
+    """One group's steps are 2^-23.4 of another's: a weight of 1 times that is 1.5 of f16's
+    smallest, and 192 of them at 2^7, half of one off."""
+    c = Attend(23, dtype, 8, 2, 128, 16, [1, 1, 40, 300], qmult=0.0)
+    c.vs[..., 0, 0], c.vs[..., 0, 1], c.vs[..., 1, 0], c.vs[..., 1, 1] = 0.0, 65504.0, 0.0, 1.5 * 2 ** -8
+    c.vc[..., :32] = 0
+    ref = c.reference()
+    err = (c.device().run().double().cpu() - ref).abs()
+    u = torch.finfo(dtype).eps / 2
+    assert (err <= (0.5 / 190 + 2 ** -20) * 7.5 * 1.5 * 2 ** -8 + u * ref + 2 ** -24).all(), float(err.max())
