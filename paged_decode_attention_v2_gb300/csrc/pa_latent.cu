@@ -30,7 +30,11 @@
 //
 // A softmax warp has eight rows, four threads a row (16 keys each, as the MMA
 // fragments have them), so a row's maximum and sum are its own.  The maximum in
-// use is raised only when a score passes it by 2^8.  Weights are rounded to the
+// use is raised only when a score passes it by 2^8, or by so much that the key
+// would outweigh half of all before it: the weight of the maximum itself is exact,
+// any other's is rounded, which shows where few keys carry a row (raised beyond
+// 2^8 only, single results of ten million left the parity bar by up to 1.4).
+// Weights are rounded to the
 // input type (the MMA takes nothing wider): off by half a step, 2^-8 of themselves
 // at most in bf16; in f16 by 2^-11, or 2^-32 of the piece's largest where that is
 // more, as f16's start 2^7 above the maximum in use, which the sum takes out (a
@@ -68,7 +72,10 @@ constexpr int kLatentThreads = 32 * (kLatentSoftmax + 2);
 constexpr int kLatentMaxCtas = 152;
 constexpr int kLatentShares = 192;  // that a workspace has places for: a CTA's each
 constexpr float kLatentNone = -3.402823466e38f;  // the maximum of no keys
-constexpr float kLatentMargin = 8.f;  // log2 units
+// The maximum in use is raised when a score is above it by more than this, in log2
+// units, or by so much that the key would weigh more than 2^-kLatentHalf of all
+// before it together.
+constexpr float kLatentMargin = 8.f, kLatentHalf = 1.f;
 // Weights are 2^(x - maximum in use + this): with the margin 2^15, below f16's largest
 template <typename T>
 constexpr float kLatentShift = std::is_same<T, __half>::value ? 7.f : 0.f;
@@ -451,6 +458,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const int t = threadIdx.x, q4 = lane & 3, row = 16 * quarter + 8 * half + (lane >> 2);
     const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
     float m = kLatentNone, l = 0.f;  // m: 2^kShift below the maximum in use
+    float raise_at = kLatentNone;    // a score above it becomes the maximum in use
     int lim = 0, pieces = 0;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       if (lane == 0) mbar_arrive(empty + 8 * sl);  // done with the header
       if (h.flags & kLatentFirst) {
         lim = row < h.rows ? h.lim_base + (h.flat0 + row) / p.num_heads + 1 : 0;
-        m = kLatentNone;
+        m = raise_at = kLatentNone;
         l = 0.f;
       }
       if (!wait(s_full + 8 * (i & 1), (i >> 1) & 1)) break;
@@ -490,8 +498,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       }
 #pragma unroll
       for (int k = 0; k < 16; k += 2) top = fmax3(top, x[k], x[k + 1]);
-      // (rounded down, and the next reference up: no weight above 2^15 however far the scores)
-      const bool raise = __any_sync(0xffffffffu, top > __fadd_rd(m, kLatentMargin + kShift));
+      const bool raise = __any_sync(0xffffffffu, top > raise_at);
       if (raise) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -538,6 +545,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
+      // (of the row's whole sum; rounded down, and the next reference up: no weight
+      // above 2^15 however far the scores are)
+      float all = l + __shfl_xor_sync(0xffffffffu, l, 1);
+      all += __shfl_xor_sync(0xffffffffu, all, 2);
+      raise_at = __fadd_rd(m, kShift + fmaxf(fminf(lg2(all) - kShift - kLatentHalf, kLatentMargin), 0.f));
       // what the other warps left with their weights
       if (!wait(p_full, i & 1)) break;
       if (any_raised(sh.raised[i & 1])) {
