@@ -591,11 +591,12 @@ pa_status_t pa_q4_append(void *key_cache, void *value_cache, void *key_scales,
  * lengths and the GPU's SM count, so last bits of a sequence's output may differ
  * between batches.  query and out contiguous [num_rows][num_heads][head_size];
  * bf16 and f16 (PA_ERR_UNSUPPORTED for f32); max_seq_len at most 2^30; the
- * other arguments and limits as pa_forward.  Scales must be finite.  A bad table
- * entry, length or chunk is reported as PA_ERR_DEVICE_BAD_INPUT; the rows in
- * question then hold no meaningful values (zeros for a bad length without
- * q_start), or are left as they were (a bad chunk; rows that starts out of order
- * give to two sequences hold either's). */
+ * other arguments and limits as pa_forward.  Scales must be finite (a step may be
+ * negative: a code stands for lo + code * step).  A bad table entry, length or
+ * chunk is reported as PA_ERR_DEVICE_BAD_INPUT; the rows in question then hold no
+ * meaningful values (zeros for a bad length without q_start), or are left as they
+ * were (a bad chunk; rows that starts out of order give to two sequences hold
+ * either's). */
 pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache,
                           const void *value_cache, const void *key_scales,
                           const void *value_scales, const int32_t *block_tables,

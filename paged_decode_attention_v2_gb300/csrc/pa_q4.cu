@@ -17,7 +17,7 @@
 // off in the end.
 //
 // Weights: the product takes w = p st in f16, so it must neither overflow nor
-// vanish with st: with S the larger of a token's steps, the running maximum is
+// vanish with st: with S the larger of a token's |st|, the running maximum is
 // that of x + log2 S (x: score in log2 units), p' = 2^(x + log2 S - m), and a
 // group's w = p' st / S.  The normaliser sum(p' / S) is summed in fp32.  The
 // reference m is 2^7 below the maximum in use, which the sums take out: w is off
@@ -509,7 +509,8 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[h][nt][i] = fmaf(qmul[nt][i & 1], y[nt][i], x[h][nt][i]);
       }
-      // ---- values' scales of tokens g and g + 8, and the larger steps S
+      // ---- values' scales of tokens g and g + 8, and the larger steps S (by magnitude:
+      // codes may count downwards)
       float2 va[TT][NG], vb[TT][NG];
       float inv_a[TT], inv_b[TT];
       bool raise = false;
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NT>::CTAS)
         load_scales<NG>(stage + Z::VSC + (16 * h + g + 8) * NG * 4, vb[h]);
         float top_a = kQ4LeastStep, top_b = kQ4LeastStep;
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) top_a = fmaxf(top_a, va[h][gr].y), top_b = fmaxf(top_b, vb[h][gr].y);
+        for (int gr = 0; gr < NG; ++gr) top_a = fmaxf(top_a, fabsf(va[h][gr].y)), top_b = fmaxf(top_b, fabsf(vb[h][gr].y));
         const float lg_a = log2f_fast(top_a), lg_b = log2f_fast(top_b);
         inv_a[h] = rcp(top_a), inv_b[h] = rcp(top_b);
         // the maximum in use is raised when x + log2 S is 8 above it: any reference

@@ -681,3 +681,17 @@ def test_steps_far_below_the_heads_largest(dtype):
     err = (c.device().run().double().cpu() - ref).abs()
     u = torch.finfo(dtype).eps / 2
     assert (err <= (0.5 / 190 + 2 ** -20) * 7.5 * 1.5 * 2 ** -8 + u * ref + 2 ** -24).all(), float(err.max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_negative_steps(dtype, D):
+    """lowest + code step of a step below zero, in some groups, tokens or all."""
+    c = Attend(24, dtype, 8, 2, D, 16, [200, 33, 1])
+    g = torch.Generator().manual_seed(25)
+    for sc in (c.ks, c.vs):
+        sign = 1 - 2 * torch.randint(0, 2, sc.shape[:-1], generator=g)
+        sign[c.bt[2, 0].long()] = -1
+        sc[..., 1] *= sign
+    c.check(c.device().run())
