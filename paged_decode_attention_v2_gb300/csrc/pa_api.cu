@@ -1045,6 +1045,10 @@ pa_status_t host_launch(const void *fn, unsigned grid_x, unsigned grid_y, int th
   return PA_OK;
 }
 
+void host_clear(void *at, size_t bytes, void *stream) {
+  cudaMemsetAsync(at, 0, bytes, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace pa
 
 extern "C" {

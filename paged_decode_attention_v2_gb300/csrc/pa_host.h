@@ -43,4 +43,8 @@ pa_status_t host_check_cache(int dtype, int num_heads, int num_kv_heads, int hea
 pa_status_t host_launch(const void *fn, unsigned grid_x, unsigned grid_y, int threads, size_t smem,
                         void *stream, void **args, const char *what);
 
+// Zero `bytes` of device memory in the stream, after a launch that failed: what of
+// this fails too is the caller's next call's error.
+void host_clear(void *at, size_t bytes, void *stream);
+
 }  // namespace pa

@@ -726,9 +726,7 @@ pa_status_t pa_latent_forward(void *out, const void *query, const void *cache, c
   j.max_rows = kLatentRows;
   j.item_rows = q_start || num_heads > kLatentRows ? kLatentRows : num_heads;
   j.width = latent_dim;
-  void *jargs[1] = {&j};
-  return host_launch(share_join_kernel(dtype == PA_DTYPE_BF16, latent_dim), (unsigned)(kJoinCtas * sms), 1, kJoinThreads, 0,
-                     stream, jargs, "launch join kernel");
+  return share_launch_join(j, dtype == PA_DTYPE_BF16, sms, stream);
 }
 
 }  // extern "C"

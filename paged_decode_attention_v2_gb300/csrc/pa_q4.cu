@@ -779,9 +779,7 @@ pa_status_t pa_q4_forward(void *out, const void *query, const void *key_cache, c
   j.max_rows = 8 * nt;
   j.item_rows = q_start ? p.chunk_tokens * p.group : p.group;
   j.width = head_size;
-  void *jargs[1] = {&j};
-  return host_launch(share_join_kernel(dtype == PA_DTYPE_BF16, head_size), (unsigned)(kJoinCtas * sms), 1, kJoinThreads, 0, stream,
-                     jargs, "launch join kernel");
+  return share_launch_join(j, dtype == PA_DTYPE_BF16, sms, stream);
 }
 
 }  // extern "C"

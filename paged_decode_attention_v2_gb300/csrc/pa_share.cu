@@ -8,10 +8,13 @@
 // of 64 as the most of few took 35 us instead of 32 in all for drafts.
 #include "pa_share.cuh"
 
+#include "pa_host.h"
+
 namespace pa {
 
 namespace {
 
+constexpr int kJoinThreads = 256, kJoinCtas = 3;  // CTAs: an SM's
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // Sums over a row's pieces of four columns in each of C stretches of 128.
@@ -184,12 +187,16 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtas) pa_share_join_kernel(
   }
 }
 
-const void *share_join_kernel(int dtype_bf16, int width) {
+pa_status_t share_launch_join(const JoinParams &p, int dtype_bf16, int sms, void *stream) {
 #define PICK(C)                                                                          \
   (dtype_bf16 ? reinterpret_cast<const void *>(&pa_share_join_kernel<__nv_bfloat16, C>) \
               : reinterpret_cast<const void *>(&pa_share_join_kernel<__half, C>))
-  return width == 512 ? PICK(4) : width == 256 ? PICK(2) : PICK(1);
+  const void *fn = p.width == 512 ? PICK(4) : p.width == 256 ? PICK(2) : PICK(1);
 #undef PICK
+  void *args[1] = {const_cast<JoinParams *>(&p)};
+  const pa_status_t st = host_launch(fn, (unsigned)(kJoinCtas * sms), 1, kJoinThreads, 0, stream, args, "launch join kernel");
+  if (st != PA_OK) host_clear(p.space.counters + kShareTaken, (kShareDone - kShareTaken + 1) * sizeof(int), stream);
+  return st;
 }
 
 }  // namespace pa

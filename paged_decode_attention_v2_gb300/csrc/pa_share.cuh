@@ -22,6 +22,7 @@
 
 #include <math_constants.h>
 
+#include "pa.h"
 #include "pa_device.cuh"
 
 namespace pa {
@@ -246,7 +247,8 @@ struct JoinParams {
   void *out;  // [..][width], rows as the ShareJoins say
   int max_rows, item_rows, width;  // rows of a place, of the largest unit
 };
-const void *share_join_kernel(int dtype_bf16, int width);
-constexpr int kJoinThreads = 256, kJoinCtas = 3;  // CTAs: an SM's
+// Launches the join behind an attention kernel.  If that fails, the counters, which
+// the join would have reset, are cleared: the next call would take them for its own.
+pa_status_t share_launch_join(const JoinParams &p, int dtype_bf16, int sms, void *stream);
 
 }  // namespace pa
