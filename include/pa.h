@@ -627,7 +627,9 @@ size_t pa_q4_workspace_bytes(int head_size);
  *   query        [num_rows][num_heads][latent_dim + rope_dim], contiguous: the
  *                last rope_dim elements of every head; the first latent_dim,
  *                the queries through the keys' up-projection, are the caller's
- *                and are not touched
+ *                and are not touched.  query_rope may be those last elements
+ *                themselves; words of it that are written for another head or
+ *                row are PA_ERR_INVALID_ARG
  *
  * All of rope_dim turns, in pairs as interleaved says; everything in fp32 with
  * one rounding to dtype.  cos_sin, positions, rows, q_start, seq_lens and bad

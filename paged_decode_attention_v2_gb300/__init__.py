@@ -752,8 +752,9 @@ def pa_latent_append(cache, latent, rope_key, block_tables, seq_lens, workspace,
     """Append rows to a cache of shared latents [num_blocks, block_size, latent_dim +
     rope_dim]: latent [rows, latent_dim], normalised with norm_weight and eps, and
     rope_key [rows, rope_dim], rotated by cos_sin [max_position, rope_dim]; query_rope
-    [rows, H, rope_dim] (rows and heads may be strided) is rotated into the last
-    rope_dim elements of query [rows, H, latent_dim + rope_dim] (see include/pa.h)."""
+    [rows, H, rope_dim] (rows and heads may be strided; query[..., latent_dim:] itself
+    too) is rotated into the last rope_dim elements of query [rows, H, latent_dim +
+    rope_dim] (see include/pa.h)."""
     if latent.dim() != 2:
         raise ValueError("latent must be [rows, latent_dim]")
     nb, bs, width, B = _latent_shapes(cache, block_tables, seq_lens, q_start)

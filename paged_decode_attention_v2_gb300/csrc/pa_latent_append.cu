@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kLatentAppendThreads, 6)
       const T *from = h < 0 ? static_cast<const T *>(p.rope_key) + row * p.rope_key_stride
                             : static_cast<const T *>(p.query_rope) + row * p.query_stride + h * p.query_head_stride;
       const uint4 *src = reinterpret_cast<const uint4 *>(from);
-      Chunk2<T> x{__ldg(src + ca), __ldg(src + cb)};
+      Chunk2<T> x{src[ca], src[cb]};  // (which may be the query itself: no read-only path)
       Angles<N> r;
       r.load(p.cos_sin + (size_t)pos * kRope, u, kRope / 2);
       rotate_unit(x, r, il);
@@ -148,6 +148,23 @@ template <typename T>
 const void *latent_append_pick(int latent_dim) {
   return latent_dim == 512 ? reinterpret_cast<const void *>(&pa_latent_append_kernel<T, 512>)
                            : reinterpret_cast<const void *>(&pa_latent_append_kernel<T, 256>);
+}
+
+// Whether no thread reads of query_rope what another writes of query: they do not
+// meet, or heads are as far apart in both and a head's words are those that they
+// are rotated into, or none that are written.
+bool rope_apart(const void *query, const void *query_rope, long long stride, long long head_stride,
+                int num_rows, int num_heads, int latent_dim) {
+  const __int128 width = latent_dim + kRope;
+  const __int128 from =
+      (reinterpret_cast<intptr_t>(query_rope) - reinterpret_cast<intptr_t>(query)) / 2;  // elements
+  const __int128 span = (__int128)(num_rows - 1) * stride + (__int128)(num_heads - 1) * head_stride + kRope;
+  if (from >= num_rows * (num_heads * width) || from + span <= latent_dim) return true;
+  if (num_heads > 1 && head_stride != width) return false;
+  if (num_rows > 1 && stride != num_heads * width) return false;
+  if (from == latent_dim) return true;
+  const __int128 at = ((from - latent_dim) % width + width) % width;  // in a head, from its written words on
+  return at >= kRope && at <= width - kRope;
 }
 
 }  // namespace
@@ -185,6 +202,8 @@ extern "C" pa_status_t pa_latent_append(
                 query_stride < (num_heads - 1) * query_head_stride + rope_dim))
     return PA_ERR_INVALID_ARG;
   if (workspace_bytes < (size_t)kStatusBytes) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (query && !rope_apart(query, query_rope, query_stride, query_head_stride, num_rows, num_heads, latent_dim))
+    return PA_ERR_INVALID_ARG;
 
   LatentAppendParams p{};
   p.cache = cache;

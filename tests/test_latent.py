@@ -522,3 +522,39 @@ def test_peaky_logits_within_the_parity_bar(deviation):
         ref = torch.softmax(c.a[0][s:s + 10].double() @ kv.T * c.scale, -1) @ kv[:, :512]
         over = ((out[s:s + 10].double() - ref).abs() / (ATOL + RTOL * ref.abs())).max()
         assert over <= 1.0, float(over)
+
+
+@pytest.mark.parametrize("over", [
+    dict(),                                                                # other strides, same words
+    dict(query_rope=FAKE + 520 * 2, query_head_stride=576, query_stride=8 * 576),  # eight elements on
+    dict(query_rope=FAKE + (512 + 576) * 2, query_head_stride=576, query_stride=8 * 576),  # a head on
+    dict(query_rope=FAKE + (512 - 576) * 2, query_head_stride=576, query_stride=8 * 576),
+    dict(query_rope=FAKE - 64 * 2, query_head_stride=64, query_stride=512),
+])
+def test_append_refuses_queries_that_overlap(lib, over):
+    """Words that are written before another head's are read."""
+    assert lib.pa_latent_append(*dict(APPEND, **over).values()) == pa.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,L,rows,at", [(8, 512, 700, 512), (1, 256, 3, 256), (24, 256, 1, 256), (8, 512, 700, 0)])
+@pytest.mark.parametrize("il", [False, True])
+def test_append_in_place(dtype, H, L, rows, at, il):
+    """query_rope as the last elements of query's heads, or others that are not written."""
+    g = torch.Generator().manual_seed(40)
+    bt, pool = tables([rows + 9], 16, g)
+    q = torch.randn(rows, H, L + ROPE, generator=g).to(dtype)
+    down = torch.randn(rows, L + ROPE, generator=g).to(dtype).cuda()
+    ang = torch.arange(rows + 9, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    cache = torch.zeros(pool, 16, L + ROPE, dtype=dtype, device="cuda")
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dq = q.cuda()
+    pa.pa_latent_append(cache, down[:, :L], down[:, L:], bt.cuda(), i32([rows + 9]), ws, cs.cuda(), query=dq,
+                        query_rope=dq[..., at:at + ROPE], q_start=i32([0, rows]), interleaved=il)
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    got = dq.cpu()
+    assert near(got[..., L:], turn(q[..., at:at + ROPE].double(), cs[9:], il), dtype)
+    assert torch.equal(got[..., :L], q[..., :L])
