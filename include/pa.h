@@ -622,8 +622,9 @@ size_t pa_q4_workspace_bytes(int head_size);
  *   norm_weight  [latent_dim] or NULL (the latent is stored as it is): the
  *                latent is x * (mean(x^2) + eps)^-1/2 * norm_weight
  *   query_rope   [num_rows][num_heads][rope_dim] or NULL, heads
- *                query_head_stride and rows query_stride apart: the queries'
- *                parts that carry the position; rotated into
+ *                query_head_stride and rows query_stride apart (either the
+ *                further, no two overlapping): the queries' parts that carry the
+ *                position; rotated into
  *   query        [num_rows][num_heads][latent_dim + rope_dim], contiguous: the
  *                last rope_dim elements of every head; the first latent_dim,
  *                the queries through the keys' up-projection, are the caller's

@@ -198,9 +198,12 @@ extern "C" pa_status_t pa_latent_append(
   if (!host_aligned(workspace, 256)) return PA_ERR_INVALID_ARG;
   if (latent_stride < latent_dim || latent_stride % 8 || rope_key_stride < rope_dim || rope_key_stride % 8)
     return PA_ERR_INVALID_ARG;
-  if (query && (query_head_stride < rope_dim || query_head_stride % 8 || query_stride % 8 ||
-                query_stride < (num_heads - 1) * query_head_stride + rope_dim))
-    return PA_ERR_INVALID_ARG;
+  if (query) {  // a row's heads do not reach into the next row's, or a head's rows into the next head's
+    if (query_head_stride < rope_dim || query_stride < rope_dim || query_head_stride % 8 || query_stride % 8)
+      return PA_ERR_INVALID_ARG;
+    const __int128 row = query_stride, head = query_head_stride;
+    if (row < (num_heads - 1) * head + rope_dim && head < (num_rows - 1) * row + rope_dim) return PA_ERR_INVALID_ARG;
+  }
   if (workspace_bytes < (size_t)kStatusBytes) return PA_ERR_WORKSPACE_TOO_SMALL;
   if (query && !rope_apart(query, query_rope, query_stride, query_head_stride, num_rows, num_heads, latent_dim))
     return PA_ERR_INVALID_ARG;

@@ -558,3 +558,24 @@ def test_append_in_place(dtype, H, L, rows, at, il):
     got = dq.cpu()
     assert near(got[..., L:], turn(q[..., at:at + ROPE].double(), cs[9:], il), dtype)
     assert torch.equal(got[..., :L], q[..., :L])
+
+
+@pytest.mark.gpu
+def test_append_queries_heads_first():
+    """query_rope as a view of [heads][rows][64]: heads further apart than rows."""
+    g = torch.Generator().manual_seed(41)
+    H, L, rows, dt = 6, 256, 37, torch.bfloat16
+    bt, pool = tables([rows], 16, g)
+    rope = torch.randn(H, rows, ROPE, generator=g).to(dt)
+    down = torch.randn(rows, L + ROPE, generator=g).to(dt).cuda()
+    ang = torch.arange(rows, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    cache = torch.zeros(pool, 16, L + ROPE, dtype=dt, device="cuda")
+    q = torch.zeros(rows, H, L + ROPE, dtype=dt, device="cuda")
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pa.pa_latent_append(cache, down[:, :L], down[:, L:], bt.cuda(), i32([rows]), ws, cs.cuda(), query=q,
+                        query_rope=rope.cuda().transpose(0, 1), q_start=i32([0, rows]))
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    assert near(q.cpu()[..., L:], turn(rope.transpose(0, 1).double(), cs, False), dt)
+    assert (q[..., :L] == 0).all()
