@@ -579,3 +579,259 @@ def test_append_queries_heads_first():
     assert pa.pa_read_device_status(ws) == pa.PA_OK
     assert near(q.cpu()[..., L:], turn(rope.transpose(0, 1).double(), cs, False), dt)
     assert (q[..., :L] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# Bounds from a case's own data, where the parity bar says little: few keys that
+# carry the result, scores of +-1000, f16.
+
+def rounding_bound(c, ref):
+    """What rounding may do to c's outputs (ref, in 64 bits), by output.
+
+    Scores: 36 MMAs of 16 products, two roundings each at most, of terms that add up to T:
+    72 of 2^-23 T with those after it, so below 2^-16 T; that moves weights against each
+    other by a factor of exp(+-2 2^-16 T).  Weights are rounded to the type, u = eps / 2
+    (f16: or 2^-32 of the largest, the smallest number against weights that start at 2^7),
+    the sum taking them as rounded.  Sums: fp32, fewer than 2^7 additions a share, of which
+    two roundings each.  The output: half a step of its type."""
+    u = torch.finfo(c.dtype).eps / 2
+    kvs, out, row = c.cache.double(), torch.zeros_like(ref), 0
+    for s, (n, L) in enumerate(zip(c.new, c.lens)):
+        t = torch.arange(L)
+        kv = kvs[c.bt[s, t // c.bs].long(), t % c.bs]
+        for i in range(n):
+            m = L - n + i + 1
+            if m <= 0:
+                row += 1
+                continue
+            q = c.q[row].double()
+            p = torch.softmax(q @ kv[:m].T * c.scale, -1)
+            T = (q.abs() @ kv[:m].abs().T * abs(c.scale)).amax(-1)
+            off = torch.stack([(p[h, :, None] * (kv[:m, :c.L] - ref[row, h]).abs()).sum(0) for h in range(c.H)])
+            far = torch.stack([(kv[:m, :c.L] - ref[row, h]).abs().amax(0) for h in range(c.H)])
+            tiny = p.amax(-1, keepdim=True) * (m * 2.0 ** -32 if c.dtype == torch.float16 else 0.0) * far
+            out[row] = (u * 1.01 + torch.expm1(2 * 2 ** -16 * T)[:, None]) * off + tiny + 2 ** -16 * (p @ kv[:m, :c.L].abs())
+            row += 1
+    return out + u * (ref.abs() + out) + 2 ** -25
+
+
+def lose_newest(c):
+    """The case's exact outputs without each sequence's newest key."""
+    d = object.__new__(Attend)
+    d.__dict__.update(c.__dict__)
+    d.lens = [max(L - 1, 0) for L in c.lens]
+    return d.reference()
+
+
+def far_case(dtype, qmult, L=512, seed=31):
+    """Every other head looks for the newest key."""
+    c = Attend(seed, dtype, 16, L, 16, [900, 40, 33])
+    for s, n in enumerate(c.lens):
+        c.q[s, ::2] = c.cache[c.bt[s, (n - 1) // 16].long(), (n - 1) % 16]
+    c.q = (c.q.double() * qmult).to(dtype)
+    return c
+
+
+@pytest.mark.parametrize("qmult", [1.0, 8.0, 60.0])
+def test_bounds_notice_what_is_lost(qmult):
+    """Zeros, and outputs without the newest key, leave the bound (an oracle's mistake)."""
+    for dtype in (torch.bfloat16, torch.float16):
+        c = far_case(dtype, qmult)
+        ref = c.reference()
+        tol = rounding_bound(c, ref)
+        assert (ref.abs() > tol).double().mean() > 0.75
+        assert ((lose_newest(c) - ref).abs() > tol)[:, ::2].any(-1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("qmult,L", [(1.0, 512), (8.0, 512), (60.0, 512), (60.0, 256)])
+def test_far_scores_within_rounding(dtype, qmult, L):
+    c = far_case(dtype, qmult, L).device()
+    ref = c.reference()
+    err = (c.run().double().cpu() - ref).abs()
+    assert (err <= rounding_bound(c, ref)).all(), float((err - rounding_bound(c, ref)).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,L,bs,new", [(16, 512, 16, None), (128, 512, 64, None), (24, 256, 8, [5, 1, 17]),
+                                        (16, 512, 32, [5, 1, 64])])
+def test_within_rounding(dtype, H, L, bs, new):
+    c = Attend(32, dtype, H, L, bs, [700, 33, 150], new).device()
+    ref = c.reference()
+    err = (c.run().double().cpu() - ref).abs()
+    assert (err <= rounding_bound(c, ref)).all(), float((err - rounding_bound(c, ref)).max())
+
+
+# ---------------------------------------------------------------------------
+# Appends and attention together, captured; streams; what the appends' tests left out
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H,L", [(torch.bfloat16, 20, 256), (torch.float16, 80, 512)])
+def test_append_and_attend_as_graphs(dtype, H, L):
+    """A prompt, then decode steps and draft chunks of which some tokens are taken back, each
+    an append and the attention behind it: captured once and replayed as the lengths grow,
+    beside the same calls one by one on a cache of their own.  Every output against 64 bits
+    over the rows that the cache then holds."""
+    bs, B, scale = 16, 3, 0.06
+    g = torch.Generator().manual_seed(51)
+    rng = random.Random(52)
+    lens, width = [37, 5, 90], 9
+    caches = [torch.zeros(B * width, bs, L + ROPE, dtype=dtype, device="cuda") for _ in range(2)]
+    bt = torch.randperm(B * width, generator=g).to(torch.int32).view(B, width).cuda()
+    ang = torch.arange(width * bs, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+    w = (1 + 0.2 * torch.randn(L, generator=g)).to(dtype).cuda()
+    ws = pa.alloc_latent_workspace(L)
+
+    class Step:
+        def __init__(self, new, chunks):
+            self.new, n = new, sum(new)
+            self.down = torch.zeros(n, L + ROPE, dtype=dtype, device="cuda")
+            self.rope = torch.zeros(n, H, ROPE, dtype=dtype, device="cuda")
+            self.q = torch.zeros(n, H, L + ROPE, dtype=dtype, device="cuda")
+            self.sl = torch.zeros(B, dtype=torch.int32, device="cuda")
+            starts = [sum(new[:i]) for i in range(B + 1)]
+            self.qs = torch.tensor(starts, dtype=torch.int32, device="cuda") if chunks else None
+            self.out = torch.zeros(n, H, L, dtype=dtype, device="cuda")
+
+        def calls(self, cache):
+            pa.pa_latent_append(cache, self.down[:, :L], self.down[:, L:], bt, self.sl, ws, cs, query=self.q,
+                                query_rope=self.rope, norm_weight=w, eps=1e-6, q_start=self.qs)
+            pa.pa_latent_forward(self.out, self.q, cache, bt, self.sl, scale, ws, q_start=self.qs)
+
+        def fill(self):
+            for t in (self.down, self.rope, self.q):
+                t.copy_(torch.randn(t.shape, generator=g))
+            self.sl.copy_(torch.tensor(lens))
+
+        def check(self):
+            row = 0
+            for s, (n, m) in enumerate(zip(self.new, lens)):
+                t = torch.arange(m, device="cuda")
+                kv = caches[0][bt[s, t // bs].long(), t % bs].double()
+                for i in range(m - n + 1, m + 1):
+                    ref = torch.softmax(self.q[row].double() @ kv[:i].T * scale, -1) @ kv[:i, :L]
+                    assert ((self.out[row].double() - ref).abs() <= ATOL + RTOL * ref.abs()).all()
+                    row += 1
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        prompt = Step(list(lens), True)
+        prompt.fill()
+        for cache in caches:
+            prompt.calls(cache)
+        prompt.check()
+        kinds = [Step([1] * B, False), Step([3, 1, 2], True)]
+        graphs = []
+        for k in kinds:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                k.calls(caches[0])
+            graphs.append(graph)
+        for i in range(8):
+            k = kinds[i % 2]
+            lens = [a + b for a, b in zip(lens, k.new)]
+            k.fill()
+            graphs[i % 2].replay()
+            got = [t.clone() for t in (k.out, k.q)]
+            k.check()
+            k.calls(caches[1])
+            assert all(torch.equal(a, b) for a, b in zip(got, (k.out, k.q)))
+            assert torch.equal(*caches)
+            if i % 2:  # drafts that were not right: their places are written again
+                lens = [a - rng.randint(0, b - 1) for a, b in zip(lens, k.new)]
+        assert pa.pa_read_device_status(ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+def test_two_streams_bit_by_bit():
+    """A workspace each: every call gives the bits that it gives alone."""
+    a = Attend(10, torch.bfloat16, 128, 512, 16, [3000, 5, 700]).device()
+    b = Attend(11, torch.bfloat16, 12, 512, 8, [44, 900], [7, 3]).device()
+    alone = [c.run().clone() for c in (a, b)]
+    outs = [torch.empty_like(x) for x in alone]
+    s2 = torch.cuda.Stream()
+    for _ in range(20):
+        for o in outs:
+            o.fill_(7.0)
+        s2.wait_stream(torch.cuda.current_stream())
+        b.run(stream=s2, out=outs[1])
+        a.run(out=outs[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, alone))
+
+
+def append_rows(dtype, L, rows, lens, bt, cache, down, cs, w=None, eps=0.0, positions=None):
+    """Rows of one sequence appended by the call; what the cache should hold of them, in 64 bits."""
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    d = down.cuda()
+    pa.pa_latent_append(cache, d[:, :L], d[:, L:], bt.cuda(), i32(lens), ws, cs.cuda(), norm_weight=None if w is None else w.cuda(),
+                        eps=eps, positions=positions, q_start=i32([0, rows]))
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    x = down.double()
+    c = x[:, :L]
+    if w is not None:
+        c = c / torch.sqrt((c * c).mean(-1, keepdim=True) + eps) * w.double()
+    at = torch.arange(lens[0] - rows, lens[0]) if positions is None else positions.cpu().long()
+    return torch.cat([c, turn(x[:, None, L:], cs[at], False)[:, 0]], -1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("L", [256, 512])
+def test_append_rows_near_zero(dtype, L):
+    """Rows whose mean square is far below eps, and of zeros: the root is eps's."""
+    g = torch.Generator().manual_seed(42)
+    rows = 40
+    down = torch.randn(rows, L + ROPE, generator=g)
+    down[:, :L] *= 10.0 ** -torch.linspace(0, 4, rows)[:, None]
+    down[7, :L] = 0.0
+    down, w = down.to(dtype), (1 + 0.2 * torch.randn(L, generator=g)).to(dtype)
+    bt, pool = tables([rows], 16, g)
+    cache = torch.zeros(pool, 16, L + ROPE, dtype=dtype, device="cuda")
+    ang = torch.arange(rows, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    ref = append_rows(dtype, L, rows, [rows], bt, cache, down, cs, w, 1e-5)
+    t = torch.arange(rows)
+    got = cache.cpu()[bt[0, t // 16].long(), t % 16]
+    for r in range(rows):  # (each row's bound by its own size)
+        assert near(got[r, :L], ref[r, :L], dtype) and near(got[r, L:], ref[r, L:], dtype)
+    assert (got[7, :L] == 0).all()
+
+
+@pytest.mark.gpu
+def test_append_positions():
+    """Positions of the caller's: the keys' angles, not their places."""
+    g = torch.Generator().manual_seed(43)
+    rows, L, dtype = 50, 512, torch.bfloat16
+    down = torch.randn(rows, L + ROPE, generator=g).to(dtype)
+    bt, pool = tables([rows + 30], 16, g)
+    cache = torch.zeros(pool, 16, L + ROPE, dtype=dtype, device="cuda")
+    ang = torch.arange(700, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    pos = torch.randint(0, 700, (rows,), generator=g).to(torch.int32).cuda()
+    ref = append_rows(dtype, L, rows, [rows + 30], bt, cache, down, cs, positions=pos)
+    t = torch.arange(30, rows + 30)
+    assert near(cache.cpu()[bt[0, t // 16].long(), t % 16], ref, dtype)
+
+
+@pytest.mark.gpu
+def test_append_far_pages():
+    """Pages beyond 2^31 elements and 2^32 bytes; nothing else is written."""
+    L, bs, nb, dtype, rows = 512, 64, 70000, torch.bfloat16, 100
+    g = torch.Generator().manual_seed(44)
+    cache = torch.zeros(nb, bs, L + ROPE, dtype=dtype, device="cuda")
+    down = torch.randn(rows, L + ROPE, generator=g).to(dtype)
+    bt = torch.tensor([[nb - 1, nb - 9]], dtype=torch.int32)
+    ang = torch.arange(rows, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, ROPE, 2) / ROPE)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    ref = append_rows(dtype, L, rows, [rows], bt, cache, down, cs)
+    t = torch.arange(rows)
+    assert near(cache[bt[0, t // bs].long().cuda(), (t % bs).cuda()].cpu(), ref, dtype)
+    for p in bt[0].tolist():
+        cache[p] = 0.0
+    assert not cache.any()

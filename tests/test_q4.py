@@ -695,3 +695,243 @@ def test_negative_steps(dtype, D):
         sign[c.bt[2, 0].long()] = -1
         sc[..., 1] *= sign
     c.check(c.device().run())
+
+
+# ---------------------------------------------------------------------------
+# Bounds from a case's own data, where the parity bar says little: few keys that
+# carry the result, scores of +-1000, f16.
+
+def rounding_bound(c, ref):
+    """What rounding may do to c's outputs (ref, in 64 bits), by output.
+
+    Scores: fp32 sums of terms that add up to T at most, T = scale sum |q| (|lo| + 15
+    |step|): 18 additions of q a group, 16 MMAs a head of two roundings each, ten more:
+    60 of 2^-24 T, so below 2^-18 T.  That moves weights against each other by a factor
+    of exp(+-2 2^-18 T).  Weights times steps are rounded to f16 and meet codes about
+    their middle: 2^-11 sum p |code - 7.5| step, or 2^-32 of the largest p x step a key
+    where that is more (the smallest f16 against weights that start at 2^7).  Sums: fp32,
+    fewer than 2^7 additions one behind another a share.  The output: half a step of its
+    type."""
+    u = torch.finfo(c.dtype).eps / 2
+    G, NG = c.H // c.K, c.D // 64
+    k, v = values(c.kc, c.ks), values(c.vc, c.vs)
+    reach = (c.ks[..., 0].double().abs() + 15 * c.ks[..., 1].double().abs()).repeat_interleave(64, -1)
+    step = c.vs[..., 1].double().abs()
+    mid = (v - (c.vs[..., 0].double() + 7.5 * c.vs[..., 1].double()).repeat_interleave(64, -1)).abs()
+    size = (c.vs[..., 0].double().abs() + 15 * step).repeat_interleave(64, -1)
+    out, row = torch.zeros_like(ref), 0
+    for s, (n, L) in enumerate(zip(c.new, c.lens)):
+        t = torch.arange(L)
+        kk, vv, rr, st, md, sz = (x[c.bt[s, t // c.bs].long(), :, t % c.bs] for x in (k, v, reach, step, mid, size))
+        for i in range(n):
+            m = L - n + i + 1
+            if m <= 0:
+                row += 1
+                continue
+            for h in range(c.K):
+                at = slice(h * G, (h + 1) * G)
+                q = c.q[row, at].double()
+                p = torch.softmax(q @ kk[:m, h].T * c.scale, -1)
+                T = (q.abs() @ rr[:m, h].T * abs(c.scale)).amax(-1)
+                o = ref[row, at]
+                spread = torch.stack([(p[g, :, None] * (vv[:m, h] - o[g]).abs()).sum(0) for g in range(G)])
+                tiny = (p * st[:m, h].amax(-1)).amax(-1) * (m * 7.5 * 2 ** -32)
+                e = torch.expm1(2 * 2 ** -18 * T)[:, None] * spread + 2 ** -11 * 1.01 * (p @ md[:m, h])
+                out[row, at] = e + tiny[:, None] + 2 ** -16 * (p @ sz[:m, h])
+            row += 1
+    return out + u * (ref.abs() + out) + 2 ** -25
+
+
+def lose_newest(c):
+    """The case's exact outputs without each sequence's newest key."""
+    d = object.__new__(Attend)
+    d.__dict__.update(c.__dict__)
+    d.kc, d.ks = c.kc.clone(), c.ks.clone()
+    d.lens = [max(L - 1, 0) for L in c.lens]
+    return d.reference()
+
+
+def far_case(dtype, kind, seed=21):
+    """Scores of +-1000, or keys far from zero; every other head looks for the newest key."""
+    c = Attend(seed, dtype, 8, 2, 128, 16, [900, 40, 33], offset=50.0 if kind == "offset" else 0.0)
+    k = values(c.kc, c.ks)
+    for s, L in enumerate(c.lens):
+        last = k[c.bt[s, (L - 1) // 16].long(), :, (L - 1) % 16]
+        last = (last - (50.0 if kind == "offset" else 0.0)).repeat_interleave(4, 0)
+        c.q[s, ::2] = last[::2].to(dtype)
+    c.q = (c.q.double() * {"peaked": 30.0, "far": 200.0, "offset": 1.0}[kind]).to(dtype)
+    return c
+
+
+@pytest.mark.parametrize("kind", ["peaked", "far", "offset"])
+def test_bounds_notice_what_is_lost(kind):
+    """Zeros, and outputs without the newest key, leave the bound (an oracle's mistake)."""
+    for dtype in (torch.bfloat16, torch.float16):
+        c = far_case(dtype, kind)
+        ref = c.reference()
+        tol = rounding_bound(c, ref)
+        assert (ref.abs() > tol).double().mean() > 0.75
+        assert ((lose_newest(c) - ref).abs() > tol)[:, ::2].any(-1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("kind", ["peaked", "far", "offset"])
+def test_far_scores_within_rounding(dtype, kind):
+    c = far_case(dtype, kind).device()
+    ref = c.reference()
+    err = (c.run().double().cpu() - ref).abs()
+    assert (err <= rounding_bound(c, ref)).all(), float((err - rounding_bound(c, ref)).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,K,D,bs,new", [(8, 2, 128, 16, None), (16, 1, 64, 8, None), (7, 1, 256, 32, [5, 1, 17]),
+                                          (8, 1, 128, 64, [5, 1, 64])])
+def test_within_rounding(dtype, H, K, D, bs, new):
+    c = Attend(22, dtype, H, K, D, bs, [700, 33, 150], new).device()
+    ref = c.reference()
+    err = (c.run().double().cpu() - ref).abs()
+    assert (err <= rounding_bound(c, ref)).all(), float((err - rounding_bound(c, ref)).max())
+
+
+# ---------------------------------------------------------------------------
+# Appends and attention together, captured; streams; positions of the caller's
+
+def attend_in_64_bits(q, kc, vc, ks, vs, bt, lens, new, bs):
+    """[rows, H, D]: over what the cache holds, gathered from its codes and scales."""
+    k, v = values(kc.cpu(), ks.cpu()), values(vc.cpu(), vs.cpu())
+    q, bt = q.double().cpu(), bt.cpu()
+    K, D = k.shape[1], k.shape[3]
+    out = []
+    for s, (n, L) in enumerate(zip(new, lens)):
+        t = torch.arange(L)
+        kk, vv = (x[bt[s, t // bs].long(), :, t % bs] for x in (k, v))
+        for m in range(L - n + 1, L + 1):
+            x = torch.einsum("kgd,tkd->kgt", q[len(out)].view(K, -1, D), kk[:m]) * D ** -0.5
+            out.append(torch.einsum("kgt,tkd->kgd", torch.softmax(x, -1), vv[:m]).reshape(-1, D))
+    return torch.stack(out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_append_and_attend_as_graphs(dtype):
+    """A prompt, then decode steps and draft chunks of which some tokens are taken back, each
+    an append and the attention behind it: captured once and replayed as the lengths grow,
+    beside the same calls one by one on a cache of their own.  Every output against 64 bits
+    over the codes and scales that the cache then holds."""
+    H, K, D, bs, B = 8, 2, 128, 16, 3
+    g = torch.Generator().manual_seed(51)
+    rng = random.Random(52)
+    lens, width = [37, 5, 90], 9
+    caches = []
+    for _ in range(2):
+        (kc, ks), (vc, vs) = (pa.alloc_q4_cache(B * width, K, bs, D) for _ in range(2))
+        caches.append((kc, vc, ks, vs))
+    bt = torch.randperm(B * width, generator=g).to(torch.int32).view(B, width).cuda()
+    ang = torch.arange(width * bs, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, D, 2) / D)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+    ws = pa.alloc_q4_workspace(D)
+
+    class Step:
+        def __init__(self, new, chunks):
+            self.new, n = new, sum(new)
+            self.qkv = torch.zeros(n, (H + 2 * K) * D, dtype=dtype, device="cuda")
+            self.sl = torch.zeros(B, dtype=torch.int32, device="cuda")
+            starts = [sum(new[:i]) for i in range(B + 1)]
+            self.qs = torch.tensor(starts, dtype=torch.int32, device="cuda") if chunks else None
+            self.qo, self.out = (torch.zeros(n, H, D, dtype=dtype, device="cuda") for _ in range(2))
+
+        def calls(self, cache):
+            n = len(self.qkv)
+            q, k, v = (self.qkv[:, a * D:b * D].view(n, -1, D) for a, b in ((0, H), (H, H + K), (H + K, H + 2 * K)))
+            pa.pa_q4_append(*cache, k, v, bt, self.sl, ws, query=q, query_out=self.qo, cos_sin=cs, q_start=self.qs)
+            pa.pa_q4_forward(self.out, self.qo, *cache, bt, self.sl, D ** -0.5, ws, q_start=self.qs)
+
+        def fill(self):
+            self.qkv.copy_(torch.randn(self.qkv.shape, generator=g))
+            self.sl.copy_(torch.tensor(lens))
+
+        def check(self):
+            kc, vc, ks, vs = caches[0]
+            ref = attend_in_64_bits(self.qo, kc, vc, ks, vs, bt, lens, self.new, bs)
+            assert ((self.out.double().cpu() - ref).abs() <= ATOL + RTOL * ref.abs()).all()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        prompt = Step(list(lens), True)
+        prompt.fill()
+        for cache in caches:
+            prompt.calls(cache)
+        prompt.check()
+        kinds = [Step([1] * B, False), Step([3, 1, 2], True)]
+        graphs = []
+        for k in kinds:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                k.calls(caches[0])
+            graphs.append(graph)
+        for i in range(8):
+            k = kinds[i % 2]
+            lens = [a + b for a, b in zip(lens, k.new)]
+            k.fill()
+            graphs[i % 2].replay()
+            got = [t.clone() for t in (k.out, k.qo)]
+            k.check()
+            k.calls(caches[1])
+            assert all(torch.equal(a, b) for a, b in zip(got, (k.out, k.qo)))
+            assert all(torch.equal(a, b) for a, b in zip(*caches))
+            if i % 2:  # drafts that were not right: their places are written again
+                lens = [a - rng.randint(0, b - 1) for a, b in zip(lens, k.new)]
+        assert pa.pa_read_device_status(ws) == pa.PA_OK
+
+
+@pytest.mark.gpu
+def test_two_streams_bit_by_bit():
+    """A workspace each: every call gives the bits that it gives alone."""
+    a = Attend(10, torch.bfloat16, 8, 2, 128, 16, [3000, 5, 700]).device()
+    b = Attend(11, torch.bfloat16, 16, 1, 128, 8, [44, 900], [7, 3]).device()
+    alone = [c.run().clone() for c in (a, b)]
+    outs = [torch.empty_like(x) for x in alone]
+    s2 = torch.cuda.Stream()
+    for _ in range(20):
+        for o in outs:
+            o.fill_(7.0)
+        s2.wait_stream(torch.cuda.current_stream())
+        b.run(stream=s2, out=outs[1])
+        a.run(out=outs[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, alone))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("decode", [False, True])
+def test_append_positions(decode):
+    """Positions of the caller's: the keys' and queries' angles, not their places."""
+    new = [1] * 4 if decode else [5, 0, 33, 2]
+    c = Append(26, torch.bfloat16, 8, 2, 128, 16, new, [3, 7, 15, 60], 128, decode=decode)
+    rows, top = sum(new), 500
+    ang = torch.arange(top, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, 128, 2) / 128)
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    pos = torch.randint(0, top, (rows,), generator=torch.Generator().manual_seed(27)).to(torch.int32)
+    d, H, K, D = "cuda", c.H, c.K, c.D
+    qkv = c.qkv.to(d)
+    q, k, v = (qkv[:, a * D:b * D].view(rows, -1, D) for a, b in ((0, H), (H, H + K), (H + K, H + 2 * K)))
+    c.dev = dict(codes=[x.to(d) for x in c.codes], scales=[x.to(d) for x in c.scales],
+                 qo=torch.empty(rows, H, D, dtype=c.dtype, device=d), ko=torch.empty(rows, K, D, dtype=c.dtype, device=d),
+                 vo=torch.empty(rows, K, D, dtype=c.dtype, device=d))
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    pa.pa_q4_append(*c.dev["codes"], *c.dev["scales"], k, v, c.bt.to(d), torch.tensor(c.lens, dtype=torch.int32, device=d), ws,
+                    query=q, query_out=c.dev["qo"], key_out=c.dev["ko"], value_out=c.dev["vo"], cos_sin=cs.to(d),
+                    positions=pos.to(d), q_start=None if decode else torch.tensor(c.qs, dtype=torch.int32, device=d))
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    x, at = c.qkv, cs[pos.long()]
+    key = rotate(x[:, H * D:(H + K) * D].view(rows, K, D).float(), at, 128, False).to(c.dtype)
+    assert torch.equal(c.dev["qo"].cpu(), rotate(x[:, :H * D].view(rows, H, D).float(), at, 128, False).to(c.dtype))
+    for i, want in enumerate((key, x[:, (H + K) * D:].view(rows, K, D))):
+        codes, scales, _ = quantise(want)
+        for r, (s, t) in enumerate(c.place):
+            p, o = int(c.bt[s, t // 16]), t % 16
+            assert torch.equal(c.dev["codes"][i][p, :, o].cpu(), codes[r])
+            assert torch.equal(c.dev["scales"][i][p, :, o].cpu(), scales[r])
