@@ -182,6 +182,7 @@ struct Q4Batch {
       r.y = __ldg(p.q_start + s);
       const int e = __ldg(p.q_start + s + 1);
       bad = bad || r.y < 0 || e < r.y || e > p.num_rows || e - r.y > r.x;
+      if (tell && s == 0 && r.y > 0) report(p.status, kStatusBadInput);  // rows that are nobody's
       r.z = e - r.y;
     }
     if (bad) {

@@ -935,3 +935,16 @@ def test_append_positions(decode):
             p, o = int(c.bt[s, t // 16]), t % 16
             assert torch.equal(c.dev["codes"][i][p, :, o].cpu(), codes[r])
             assert torch.equal(c.dev["scales"][i][p, :, o].cpu(), scales[r])
+
+
+@pytest.mark.gpu
+def test_first_start_is_zero():
+    """Rows before the first chunk are nobody's: reported, and left as they were."""
+    c = Attend(28, torch.bfloat16, 8, 2, 128, 16, [100, 40], [3, 2], pad=2).device()
+    ref = c.reference()
+    c.qs += 2
+    c.a[0].copy_(c.a[0].roll(2, 0))
+    out = c.run().double().cpu()
+    assert pa.pa_read_device_status(c.ws) == pa.PA_ERR_DEVICE_BAD_INPUT
+    assert (out[:2] == 7.0).all()
+    assert ((out[2:7] - ref[:5]).abs() <= ATOL + RTOL * ref[:5].abs()).all()
