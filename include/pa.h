@@ -556,7 +556,9 @@ size_t pa_prefix_workspace_bytes(int num_seqs, int num_prefixes, int num_heads,
  * (with the three operations of each element rounded apart), then coded; query
  * is rotated into query_out.  key_out, value_out [num_rows][num_kv_heads]
  * [head_size] (dtype), or NULL, receive what the appended codes stand for, for
- * attention among a prompt's own tokens that agrees with later decode steps.
+ * attention among a prompt's own tokens that agrees with later decode steps; they
+ * may be key and value themselves where those are contiguous (other strides in
+ * place are PA_ERR_INVALID_ARG).
  *
  * Rows, q_start, seq_lens, positions, strides, rotation, the workspace and bad
  * data as in pa_append_kv; padding rows leave query_out, key_out and value_out

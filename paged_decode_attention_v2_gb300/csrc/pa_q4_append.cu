@@ -251,6 +251,8 @@ extern "C" pa_status_t pa_q4_append(
   if (query && query == query_out && query_stride != (long long)num_heads * head_size)
     return PA_ERR_INVALID_ARG;
   if (workspace_bytes < (size_t)kStatusBytes) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (num_rows > 1 && ((key == key_out && key_stride != kv_row) || (value == value_out && value_stride != kv_row)))
+    return PA_ERR_INVALID_ARG;
 
   Q4AppendParams p{};
   p.key_codes = static_cast<uint8_t *>(key_cache);

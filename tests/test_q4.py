@@ -948,3 +948,27 @@ def test_first_start_is_zero():
     assert pa.pa_read_device_status(c.ws) == pa.PA_ERR_DEVICE_BAD_INPUT
     assert (out[:2] == 7.0).all()
     assert ((out[2:7] - ref[:5]).abs() <= ATOL + RTOL * ref[:5].abs()).all()
+
+
+@pytest.mark.parametrize("over", [dict(key_out=FAKE, value_out=0), dict(key_out=0, value_out=FAKE)])
+def test_append_refuses_strided_rows_in_place(lib, over):
+    """Rows written in place at another stride would be rows not yet read."""
+    assert lib.pa_q4_append(*dict(APPEND, **over).values()) == pa.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("il", [False, True])
+def test_append_gives_back_in_place(il):
+    c = Append(29, torch.float16, 8, 2, 128, 16, [300, 1, 9], [5, 0, 11], 128, il)
+    c.run()
+    d, (H, K, D) = c.dev, (c.H, c.K, c.D)
+    want = d["ko"].clone(), d["vo"].clone()
+    k, v = (c.qkv[:, a * D:b * D].reshape(-1, K, D).cuda() for a, b in ((H, H + K), (H + K, H + 2 * K)))
+    ws = pa.alloc_workspace(1, 1, 64, 0, 64)
+    before = [t.clone() for t in d["codes"] + d["scales"]]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pa.pa_q4_append(*d["codes"], *d["scales"], k, v, c.bt.cuda(), i32(c.lens), ws, key_out=k, value_out=v,
+                    cos_sin=c.cs.cuda(), q_start=i32(c.qs), interleaved=il)
+    assert pa.pa_read_device_status(ws) == pa.PA_OK
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    assert all(torch.equal(a, b) for a, b in zip(before, d["codes"] + d["scales"]))
