@@ -20,8 +20,8 @@
 // there for copies to run beside MMAs.
 //
 // Measured on GB300: one sequence of 100000 keys, 16 heads: 40 us (17 at the
-// bytes' rate; 10 of them the beginning and the join); 64 sequences of 1024 to
-// 8192 keys, 128 heads: 144 us, 2.5 TB/s and 580 TFLOP/s.  There a tile takes
+// bytes' rate; 13 of them the start, the epilogue and the join); 64 sequences of
+// 1024 to 8192 keys, 128 heads: 146 us, 2.5 TB/s and 580 TFLOP/s.  There a tile takes
 // 3700 cycles, 2550 of them MMAs: with two tiles in the ring its copy (2300
 // cycles; 1000 when an SM's own side of L2 has it), S, the softmax (900) and O^T
 // stand behind one another.  Slower were: tiles in parts that are copied, used

@@ -48,9 +48,14 @@
 //
 // Measured on GB300, bf16: 256 sequences of 512 to 3584 tokens, 32/4 heads, D 128:
 // 77 us (293 MB: 3.8 TB/s; 44 at the copy rate), one of 100,000 25 us (9), 64 of 16 to
-// 32,768, 16/2 heads, D 256, 41 us (16).  Half of the issue slots are used and hardly
-// a stall is memory's: it waits for its own steps, three warps a scheduler (two at
-// D 256) being what the registers hold.  Beginning and join are 10 us of each.
+// 32,768, 16/2 heads, D 256, 41 us (16).  Nothing is full: half of the issue slots are
+// used (a third at D 256), half of DRAM's rate, a fifth of the tensor pipe, and hardly
+// a stall is memory's.  Each warp copies, scores, exponentiates and sums one tile
+// behind another, and three warps a scheduler (two at D 256) are what the registers
+// hold.  Beginning and join are 10, 8 and 12 us of these.
+// A unit has 16 rows, so long chunks read and unmask the keys once for every 16 / group
+// tokens: 8 sequences of 8192 with 1, 5, 16, 64 and 256 tokens each take 40, 62, 126,
+// 388 and 1430 us (193 TFLOP/s), over 16-bit keys and values 44, 56, 66, 167 and 365.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <math_constants.h>

@@ -5,7 +5,8 @@
 // deep.  Bound: the launch and a chain of three loads (how many units, the unit,
 // its pieces); the bytes are a few MB that the attention kernel left in L2.  It
 // adds 4 us to 8 us; four pieces at once in a warp took no less, and 16 instead
-// of 64 as the most of few took 35 us instead of 32 in all for drafts.
+// of 64 as the most of few took 35 us instead of 32 in all for drafts.  Three CTAs
+// an SM leave a thread 80 registers: 40 to 64 bytes of spills are loaded again.
 #include "pa_share.cuh"
 
 #include "pa_host.h"

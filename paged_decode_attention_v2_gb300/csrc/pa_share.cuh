@@ -8,9 +8,10 @@
 // Every worker has a large share first, all equal; where pieces are cheap and
 // there is work enough, the rest of the line is cut into small ones that the
 // workers take from a counter as they get done, since SMs do not run alike (with
-// equal shares alone, CTAs of the same work ended between 50 and 76 us).  A share has at most two units that it does not hold
-// whole, its first and its last, so the space for partial results is two
-// places a share, whatever the batch.  Every CTA works the shares out of the
+// equal shares alone, CTAs of the same work ended between 50 and 76 us).  A share
+// has at most two units that it does not hold whole, its first and its last, so
+// the space for partial results is two places a share, whatever the batch.  Every
+// CTA works the shares out of the
 // lengths by itself: a scan over the sequences, which all CTAs do at once,
 // instead of a launch that would plan.
 //
@@ -28,7 +29,7 @@
 namespace pa {
 
 // A workspace, behind its status block: the units to join, then the places'
-// (maximum, sum) a row and their unnormalised outputs; 256-byte aligned each.
+// (reference, sum) a row and their unnormalised outputs; 256-byte aligned each.
 // Ints of the status block: shares taken, units to join of few and of many
 // pieces, join CTAs done.
 constexpr int kShareTaken = 16, kShareFew = 17, kShareMany = 18, kShareDone = 19;
@@ -45,8 +46,9 @@ struct alignas(16) ShareJoin {
 
 struct ShareSpace {
   ShareJoin *join;  // [shares]: units of few pieces from the front, of many from the back
-  float2 *ml;       // [shares][2][rows]: maximum (log2 units), sum of exp2(x - maximum)
-  float *o;         // [shares][2][rows][width]: sum of exp2(x - maximum) v
+  // m: what the weights are relative to, log2 units (any that keeps them in range)
+  float2 *ml;       // [shares][2][rows]: m, sum of exp2(x - m)
+  float *o;         // [shares][2][rows][width]: sum of exp2(x - m) v
   int *counters;    // the status block
   int shares;
 };
@@ -118,7 +120,8 @@ struct ShareSeq {
 };
 
 // The batch's side of the plan: Batch has num_seqs; read(s), a sequence's
-// (len, row0, n), checked, n < 0 if it is bad; seq(int4), the ShareSeq of it.
+// (len, row0, n), checked, no keys and no rows if it is bad; seq(int4), the ShareSeq
+// of it.
 template <int THREADS_, int CACHE_>
 struct ShareScan {
   static constexpr int THREADS = THREADS_, CACHE = CACHE_;  // CACHE: sequences kept in shared memory
