@@ -848,3 +848,23 @@ def test_first_start_is_zero():
     assert pa.pa_read_device_status(c.ws) == pa.PA_ERR_DEVICE_BAD_INPUT
     assert (out[:2] == 7.0).all()
     assert ((out[2:7] - ref[:5]).abs() <= ATOL + RTOL * ref[:5].abs()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("top", [1e4, 1e7, 1e8, 1e9])
+def test_weights_stay_in_range_however_far_the_scores(dtype, top):
+    """Scores near `top`, rising by a few units a key, where fp32's spacing is up to 64:
+    latents that are all 3 come back as 3, as no weight passes the type's largest."""
+    c = Attend(45, dtype, 16, 256, 16, [900, 77, 2000], scale=top / 2.0 ** 22)
+    c.q.zero_()
+    c.cache[..., :256] = 3.0
+    c.q[..., 256], c.q[..., 257] = 2.0 ** 11, min(12 / c.scale / 2000, 6e4)
+    for sign in (1.0, -1.0):
+        for s, n in enumerate(c.lens):
+            t = torch.arange(n)
+            c.cache[c.bt[s, t // 16].long(), t % 16, 256] = sign * 2.0 ** 11
+            c.cache[c.bt[s, t // 16].long(), t % 16, 257] = t.to(dtype)
+            c.cache[c.bt[s, t // 16].long(), t % 16, 258:] = 0.0
+        out = c.device().run().double()
+        assert ((out - 3.0).abs() <= 3 * (torch.finfo(dtype).eps / 2 + 2 ** -16)).all()

@@ -972,3 +972,29 @@ def test_append_gives_back_in_place(il):
     assert pa.pa_read_device_status(ws) == pa.PA_OK
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
     assert all(torch.equal(a, b) for a, b in zip(before, d["codes"] + d["scales"]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("top", [1e4, 1e7, 1e8, 1e9])
+def test_weights_stay_in_range_however_far_the_scores(dtype, top):
+    """Scores near `top`, rising by a few units a key, where fp32's spacing is up to 64: values
+    that are all 3 come back as 3, as no weight passes f16's largest."""
+    c = Attend(45, dtype, 4, 1, 64, 16, [900, 77, 2000])
+    c.scale = 1.0
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = 2.0 ** 12, 1.0
+    c.kc.zero_()
+    c.ks[..., 0], c.ks[..., 1] = 0.0, 0.0
+    c.vc.fill_(0x11)
+    c.vs[..., 0], c.vs[..., 1] = 2.0, 1.0
+    for sign in (1.0, -1.0):
+        c.scale = top / (2.0 ** 12 * 60000.0)
+        for s, L in enumerate(c.lens):
+            for t in range(L):
+                # (the group's lowest value lifts elements 0 and 1 alike)
+                c.ks[c.bt[s, t // 16].long(), :, t % 16, 0, 0] = sign * 60000.0
+                c.ks[c.bt[s, t // 16].long(), :, t % 16, 0, 1] = 32.0
+                c.kc[c.bt[s, t // 16].long(), :, t % 16, 0] = t * 16 // L
+        out = c.device().run().double()
+        assert ((out - 3.0).abs() <= 3 * (torch.finfo(dtype).eps / 2 + 2 ** -11)).all()
